@@ -1,4 +1,6 @@
-"""Exact top-k indexer selection (HyTopK) and selection replay on MI355X.
+"""Exact top-k indexer selection (HyTopK) and selection replay on MI355X, with
+the operators around it: rotary positions, the quantised cache, the attention's
+mass at the selected entries and the indexer's loss.
 
 A thin ctypes binding over ``libhytopk.so`` (``include/hytopk.h``): it only
 marshals torch tensors into pointers and sizes; every step of the selection
@@ -16,7 +18,9 @@ __all__ = [
     "baseline_select", "select_workspace_bytes", "baseline_workspace_bytes", "HytopkError",
     "EXPORTS", "BF16", "FP8_E4M3", "MXFP8_E4M3", "MXFP4_E2M1", "PATH_AUTO", "PATH_ROWS_ALL", "trace_enable", "trace_read",
     "backward", "backward_workspace_bytes", "select_noalloc", "NOALLOC_SCRATCH_BYTES",
-    "select_async", "ASYNC_STATUS_WORDS",
+    "select_async", "ASYNC_STATUS_WORDS", "Rotary", "rotary", "cache_write", "cache_read",
+    "cache_write_workspace_bytes", "quantize", "attention_mass", "attention_mass_workspace_bytes",
+    "index_loss",
 ]
 
 BF16, FP8_E4M3, MXFP8_E4M3, MXFP4_E2M1 = 0, 1, 2, 3
@@ -26,7 +30,9 @@ EXPORTS = (
     "hytopk_select_workspace", "hytopk_baseline_workspace", "hytopk_select", "hytopk_replay",
     "hytopk_baseline_select", "hytopk_backward_workspace", "hytopk_backward",
     "hytopk_status_string", "hytopk_last_error", "hytopk_trace_enable", "hytopk_trace_read",
-    "hytopk_select_noalloc", "hytopk_select_async",
+    "hytopk_select_noalloc", "hytopk_select_async", "hytopk_rotary_frequencies", "hytopk_rotary",
+    "hytopk_cache_write_workspace", "hytopk_cache_write", "hytopk_cache_read",
+    "hytopk_attention_mass_workspace", "hytopk_attention_mass", "hytopk_index_loss",
 )
 NOALLOC_SCRATCH_BYTES = 64 << 20  # HYTOPK_NOALLOC_SCRATCH_BYTES
 
@@ -58,6 +64,30 @@ class Stats(ctypes.Structure):
 class TraceEntry(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 32), ("launches", ctypes.c_int32),
                 ("total_ms", ctypes.c_double)]
+
+
+class RowsArray(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class RotaryPlan(ctypes.Structure):
+    _fields_ = [("freq", ctypes.c_void_p), ("gain", ctypes.c_double), ("dim", ctypes.c_int32),
+                ("first", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class Cache(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("L", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class Attention(ctypes.Structure):
+    _fields_ = [("L", ctypes.c_int64), ("n", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("key_heads", ctypes.c_int32), ("d", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("softmax_scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
 
 
 class HytopkError(RuntimeError):
@@ -113,6 +143,25 @@ def load_library():
     lib.hytopk_trace_enable.restype = ctypes.c_int
     lib.hytopk_trace_read.argtypes = [P(TraceEntry), ctypes.c_int]
     lib.hytopk_trace_read.restype = ctypes.c_int
+    i32, i64, dbl = ctypes.c_int32, ctypes.c_int64, ctypes.c_double
+    lib.hytopk_rotary_frequencies.argtypes = [i32, dbl, i32, dbl, i64, vp, P(dbl)]
+    lib.hytopk_rotary_frequencies.restype = ctypes.c_int
+    lib.hytopk_rotary.argtypes = [P(RotaryPlan), i64, i32, i32, P(RowsArray), P(RowsArray), vp, i64,
+                                  i32, vp]
+    lib.hytopk_rotary.restype = ctypes.c_int
+    lib.hytopk_cache_write_workspace.argtypes = [P(Cache), i64, i32]
+    lib.hytopk_cache_write_workspace.restype = sz
+    lib.hytopk_cache_write.argtypes = [P(Cache), i64, P(RowsArray), vp, i64, P(RotaryPlan), vp, i64,
+                                       vp, sz, vp]
+    lib.hytopk_cache_write.restype = ctypes.c_int
+    lib.hytopk_cache_read.argtypes = [P(Cache), i64, vp, i64, vp, i32, vp]
+    lib.hytopk_cache_read.restype = ctypes.c_int
+    lib.hytopk_attention_mass_workspace.argtypes = [P(Attention)]
+    lib.hytopk_attention_mass_workspace.restype = sz
+    lib.hytopk_attention_mass.argtypes = [P(Attention), vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.hytopk_attention_mass.restype = ctypes.c_int
+    lib.hytopk_index_loss.argtypes = [i64, i32, vp, vp, vp, vp, vp, vp]
+    lib.hytopk_index_loss.restype = ctypes.c_int
     _LIB = lib
     return lib
 
@@ -429,3 +478,304 @@ def backward(q, k, w, idx, d_score, *, q_scale=None, k_scale=None, q_start=None,
                                _ptr(res.get("dw")), _ptr(res.get("dk")), _ptr(workspace),
                                0 if workspace is None else workspace.numel(), _stream(q)))
     return res
+
+
+# ----------------------------------------- rotary positions and the cache
+
+_LAYOUTS = {"half": 0, "interleaved": 1}
+_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def _on(t):
+    """Makes the tensor's GPU the current one for a launch."""
+    import contextlib
+
+    import torch
+    dev = t.device
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def _gpu(t, name: str) -> None:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
+
+
+def _rows_array(t, name: str):
+    """[n][d] or [n][heads][d] rows of bf16 or fp32, any strides but the last."""
+    import torch
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name} must be [n][d] or [n][heads][d], got {tuple(t.shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last axis of {name} must be contiguous")
+    return RowsArray(t.data_ptr(), t.stride(0), t.stride(1) if t.dim() == 3 else 0,
+                     0 if t.dtype == torch.bfloat16 else 1, 0)
+
+
+def _ints(t, name: str, n: int, device) -> None:
+    import torch
+    if t is not None:
+        _need(t, name, (n,), torch.int32, device)
+
+
+class Rotary:
+    """A rotation of elements ``first .. first + dim - 1`` of every head: the
+    frequencies (``freq``, float64 on the GPU) and the factor on the rotated
+    part (``gain``), made once and kept for every call.  ``layout`` pairs
+    elements (i, i + dim/2) ("half") or (2i, 2i + 1) ("interleaved");
+    ``scaling`` ("none", "linear", "ntk", "yarn") stretches the positions by
+    ``factor`` for a model whose positions reached ``original`` before."""
+
+    def __init__(self, dim: int, *, first: int = 0, layout: str = "half", base: float = 10000.0,
+                 scaling: str = "none", factor: float = 1.0, original: int = 0, device="cuda"):
+        import torch
+        if layout not in _LAYOUTS:
+            raise ValueError(f"unknown rotary layout {layout!r}")
+        if scaling not in _SCALINGS:
+            raise ValueError(f"unknown rotary scaling {scaling!r}")
+        lib = load_library()
+        freq = torch.empty(max(int(dim) // 2, 1), dtype=torch.float64)
+        gain = ctypes.c_double()
+        _check(lib.hytopk_rotary_frequencies(int(dim), float(base), _SCALINGS[scaling],
+                                             float(factor), int(original), _ptr(freq),
+                                             ctypes.byref(gain)))
+        if int(first) < 0:
+            raise ValueError("first must be >= 0")
+        self.freq = freq.to(device)
+        self.gain, self.dim, self.first, self.layout = gain.value, int(dim), int(first), layout
+        self._plan = RotaryPlan(self.freq.data_ptr(), self.gain, self.dim, self.first,
+                                _LAYOUTS[layout], 0)
+
+
+def _plan(rot, device):
+    if rot is None:
+        return None
+    if rot.freq.device != device:
+        raise ValueError(f"the rotary plan is on {rot.freq.device}, the rows on {device}")
+    return ctypes.byref(rot._plan)
+
+
+def rotary(x, rot: Rotary, *, q_start: int = 0, q_pos=None, backward: bool = False, out=None,
+           out_dtype=None):
+    """Rotary positions of rows x [n][d] or [n][heads][d] (bf16 or fp32, any
+    strides but the last).  Token i sits at ``q_pos[i]`` (int32 [n] on the GPU) or
+    ``q_start + i``.  ``backward`` applies the transposed rotation, which
+    takes a gradient of the result to one of x.  ``out`` may be x itself."""
+    import torch
+    lib = _LIB or load_library()
+    _gpu(x, "x")
+    xa = _rows_array(x, "x")
+    n, d = x.shape[0], x.shape[-1]
+    heads = x.shape[1] if x.dim() == 3 else 1
+    if out is None:
+        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+    elif out.shape != x.shape or out.device != x.device or out_dtype not in (None, out.dtype):
+        raise ValueError(f"out must have x's shape {tuple(x.shape)} and device, and out_dtype")
+    ya = _rows_array(out, "out")
+    _ints(q_pos, "q_pos", n, x.device)
+    with _on(x):
+        _check(lib.hytopk_rotary(_plan(rot, x.device), n, heads, d, ctypes.byref(xa),
+                                 ctypes.byref(ya), _ptr(q_pos), int(q_start), 1 if backward else 0,
+                                 _stream(x)))
+    return out
+
+
+def _cache(codes, scale, fmt):
+    """codes [L][d] or [L][heads][d] (MXFP4: the last axis holds d/2 bytes) and
+    scales as ``select`` takes them."""
+    import torch
+    _gpu(codes, "codes")
+    code = _dtype_code(codes, fmt)
+    if codes.dim() not in (2, 3):
+        raise ValueError(f"codes must be [L][d] or [L][heads][d], got {tuple(codes.shape)}")
+    if not codes.is_contiguous():
+        raise ValueError("codes must be contiguous")
+    want = {BF16: (torch.bfloat16,), FP8_E4M3: (torch.uint8, torch.float8_e4m3fn)}.get(
+        code, (torch.uint8,))
+    if codes.dtype not in want:
+        raise ValueError(f"codes of this format must be {want[0]}, got {codes.dtype}")
+    L, last = codes.shape[0], codes.shape[-1]
+    heads = codes.shape[1] if codes.dim() == 3 else 1
+    d = 2 * last if code == MXFP4_E2M1 else last
+    if code == BF16:
+        if scale is not None:
+            raise ValueError("a bf16 cache takes no scale")
+    elif scale is None:
+        raise ValueError("fp8 and MX caches need scale")
+    elif code == FP8_E4M3:
+        _need(scale, "scale", (L,), torch.float32, codes.device)
+    else:
+        _need(scale, "scale", tuple(codes.shape[:-1]) + (d // 32,), torch.uint8, codes.device)
+    return Cache(codes.data_ptr(), None if scale is None else scale.data_ptr(), L, heads, d, code, 0)
+
+
+def cache_write_workspace_bytes(codes, scale, n: int, *, fmt=None) -> int:
+    """Workspace bytes of a cache_write of n rows by slot (0: none)."""
+    return int(load_library().hytopk_cache_write_workspace(
+        ctypes.byref(_cache(codes, scale, fmt)), n, 1))
+
+
+def cache_write(x, codes, scale=None, *, fmt=None, start: int = 0, slots=None, rotary=None,
+                q_start: int = 0, q_pos=None, workspace=None) -> None:
+    """Quantise rows x ([n][d] or [n][heads][d], bf16 or fp32, any strides but the
+    last) into cache rows ``slots[i]`` (int32 [n] on the GPU; rows outside the
+    cache are padding and skipped; the last of several rows of one slot is
+    kept) or ``start + i``.  ``codes`` and ``scale`` are laid out as ``select`` takes them
+    (``fmt`` as there).  ``rotary`` (a Rotary) rotates the rows first, at positions
+    ``q_pos`` / ``q_start + i``."""
+    import torch
+    lib = _LIB or load_library()
+    c = _cache(codes, scale, fmt)
+    xa = _rows_array(x, "x")
+    n = x.shape[0]
+    if x.device != codes.device:
+        raise ValueError(f"x is on {x.device}, the cache on {codes.device}")
+    if x.shape[-1] != c.d or (x.shape[1] if x.dim() == 3 else 1) != c.heads:
+        raise ValueError(f"x {tuple(x.shape)} does not fit cache rows of {c.heads} x {c.d}")
+    _ints(slots, "slots", n, x.device)
+    _ints(q_pos, "q_pos", n, x.device)
+    with _on(x):
+        if workspace is None and slots is not None:
+            need = int(lib.hytopk_cache_write_workspace(ctypes.byref(c), n, 1))
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        if workspace is not None:
+            _workspace(workspace, x.device)
+        _check(lib.hytopk_cache_write(ctypes.byref(c), n, ctypes.byref(xa), _ptr(slots), int(start),
+                                      _plan(rotary, x.device), _ptr(q_pos), int(q_start),
+                                      _ptr(workspace),
+                                      0 if workspace is None else workspace.numel(), _stream(x)))
+
+
+def quantize(x, fmt: str, *, rotary=None, q_start: int = 0, q_pos=None):
+    """Rows x ([n][d] or [n][heads][d]) in a storage format of ``select``: new
+    (codes, scale), scale None for "bf16".  ``rotary`` as in ``cache_write``."""
+    import torch
+    if fmt not in _FMT:
+        raise ValueError(f"unknown format {fmt!r}")
+    _gpu(x, "x")
+    code, shape, d = _FMT[fmt], tuple(x.shape), x.shape[-1]
+    if code != BF16 and d % 32:
+        raise ValueError("quantised rows need d in multiples of 32")
+    codes = torch.empty(shape[:-1] + (d // 2 if code == MXFP4_E2M1 else d,), device=x.device,
+                        dtype=torch.bfloat16 if code == BF16 else torch.uint8)
+    scale = None
+    if code == FP8_E4M3:
+        scale = torch.empty(shape[0], dtype=torch.float32, device=x.device)
+    elif code != BF16:
+        scale = torch.empty(shape[:-1] + (d // 32,), dtype=torch.uint8, device=x.device)
+    if shape[0]:
+        cache_write(x, codes, scale, fmt=fmt, rotary=rotary, q_start=q_start, q_pos=q_pos)
+    return codes, scale
+
+
+def cache_read(codes, scale=None, *, fmt=None, slots=None, start: int = 0, count=None,
+               dtype=None, out=None):
+    """Cache rows decoded: rows ``slots`` (int32 [n] on the GPU; rows outside the cache read as
+    zeros) or ``start .. start + count - 1`` (to the end by default), as [n][d]
+    or [n][heads][d] of ``dtype`` (bf16 by default, or fp32)."""
+    import torch
+    lib = _LIB or load_library()
+    c = _cache(codes, scale, fmt)
+    n = slots.shape[0] if slots is not None else (c.L - int(start) if count is None else int(count))
+    if count is not None and n != count:
+        raise ValueError(f"count {count} differs from the {n} slots")
+    _ints(slots, "slots", n, codes.device)
+    shape = (n, c.d) if codes.dim() == 2 else (n, c.heads, c.d)
+    if out is None:
+        if n < 0:
+            raise ValueError("start lies behind the cache")
+        out = torch.empty(shape, dtype=dtype or torch.bfloat16, device=codes.device)
+    _need(out, "out", shape, dtype or out.dtype, codes.device)
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"rows are read as bfloat16 or float32, got {out.dtype}")
+    with _on(codes):
+        _check(lib.hytopk_cache_read(ctypes.byref(c), n, _ptr(slots), int(start), _ptr(out),
+                                     0 if out.dtype == torch.bfloat16 else 1, _stream(codes)))
+    return out
+
+
+# ------------------------------------------- the indexer's target and loss
+
+def _attention(q, k, idx, softmax_scale) -> Attention:
+    """q [n][heads][d], k [L][key_heads][d] or [L][d], idx [n][k]."""
+    import torch
+    if q.dim() != 3 or k.dim() not in (2, 3) or k.shape[-1] != q.shape[-1]:
+        raise ValueError("shapes must be q [n][heads][d], k [L][key_heads][d] or [L][d]")
+    for t, name in ((q, "q"), (k, "k")):
+        if t.dtype != torch.bfloat16 or not t.is_cuda or not t.is_contiguous() or t.device != q.device:
+            raise ValueError(f"{name} must be contiguous bfloat16 on one GPU")
+    n, heads, d = q.shape
+    if idx.dim() != 2:
+        raise ValueError("idx must be [n][k]")
+    _need(idx, "idx", (n, idx.shape[1]), torch.int32, q.device)
+    scale = d ** -0.5 if softmax_scale is None else float(softmax_scale)
+    return Attention(k.shape[0], n, heads, k.shape[1] if k.dim() == 3 else 1, d, idx.shape[1], scale, 0)
+
+
+def attention_mass_workspace_bytes(q, k, idx) -> int:
+    """Workspace bytes of attention_mass without lse."""
+    return int(load_library().hytopk_attention_mass_workspace(
+        ctypes.byref(_attention(q, k, idx, None))))
+
+
+def attention_mass(q, k, idx, *, softmax_scale=None, lse=None, workspace=None, out=None):
+    """The attention's probability at the selected entries idx [n][k], averaged
+    over heads (fp32 [n][k]; 0 at padding): the target of ``index_loss``.
+    q [n][heads][d] and k [L][key_heads][d] (or [L][d]) are the attention's, bf16;
+    ``softmax_scale`` is d ** -0.5 by default; ``lse`` (fp32 [n][heads]) is the attention's
+    log-sum-exp, by default taken over the row's entries."""
+    import torch
+    lib = _LIB or load_library()
+    p = _attention(q, k, idx, softmax_scale)
+    if lse is not None:
+        _need(lse, "lse", (p.n, p.heads), torch.float32, q.device)
+    if out is None:
+        out = torch.empty((p.n, p.k), dtype=torch.float32, device=q.device)
+    _need(out, "out", (p.n, p.k), torch.float32, q.device)
+    with _on(q):
+        if workspace is None and lse is None:
+            need = int(lib.hytopk_attention_mass_workspace(ctypes.byref(p)))
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        if workspace is not None:
+            _workspace(workspace, q.device)
+        _check(lib.hytopk_attention_mass(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(idx), _ptr(lse),
+                                         _ptr(out), _ptr(workspace),
+                                         0 if workspace is None else workspace.numel(), _stream(q)))
+    return out
+
+
+def index_loss(score, mass, *, weight=None, want=("loss", "d_score"), out=None):
+    """The indexer's loss per query and its gradient: the divergence of
+    softmax(score) from mass / sum(mass) over the entries whose score is not -inf,
+    times ``weight`` (fp32 [n], 1 by default).  score (``replay``'s) and mass
+    (``attention_mass``'s) are fp32 [n][k].  Returns (loss [n], d_score [n][k]),
+    None for one that ``want`` leaves out; ``backward`` takes d_score.  ``out`` gives
+    the two tensors instead (either may be None; d_score may be score or mass)."""
+    import torch
+    lib = _LIB or load_library()
+    _gpu(score, "score")
+    if score.dim() != 2:
+        raise ValueError("score must be [n][k]")
+    n, k = score.shape
+    dev = score.device
+    _need(score, "score", (n, k), torch.float32, dev)
+    _need(mass, "mass", (n, k), torch.float32, dev)
+    if weight is not None:
+        _need(weight, "weight", (n,), torch.float32, dev)
+    if out is None:
+        loss = torch.empty(n, dtype=torch.float32, device=dev) if "loss" in want else None
+        grad = torch.empty((n, k), dtype=torch.float32, device=dev) if "d_score" in want else None
+    else:
+        loss, grad = out
+        if loss is not None:
+            _need(loss, "out[0] (loss)", (n,), torch.float32, dev)
+        if grad is not None:
+            _need(grad, "out[1] (d_score)", (n, k), torch.float32, dev)
+    with _on(score):
+        _check(lib.hytopk_index_loss(n, k, _ptr(score), _ptr(mass), _ptr(weight), _ptr(loss),
+                                     _ptr(grad), _stream(score)))
+    return loss, grad

@@ -19,7 +19,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libhytopk.so")
-SOURCES = ["api.hip", "score.hip", "gather.hip", "radix.hip", "backward.hip"]
+SOURCES = ["api.hip", "score.hip", "gather.hip", "radix.hip", "backward.hip", "rows.hip", "loss.hip"]
+# These keep NaN semantics: padding may hold anything, and what is not finite in a
+# live entry has to show in the result.
+NAN_SOURCES = ("rows.hip", "loss.hip")
 ARCH = os.environ.get("HYTOPK_ARCH", "gfx950")
 
 FLAGS = [
@@ -59,7 +62,8 @@ def build(verbose: bool = True) -> str:
     for src in SOURCES:
         obj = os.path.join(BUILD, src.replace(".hip", ".o"))
         objs.append(obj)
-        jobs.append([cc, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj])
+        extra = ["-fhonor-nans"] if src in NAN_SOURCES else []
+        jobs.append([cc, *FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj])
     workers = min(len(jobs), max(1, min(16, os.cpu_count() or 1)))
     with cf.ThreadPoolExecutor(workers) as ex:
         list(ex.map(_run, jobs))

@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -741,6 +742,377 @@ int hytopk_backward(const hytopk_problem* p, const void* q, const void* q_scale,
     }
   }
   return HYTOPK_OK;
+}
+
+}  // extern "C"
+
+// ------------------------------------- rotary, cache, attention mass, loss
+
+namespace {
+
+// Runs an entry point's body; what it throws (host memory running out) comes
+// back as a status.
+template <typename F>
+int guarded(F body) noexcept {
+  try {
+    g_err.clear();
+    return body();
+  } catch (...) {
+    return HYTOPK_EHIP;
+  }
+}
+
+constexpr int64_t kMaxRows = int64_t(1) << 31;
+constexpr int kMaxRotary = 1024;
+constexpr int kMaxRowElems = 8192;
+
+bool misaligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+
+int rows_elem(const hytopk_rows* r) { return r->dtype == HYTOPK_ROWS_BF16 ? 2 : 4; }
+
+int check_rows(const hytopk_rows* r, int64_t n, int32_t heads, int32_t d) {
+  if (!r) return fail(HYTOPK_EINVAL, "rows are NULL");
+  if (r->dtype != HYTOPK_ROWS_BF16 && r->dtype != HYTOPK_ROWS_FP32)
+    return fail(HYTOPK_EINVAL, "unknown rows dtype");
+  if (r->token_stride < 0 || r->head_stride < 0) return fail(HYTOPK_EINVAL, "strides must be >= 0");
+  if (n == 0) return HYTOPK_OK;
+  if (!r->data) return fail(HYTOPK_EINVAL, "rows data is NULL");
+  if (misaligned(r->data, (uintptr_t)rows_elem(r)))
+    return fail(HYTOPK_EINVAL, "rows must be aligned to their element");
+  const __int128 span = (__int128)(n - 1) * r->token_stride + (__int128)(heads - 1) * r->head_stride + d;
+  if (span > ((__int128)1 << 60)) return fail(HYTOPK_EINVAL, "rows span more memory than exists");
+  return HYTOPK_OK;
+}
+
+int check_tokens(int64_t n, int32_t heads, int32_t d) {
+  if (n < 0 || heads <= 0 || d <= 0) return fail(HYTOPK_EINVAL, "n must be >= 0 and heads, d > 0");
+  if (n >= kMaxRows) return fail(HYTOPK_EUNSUPPORTED, "n >= 2^31");
+  if ((int64_t)heads * d >= kMaxRows) return fail(HYTOPK_EUNSUPPORTED, "heads * d >= 2^31");
+  return HYTOPK_OK;
+}
+
+// Whether no two rows share an element: one axis' rows lie apart and the other axis steps over
+// all of them.
+bool rows_apart(const hytopk_rows* r, int64_t n, int32_t heads, int32_t d) {
+  const __int128 t = r->token_stride, h = r->head_stride;
+  if (heads == 1) return n == 1 || t >= d;
+  if (n == 1) return h >= d;
+  return (h >= d && t >= (heads - 1) * h + d) || (t >= d && h >= (n - 1) * t + d);
+}
+
+struct Extent {
+  uintptr_t lo, hi;
+};
+
+Extent extent(const hytopk_rows* r, int64_t n, int32_t heads, int32_t d) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(r->data);
+  const int64_t span = (n - 1) * r->token_stride + (heads - 1) * r->head_stride + d;
+  return Extent{lo, lo + (uintptr_t)(span * rows_elem(r))};
+}
+
+Extent extent(const void* p, int64_t bytes) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  return Extent{lo, lo + (uintptr_t)bytes};
+}
+
+bool overlap(Extent a, Extent b) { return a.lo < b.hi && b.lo < a.hi; }
+
+int check_plan(const hytopk_rotary_plan* p, int32_t d) {
+  if (!p) return fail(HYTOPK_EINVAL, "rotary plan is NULL");
+  if (p->dim <= 0 || p->dim % 2) return fail(HYTOPK_EINVAL, "the rotary dim must be even and > 0");
+  if (p->first < 0 || (int64_t)p->first + p->dim > d)
+    return fail(HYTOPK_EINVAL, "the rotated part lies outside the head");
+  if (p->dim > kMaxRotary) return fail(HYTOPK_EUNSUPPORTED, "rotary dim > 1024");
+  if (p->layout != HYTOPK_ROTARY_HALF && p->layout != HYTOPK_ROTARY_INTERLEAVED)
+    return fail(HYTOPK_EINVAL, "unknown rotary layout");
+  if (!p->freq) return fail(HYTOPK_EINVAL, "rotary freq is NULL");
+  if (misaligned(p->freq, 8)) return fail(HYTOPK_EINVAL, "rotary freq must be 8-byte aligned");
+  if (!std::isfinite(p->gain)) return fail(HYTOPK_EINVAL, "the rotary gain must be finite");
+  return HYTOPK_OK;
+}
+
+int check_positions(int64_t n, const int32_t* q_pos, int64_t q_start) {
+  if (q_pos) {
+    if (misaligned(q_pos, 4)) return fail(HYTOPK_EINVAL, "q_pos must be 4-byte aligned");
+  } else if (q_start < 0 || q_start > kMaxRows - n) {
+    return fail(HYTOPK_EINVAL, "positions q_start .. q_start + n - 1 must lie in [0, 2^31)");
+  }
+  return HYTOPK_OK;
+}
+
+hk::RotArgs rot_args(const hytopk_rotary_plan* p, const int32_t* q_pos, int64_t q_start, bool backward) {
+  hk::RotArgs r{};
+  if (!p) return r;
+  r.freq = p->freq;
+  r.pos = q_pos;
+  r.pos0 = q_start;
+  r.gain = (float)p->gain;
+  r.sign = backward ? -1.0f : 1.0f;
+  r.dim = p->dim;
+  r.first = p->first;
+  r.layout = p->layout;
+  return r;
+}
+
+int64_t cache_code_bytes(const hytopk_cache* c) {
+  const int64_t e = c->L * c->heads * c->d;
+  return c->dtype == HYTOPK_BF16 ? 2 * e : (c->dtype == HYTOPK_MXFP4_E2M1 ? e / 2 : e);
+}
+
+// The geometry alone (what the workspace query knows).
+int check_cache_shape(const hytopk_cache* c) {
+  if (!c) return fail(HYTOPK_EINVAL, "cache is NULL");
+  if (c->L <= 0 || c->heads <= 0 || c->d <= 0) return fail(HYTOPK_EINVAL, "L, heads and d must be > 0");
+  if (c->dtype < HYTOPK_BF16 || c->dtype > HYTOPK_MXFP4_E2M1) return fail(HYTOPK_EINVAL, "unknown dtype");
+  if (c->L >= kMaxRows) return fail(HYTOPK_EUNSUPPORTED, "L >= 2^31");
+  if (c->d % 32) return fail(HYTOPK_EUNSUPPORTED, "cache rows need d in multiples of 32");
+  if ((int64_t)c->heads * c->d > kMaxRowElems) return fail(HYTOPK_EUNSUPPORTED, "heads * d > 8192");
+  return HYTOPK_OK;
+}
+
+int check_cache(const hytopk_cache* c, int64_t n, const int32_t* slots, int64_t start) {
+  int rc = check_cache_shape(c);
+  if (rc) return rc;
+  if (n < 0) return fail(HYTOPK_EINVAL, "n must be >= 0");
+  if (n >= kMaxRows) return fail(HYTOPK_EUNSUPPORTED, "n >= 2^31");
+  if (!c->codes) return fail(HYTOPK_EINVAL, "cache codes are NULL");
+  if (misaligned(c->codes, 16)) return fail(HYTOPK_EINVAL, "cache codes must be 16-byte aligned");
+  if (c->dtype != HYTOPK_BF16) {
+    if (!c->scale) return fail(HYTOPK_EINVAL, "fp8 and MX caches need scales");
+    if (misaligned(c->scale, 4)) return fail(HYTOPK_EINVAL, "cache scales must be 4-byte aligned");
+  }
+  if (slots) {
+    if (misaligned(slots, 4)) return fail(HYTOPK_EINVAL, "slots must be 4-byte aligned");
+  } else if (start < 0 || start > c->L - n) {
+    return fail(HYTOPK_EINVAL, "rows start .. start + n - 1 lie outside the cache");
+  }
+  return HYTOPK_OK;
+}
+
+bool wants_claim(int64_t n, bool by_slot) { return by_slot && n > hk::kClaimRows; }
+
+int check_attention(const hytopk_attention* p) {
+  if (!p) return fail(HYTOPK_EINVAL, "attention is NULL");
+  if (p->L <= 0 || p->n < 0) return fail(HYTOPK_EINVAL, "L must be > 0 and n >= 0");
+  if (p->heads <= 0 || p->key_heads <= 0 || p->heads % p->key_heads)
+    return fail(HYTOPK_EINVAL, "key_heads must divide heads");
+  if (p->k <= 0) return fail(HYTOPK_EINVAL, "k must be > 0");
+  if (!std::isfinite(p->softmax_scale)) return fail(HYTOPK_EINVAL, "softmax_scale must be finite");
+  if (p->k > kMaxK) return fail(HYTOPK_EUNSUPPORTED, "k > 2048");
+  if (p->L >= kMaxRows) return fail(HYTOPK_EUNSUPPORTED, "L >= 2^31");
+  if (p->n >= int64_t(1) << 24) return fail(HYTOPK_EUNSUPPORTED, "n >= 2^24");
+  if (!hk::mass_supports(p->d)) return fail(HYTOPK_EUNSUPPORTED, "d must be 64, 96, 128, 192, 256, 512 or 576");
+  if (p->heads > 1024) return fail(HYTOPK_EUNSUPPORTED, "heads > 1024");
+  return HYTOPK_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int hytopk_rotary_frequencies(int32_t dim, double base, int32_t scaling, double factor,
+                              int64_t original, double* freq, double* gain) {
+  return guarded([&]() -> int {
+    if (!freq || !gain) return fail(HYTOPK_EINVAL, "freq and gain must be non-NULL");
+    if (dim <= 0 || dim % 2) return fail(HYTOPK_EINVAL, "the rotary dim must be even and > 0");
+    if (dim > kMaxRotary) return fail(HYTOPK_EUNSUPPORTED, "rotary dim > 1024");
+    if (!(base > 1.0) || !std::isfinite(base)) return fail(HYTOPK_EINVAL, "base must be finite and > 1");
+    if (scaling < HYTOPK_SCALING_NONE || scaling > HYTOPK_SCALING_YARN)
+      return fail(HYTOPK_EINVAL, "unknown rotary scaling");
+    if (scaling != HYTOPK_SCALING_NONE && (!(factor >= 1.0) || !std::isfinite(factor)))
+      return fail(HYTOPK_EINVAL, "factor must be finite and >= 1");
+    if (scaling == HYTOPK_SCALING_YARN && original <= 0)
+      return fail(HYTOPK_EINVAL, "yarn needs the original context length");
+    double b = base;
+    // base^(-(dim - 2)/dim) divided by factor is the slowest frequency of the raised base
+    if (scaling == HYTOPK_SCALING_NTK) b *= std::pow(factor, (double)dim / std::max(dim - 2, 1));
+    double lo = 0.0, width = 1.0;
+    if (scaling == HYTOPK_SCALING_YARN) {
+      // the pair that makes r turns in the original context
+      auto pair = [&](double r) {
+        return dim * std::log((double)original / (r * 2.0 * M_PI)) / (2.0 * std::log(base));
+      };
+      lo = std::max(std::floor(pair(32.0)), 0.0);
+      const double hi = std::min(std::ceil(pair(1.0)), (double)(dim - 1));
+      width = std::max(hi - lo, 1e-3);
+    }
+    for (int i = 0; i < dim / 2; ++i) {
+      const double f = std::pow(b, -2.0 * i / dim);
+      if (scaling == HYTOPK_SCALING_LINEAR) {
+        freq[i] = f / factor;
+      } else if (scaling == HYTOPK_SCALING_YARN) {
+        const double r = std::min(std::max((i - lo) / width, 0.0), 1.0);
+        freq[i] = f * (1.0 - r) + f / factor * r;
+      } else {
+        freq[i] = f;
+      }
+    }
+    *gain = scaling == HYTOPK_SCALING_YARN ? 0.1 * std::log(factor) + 1.0 : 1.0;
+    return HYTOPK_OK;
+  });
+}
+
+int hytopk_rotary(const hytopk_rotary_plan* plan, int64_t n, int32_t heads, int32_t d,
+                  const hytopk_rows* x, const hytopk_rows* y, const int32_t* q_pos,
+                  int64_t q_start, int32_t backward, void* stream) {
+  return guarded([&]() -> int {
+    int rc = check_tokens(n, heads, d);
+    if (rc) return rc;
+    if ((rc = check_plan(plan, d))) return rc;
+    if ((rc = check_rows(x, n, heads, d)) || (rc = check_rows(y, n, heads, d))) return rc;
+    if ((rc = check_positions(n, q_pos, q_start))) return rc;
+    if (n == 0) return HYTOPK_OK;
+    if (!rows_apart(y, n, heads, d)) return fail(HYTOPK_EINVAL, "rows of y overlap each other");
+    const bool same = x->data == y->data && x->dtype == y->dtype &&
+                      (n == 1 || x->token_stride == y->token_stride) &&
+                      (heads == 1 || x->head_stride == y->head_stride);
+    if (!same && overlap(extent(x, n, heads, d), extent(y, n, heads, d)))
+      return fail(HYTOPK_EINVAL, "x and y overlap (y may be x itself)");
+    hk::RotaryArgs a{};
+    a.x = x->data;
+    a.y = y->data;
+    a.xts = x->token_stride; a.xhs = x->head_stride;
+    a.yts = y->token_stride; a.yhs = y->head_stride;
+    a.n = (int)n;
+    a.heads = heads;
+    a.d = d;
+    a.rot = rot_args(plan, q_pos, q_start, backward != 0);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    Span sp("rotary", s);
+    HK_HIP(hk::launch_rotary(a, x->dtype, y->dtype, s), "rotary launch");
+    return HYTOPK_OK;
+  });
+}
+
+size_t hytopk_cache_write_workspace(const hytopk_cache* c, int64_t n, int32_t by_slot) {
+  if (check_cache_shape(c) != HYTOPK_OK || !wants_claim(n, by_slot != 0)) return 0;
+  return align_up((size_t)c->L * sizeof(int32_t));
+}
+
+int hytopk_cache_write(const hytopk_cache* c, int64_t n, const hytopk_rows* x,
+                       const int32_t* slots, int64_t start, const hytopk_rotary_plan* plan,
+                       const int32_t* q_pos, int64_t q_start, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  return guarded([&]() -> int {
+    int rc = check_cache(c, n, slots, start);
+    if (rc) return rc;
+    if ((rc = check_rows(x, n, c->heads, c->d))) return rc;
+    if (plan && ((rc = check_plan(plan, c->d)) || (rc = check_positions(n, q_pos, q_start)))) return rc;
+    if (n == 0) return HYTOPK_OK;
+    if (overlap(extent(x, n, c->heads, c->d), extent(c->codes, cache_code_bytes(c))))
+      return fail(HYTOPK_EINVAL, "x overlaps the cache");
+    const bool claim = wants_claim(n, slots != nullptr);
+    if (claim && (rc = check_ws(workspace, workspace_bytes, hytopk_cache_write_workspace(c, n, 1)))) return rc;
+    hk::CacheWriteArgs a{};
+    a.x = x->data;
+    a.ts = x->token_stride;
+    a.hs = x->head_stride;
+    a.n = (int)n;
+    a.heads = c->heads;
+    a.d = c->d;
+    a.rot = rot_args(plan, q_pos, q_start, false);
+    a.codes = static_cast<uint8_t*>(c->codes);
+    a.scale = c->scale;
+    a.L = (int)c->L;
+    a.slots = slots;
+    a.start = start;
+    a.claim = claim ? static_cast<int*>(workspace) : nullptr;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    Span sp("cache_write", s);
+    HK_HIP(hk::launch_cache_write(a, x->dtype, c->dtype, s), "cache write launch");
+    return HYTOPK_OK;
+  });
+}
+
+int hytopk_cache_read(const hytopk_cache* c, int64_t n, const int32_t* slots, int64_t start,
+                      void* out, int32_t out_dtype, void* stream) {
+  return guarded([&]() -> int {
+    int rc = check_cache(c, n, slots, start);
+    if (rc) return rc;
+    if (out_dtype != HYTOPK_ROWS_BF16 && out_dtype != HYTOPK_ROWS_FP32)
+      return fail(HYTOPK_EINVAL, "unknown rows dtype");
+    if (n == 0) return HYTOPK_OK;
+    if (!out) return fail(HYTOPK_EINVAL, "out is NULL");
+    if (misaligned(out, 16)) return fail(HYTOPK_EINVAL, "out must be 16-byte aligned");
+    const int64_t bytes = n * c->heads * c->d * (out_dtype == HYTOPK_ROWS_BF16 ? 2 : 4);
+    if (overlap(extent(out, bytes), extent(c->codes, cache_code_bytes(c))))
+      return fail(HYTOPK_EINVAL, "out overlaps the cache");
+    hk::CacheReadArgs a{};
+    a.codes = static_cast<const uint8_t*>(c->codes);
+    a.scale = c->scale;
+    a.L = (int)c->L;
+    a.slots = slots;
+    a.start = start;
+    a.n = (int)n;
+    a.row = c->heads * c->d;
+    a.out = out;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    Span sp("cache_read", s);
+    HK_HIP(hk::launch_cache_read(a, out_dtype, c->dtype, s), "cache read launch");
+    return HYTOPK_OK;
+  });
+}
+
+size_t hytopk_attention_mass_workspace(const hytopk_attention* p) {
+  if (check_attention(p) != HYTOPK_OK) return 0;
+  int nsplit = 1, len = 0;
+  hk::mass_splits(p->n, p->k, nsplit, len);
+  const size_t parts = nsplit > 1 ? (size_t)p->n * nsplit * (size_t)hk::mass_rows(p->heads, p->key_heads) : 0;
+  return align_up(std::max<size_t>(parts * sizeof(float2), 1));
+}
+
+int hytopk_attention_mass(const hytopk_attention* p, const void* q, const void* k,
+                          const int32_t* idx, const float* lse, float* mass, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  return guarded([&]() -> int {
+    int rc = check_attention(p);
+    if (rc) return rc;
+    if (p->n == 0) return HYTOPK_OK;
+    if (!q || !k || !idx || !mass) return fail(HYTOPK_EINVAL, "q, k, idx and mass must be non-NULL");
+    if (misaligned(q, 16) || misaligned(k, 16)) return fail(HYTOPK_EINVAL, "q and k must be 16-byte aligned");
+    if (misaligned(idx, 4) || misaligned(lse, 4) || misaligned(mass, 4))
+      return fail(HYTOPK_EINVAL, "idx, lse and mass must be 4-byte aligned");
+    if (!lse && (rc = check_ws(workspace, workspace_bytes, hytopk_attention_mass_workspace(p)))) return rc;
+    hk::MassArgs a{};
+    a.q = static_cast<const uint16_t*>(q);
+    a.k = static_cast<const uint16_t*>(k);
+    a.idx = idx;
+    a.lse = lse;
+    a.part = static_cast<float2*>(workspace);
+    a.mass = mass;
+    a.L = (int)p->L;
+    a.n = (int)p->n;
+    a.heads = p->heads;
+    a.groups = p->key_heads;
+    a.topk = p->k;
+    a.scale2 = (float)((double)p->softmax_scale * 1.4426950408889634074);
+    a.inv_heads = 1.0f / (float)p->heads;
+    hk::mass_splits(p->n, p->k, a.nsplit, a.split_len);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    Span sp("attention_mass", s);
+    HK_HIP(hk::launch_attention_mass(a, p->d, s), "attention mass launch");
+    return HYTOPK_OK;
+  });
+}
+
+int hytopk_index_loss(int64_t n, int32_t k, const float* score, const float* mass,
+                      const float* weight, float* loss, float* d_score, void* stream) {
+  return guarded([&]() -> int {
+    if (n < 0 || k <= 0) return fail(HYTOPK_EINVAL, "n must be >= 0 and k > 0");
+    if (n >= kMaxRows) return fail(HYTOPK_EUNSUPPORTED, "n >= 2^31");
+    if (k > kMaxK) return fail(HYTOPK_EUNSUPPORTED, "k > 2048");
+    if (n == 0) return HYTOPK_OK;
+    if (!score || !mass) return fail(HYTOPK_EINVAL, "score and mass must be non-NULL");
+    if (!loss && !d_score) return fail(HYTOPK_EINVAL, "loss and d_score are both NULL");
+    for (const void* x : {(const void*)score, (const void*)mass, (const void*)weight,
+                          (const void*)loss, (const void*)d_score})
+      if (misaligned(x, 4)) return fail(HYTOPK_EINVAL, "arrays must be 4-byte aligned");
+    hk::LossArgs a{score, mass, weight, loss, d_score, (int)n, k};
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    Span sp("index_loss", s);
+    HK_HIP(hk::launch_index_loss(a, s), "index loss launch");
+    return HYTOPK_OK;
+  });
 }
 
 }  // extern "C"

@@ -251,4 +251,95 @@ int bwd_padded_k(int topk);  // key slots per query in the u buffer
 hipError_t launch_fill_zero(float* p, int64_t n, hipStream_t s);
 size_t bwd_sort_hist_count(int64_t N);
 
+// ---- rotary positions, the quantised cache (rows.hip)
+
+constexpr int kRowsBF16 = 0, kRowsFP32 = 1;            // hytopk_rows_dtype
+constexpr int kRotHalf = 0, kRotInterleaved = 1;       // hytopk_rotary_layout
+
+// A rotation (freq == null: none) and the tokens' positions.
+struct RotArgs {
+  const double* freq;  // [dim/2] radians a position
+  const int* pos;      // [n] positions, or null (pos0 + i)
+  int64_t pos0;
+  float gain;
+  float sign;          // 1, or -1 for the transposed rotation
+  int dim;
+  int first;
+  int layout;
+};
+
+struct RotaryArgs {
+  const void* x;
+  void* y;
+  int64_t xts, xhs, yts, yhs;  // token and head strides in elements
+  int n, heads, d;
+  RotArgs rot;
+};
+
+hipError_t launch_rotary(const RotaryArgs& a, int in_dtype, int out_dtype, hipStream_t s);
+
+struct CacheWriteArgs {
+  const void* x;
+  int64_t ts, hs;
+  int n, heads, d;
+  RotArgs rot;
+  uint8_t* codes;
+  void* scale;
+  int L;
+  const int* slots;    // [n] cache rows, or null (start + i)
+  int64_t start;
+  int* claim;          // [L] last row naming each slot, or null (each row looks for a later one)
+};
+
+// Rows up to this many look for a later row of the same slot by themselves;
+// more take `claim` (two more launches).
+constexpr int kClaimRows = 1024;
+hipError_t launch_cache_write(const CacheWriteArgs& a, int in_dtype, int fmt, hipStream_t s);
+
+struct CacheReadArgs {
+  const uint8_t* codes;
+  const void* scale;
+  int L;
+  const int* slots;
+  int64_t start;
+  int n;
+  int row;             // elements of a row (heads * d)
+  void* out;
+};
+
+hipError_t launch_cache_read(const CacheReadArgs& a, int out_dtype, int fmt, hipStream_t s);
+
+// ---- attention mass at the selected entries, index loss (loss.hip)
+
+struct MassArgs {
+  const uint16_t* q;   // bf16 [n][heads][d]
+  const uint16_t* k;   // bf16 [L][groups][d]
+  const int* idx;      // [n][topk]
+  const float* lse;    // [n][heads] natural, or null
+  float2* part;        // [n][nsplit][rows]: (max, sum) of each split (nsplit > 1, without lse)
+  float* mass;         // [n][topk]
+  int L, n, heads, groups, topk;
+  float scale2;        // softmax scale * log2(e)
+  float inv_heads;
+  int nsplit;          // workgroups of a query
+  int split_len;       // entries of a split, a multiple of 64
+};
+
+// Rows of q as the kernel holds them: the heads of a key head padded to 16.
+int64_t mass_rows(int heads, int groups);
+void mass_splits(int64_t n, int topk, int& nsplit, int& split_len);
+bool mass_supports(int d);
+hipError_t launch_attention_mass(const MassArgs& a, int d, hipStream_t s);
+
+struct LossArgs {
+  const float* score;
+  const float* mass;
+  const float* weight;  // or null (1)
+  float* loss;          // or null
+  float* dscore;        // or null
+  int n, k;
+};
+
+hipError_t launch_index_loss(const LossArgs& a, hipStream_t s);
+
 }  // namespace hk

@@ -1,0 +1,446 @@
+// The indexer's training target and loss: the attention's probability mass at
+// the selected entries (MFMA over gathered key rows), and the divergence of
+// the selection's softmax from it with its gradient.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "common.h"
+#include "launch.h"
+
+namespace hk {
+
+namespace {
+
+constexpr int kMassThreads = 256;
+constexpr int kMassWaves = kMassThreads / kWave;
+constexpr int kItemTiles = 8;      // head tiles whose softmax statistics a wave keeps in registers
+constexpr float kNoMax = -3.0e38f;  // maximum of nothing: finite, so that differences stay defined
+constexpr float kLazy = 8.0f;      // a maximum moves when exceeded by 2^8: sums stay below 2^19
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// (max, sum) of two parts of a softmax sum in base 2.
+__device__ __forceinline__ float2 join(float2 a, float2 b) {
+  const float m = fmaxf(a.x, b.x);
+  return make_float2(m, a.y * exp2_fast(a.x - m) + b.y * exp2_fast(b.x - m));
+}
+
+// How the heads of a query lie on 16-row tiles: each key head's heads padded to
+// whole tiles.
+struct HeadTiles {
+  int per_group;  // heads of a key head
+  int tiles;      // tiles of a key head
+  __host__ __device__ HeadTiles(int heads, int groups)
+      : per_group(heads / groups), tiles((heads / groups + 15) / 16) {}
+  // head of row r of tile t, or -1
+  __device__ __forceinline__ int head(int t, int r) const {
+    const int g = t / tiles, h = (t - g * tiles) * 16 + r;
+    return h < per_group ? g * per_group + h : -1;
+  }
+};
+
+// LDS of a workgroup: per row of q, the row itself, (max, 1 / sum) and the
+// waves' (max, sum).
+constexpr int mass_row_bytes(int d) { return 2 * d + 8 + 8 * kMassWaves; }
+constexpr int kMassLdsBytes = 150 * 1024;  // q rows of a pass, at most
+constexpr int kMassLdsSmall = 40 * 1024;   // enough passes to keep this where key heads allow it
+
+// Tiles of a pass over a query's heads: whole key heads within kMassLdsSmall (their
+// keys differ, so passes cost nothing), or else as much of one key head
+// as the LDS holds (more than one pass then gathers its keys again).
+int mass_pass_tiles(int heads, int groups, int d) {
+  const HeadTiles ht(heads, groups);
+  const int fit = kMassLdsBytes / (16 * mass_row_bytes(d));
+  const int small = kMassLdsSmall / (16 * mass_row_bytes(d)) / ht.tiles * ht.tiles;
+  return std::min(groups * ht.tiles, std::max(small, std::min(ht.tiles, fit)));
+}
+
+// MODE 0: (max, sum) of a split; 1: mass, from lse or from the splits' parts; 2: both at once
+// (one workgroup a query).
+//
+// A workgroup holds one query, its heads in passes of `pass` tiles: their q
+// rows lie in LDS in MFMA operand order (lane l of tile t, k-step s reads the 16
+// bytes at ((t * NK + s) * 64 + l) * 16), and each of its four waves takes every
+// fourth block of 16 entries, whose key rows it gathers from memory straight
+// into operand registers, one block ahead.  A key row is read once a pass for all heads
+// of its key head.
+//   statistics: D = K Q^T, so that a lane holds four keys of one head and
+//     keeps one (max, sum) per tile;
+//   mass: D = Q K^T, so that a lane holds four heads of one key and adds
+//     their exponentials into one number.
+// The two gather the keys twice: the logits of a query (heads x k in fp32)
+// are as large as a CU's whole register file, and written out they
+// would be as many bytes as the key rows.
+template <int NK, int MODE>
+__global__ void __launch_bounds__(kMassThreads) mass_kernel(MassArgs a, int pass) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  constexpr int D = NK * 32;
+  const HeadTiles ht(a.heads, a.groups);
+  const int T = a.groups * ht.tiles, cap = pass * 16;
+  uint8_t* qs = lds;
+  float* ms = reinterpret_cast<float*>(qs + (size_t)cap * D * 2);  // [cap] reference exponent
+  float* rs = ms + cap;                                            // [cap] 1 / sum
+  float2* red = reinterpret_cast<float2*>(rs + cap);               // [waves][cap]
+  int* ids = reinterpret_cast<int*>(red + kMassWaves * cap);       // [split_len]
+  float* sums = reinterpret_cast<float*>(ids + a.split_len);       // [split_len], several passes only
+
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int col = lane & 15, grp = lane >> 4;
+  // Workgroups go to the 8 XCDs in turn; each XCD takes a contiguous run of
+  // queries, whose selections overlap, so that their keys meet in its L2.
+  const int q = [] {
+    const int nx = 8, b = blockIdx.x, x = b % nx;
+    const int base = (int)gridDim.x / nx, extra = (int)gridDim.x % nx;
+    return x * base + min(x, extra) + b / nx;
+  }();
+  const int split = blockIdx.y;
+  const int j0 = split * a.split_len, nj = min(a.split_len, a.topk - j0);
+  const int njp = (nj + 15) & ~15;
+  for (int j = tid; j < njp; j += kMassThreads) {
+    const int id = j < nj ? a.idx[(int64_t)q * a.topk + j0 + j] : -1;
+    ids[j] = (unsigned)id < (unsigned)a.L ? id : -1;
+  }
+  const int nblk = njp / 16;
+  const int mine = wave < nblk ? (nblk - wave + kMassWaves - 1) / kMassWaves : 0;  // wave-uniform
+  const int row_elems = a.groups * D;
+  auto gather = [&](int i, int g, bf16x8* f) -> int {  // the wave's i-th block, key head g
+    const int id = i < mine ? ids[(wave + i * kMassWaves) * 16 + col] : -1;
+    const uint16_t* p = a.k + (int64_t)max(id, 0) * row_elems + g * D + grp * 8;
+    if (id >= 0) {
+#pragma unroll
+      for (int s = 0; s < NK; ++s) f[s] = *reinterpret_cast<const bf16x8*>(p + s * 32);
+    } else {
+#pragma unroll
+      for (int s = 0; s < NK; ++s) f[s] = bf16x8{};
+    }
+    return id;
+  };
+  auto qfrag = [&](int t, int s) {  // t: tile of the pass
+    return *reinterpret_cast<const bf16x8*>(qs + ((t * NK + s) * 64 + lane) * 16);
+  };
+
+  for (int c0 = 0; c0 < T; c0 += pass) {
+    const int c1 = min(T, c0 + pass), rows = (c1 - c0) * 16;
+    if (c0) __syncthreads();  // the last pass is through with the LDS
+    const u32x4 zero = {0u, 0u, 0u, 0u};
+    for (int e = tid; e < rows * NK * 4; e += kMassThreads) {
+      const int r = e / (NK * 4), c = e - r * (NK * 4);
+      const int h = ht.head(c0 + (r >> 4), r & 15);
+      u32x4 v = zero;
+      if (h >= 0)
+        v = *reinterpret_cast<const u32x4*>(a.q + ((int64_t)q * a.heads + h) * D + c * 8);
+      const int slot = ((r >> 4) * NK + (c >> 2)) * 64 + (c & 3) * 16 + (r & 15);
+      *reinterpret_cast<u32x4*>(qs + slot * 16) = v;
+    }
+    if constexpr (MODE == 1) {
+      for (int r = tid; r < rows; r += kMassThreads) {
+        const int h = ht.head(c0 + (r >> 4), r & 15);
+        float m = 0.0f, rl = 0.0f;
+        if (h >= 0 && a.lse) {
+          // lse log2(e) as a rounded reference and the factor for what the rounding left
+          constexpr float kHi = 1.44269502162933349609375f, kLo = 1.925963033500011e-8f;
+          const float l = a.lse[(int64_t)q * a.heads + h];
+          m = l * kHi;
+          rl = fabsf(m) < 3.0e38f ? exp2_fast(-fmaf(l, kLo, fmaf(l, kHi, -m))) : 1.0f;
+        } else if (h >= 0) {
+          float2 p = make_float2(kNoMax, 0.0f);
+          for (int sp = 0; sp < a.nsplit; ++sp)
+            p = join(p, a.part[((int64_t)q * a.nsplit + sp) * (T * 16) + c0 * 16 + r]);
+          m = p.x;
+          rl = p.y == 0.0f ? 0.0f : 1.0f / p.y;
+        }
+        ms[r] = m;
+        rs[r] = rl;
+      }
+    }
+    __syncthreads();
+
+    if constexpr (MODE != 1) {
+      // Items: up to kItemTiles tiles of one key head.
+      for (int t0 = c0; t0 < c1;) {
+        const int g = t0 / ht.tiles;
+        const int nt = min(min(kItemTiles, (g + 1) * ht.tiles - t0), c1 - t0);
+        float m[kItemTiles], l[kItemTiles];
+#pragma unroll
+        for (int t = 0; t < kItemTiles; ++t) { m[t] = kNoMax; l[t] = 0.0f; }
+        bf16x8 f[2][NK];
+        int id[2];
+        id[0] = gather(0, g, f[0]);
+        for (int i0 = 0; i0 < mine; i0 += 2) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if (i0 + u >= mine) break;  // wave-uniform
+            id[1 - u] = gather(i0 + u + 1, g, f[1 - u]);
+            const unsigned live = (unsigned)(__ballot(id[u] >= 0) & 0xffffu) >> (4 * grp);
+#pragma unroll
+            for (int t = 0; t < kItemTiles; ++t) {
+              if (t >= nt) break;  // uniform
+              f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+              for (int s = 0; s < NK; ++s)
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[u][s], qfrag(t0 - c0 + t, s), acc, 0, 0, 0);
+              float x[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[e] = (live >> e) & 1u ? acc[e] * a.scale2 : -__builtin_inff();
+              const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+              if (top > m[t] + kLazy) {
+                l[t] *= exp2_fast(m[t] - top);
+                m[t] = top;
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) l[t] += exp2_fast(x[e] - m[t]);
+            }
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < kItemTiles; ++t) {
+          if (t >= nt) break;
+          float2 p = make_float2(m[t], l[t]);
+          p = join(p, make_float2(__shfl_xor(p.x, 16), __shfl_xor(p.y, 16)));
+          p = join(p, make_float2(__shfl_xor(p.x, 32), __shfl_xor(p.y, 32)));
+          if (grp == 0) red[wave * cap + (t0 - c0 + t) * 16 + col] = p;
+        }
+        t0 += nt;
+      }
+      __syncthreads();
+      for (int r = tid; r < rows; r += kMassThreads) {
+        float2 p = red[r];
+#pragma unroll
+        for (int w = 1; w < kMassWaves; ++w) p = join(p, red[w * cap + r]);
+        if constexpr (MODE == 0) {
+          a.part[((int64_t)q * a.nsplit + split) * (T * 16) + c0 * 16 + r] = p;
+        } else {
+          ms[r] = p.x;
+          rs[r] = ht.head(c0 + (r >> 4), r & 15) < 0 || p.y == 0.0f ? 0.0f : 1.0f / p.y;
+        }
+      }
+      if constexpr (MODE == 2) __syncthreads();
+    }
+
+    if constexpr (MODE != 0) {
+      // Steps: (block, key head of the pass), the key head innermost.
+      const int g0 = c0 / ht.tiles, g1 = (c1 + ht.tiles - 1) / ht.tiles;
+      const int steps = mine * (g1 - g0);
+      bf16x8 f[2][NK];
+      float o = 0.0f;
+      int blk = 0, g = g0;   // of the step at hand
+      int nb = 0, ng = g0;   // of the step being gathered
+      auto next = [&](bf16x8* dst) {
+        gather(nb, ng, dst);
+        if (++ng == g1) { ng = g0; ++nb; }
+      };
+      next(f[0]);
+      for (int i0 = 0; i0 < steps; i0 += 2) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (i0 + u >= steps) break;  // wave-uniform
+          next(f[1 - u]);
+          const int ta = max(c0, g * ht.tiles) - c0, tb = min(c1, (g + 1) * ht.tiles) - c0;
+          for (int t = ta; t < tb; ++t) {
+            f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int s = 0; s < NK; ++s)
+              acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qfrag(t, s), f[u][s], acc, 0, 0, 0);
+            const f32x4 m = *reinterpret_cast<const f32x4*>(ms + t * 16 + 4 * grp);
+            const f32x4 r = *reinterpret_cast<const f32x4*>(rs + t * 16 + 4 * grp);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o = fmaf(exp2_fast(fmaf(acc[e], a.scale2, -m[e])), r[e], o);
+          }
+          if (++g == g1) {
+            g = g0;
+            o += __shfl_xor(o, 16);
+            o += __shfl_xor(o, 32);
+            const int j = (wave + blk * kMassWaves) * 16 + col;
+            if (grp == 0) {  // the wave's own entries: no other wave reads or writes them
+              if (c0) o += sums[j];
+              if (c1 < T) sums[j] = o;
+              else if (j < nj) a.mass[(int64_t)q * a.topk + j0 + j] = ids[j] >= 0 ? o * a.inv_heads : 0.0f;
+            }
+            o = 0.0f;
+            ++blk;
+          }
+        }
+      }
+    }
+  }
+}
+
+template <int NK, int MODE>
+hipError_t mass_launch(const MassArgs& a, hipStream_t s) {
+  static LdsLimit lim;
+  const int pass = mass_pass_tiles(a.heads, a.groups, NK * 32);
+  const bool several = pass < mass_rows(a.heads, a.groups) / 16;
+  const int lds = pass * 16 * mass_row_bytes(NK * 32) + a.split_len * (several ? 8 : 4);
+  hipError_t e = raise_dynamic_lds((const void*)mass_kernel<NK, MODE>, lds, lim);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((mass_kernel<NK, MODE>), dim3((unsigned)a.n, (unsigned)a.nsplit),
+                     dim3(kMassThreads), (size_t)lds, s, a, pass);
+  return hipGetLastError();
+}
+
+template <int NK>
+hipError_t mass_d(const MassArgs& a, hipStream_t s) {
+  if (a.lse) return mass_launch<NK, 1>(a, s);
+  if (a.nsplit == 1) return mass_launch<NK, 2>(a, s);
+  hipError_t e = mass_launch<NK, 0>(a, s);
+  return e != hipSuccess ? e : mass_launch<NK, 1>(a, s);
+}
+
+}  // namespace
+
+int64_t mass_rows(int heads, int groups) { return (int64_t)groups * HeadTiles(heads, groups).tiles * 16; }
+
+// Splits of a query's entries so that few queries still fill the chip: about
+// 1,024 workgroups, each with a block of 16 entries for every wave.
+void mass_splits(int64_t n, int topk, int& nsplit, int& split_len) {
+  const int most = (topk + 63) / 64;
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(most, 1024 / std::max<int64_t>(1, n)));
+  split_len = (int)(((topk + want - 1) / want + 63) / 64 * 64);
+  nsplit = (topk + split_len - 1) / split_len;
+}
+
+bool mass_supports(int d) {
+  return d == 64 || d == 96 || d == 128 || d == 192 || d == 256 || d == 512 || d == 576;
+}
+
+hipError_t launch_attention_mass(const MassArgs& a, int d, hipStream_t s) {
+  if (a.n <= 0) return hipSuccess;
+  switch (d) {
+    case 64: return mass_d<2>(a, s);
+    case 96: return mass_d<3>(a, s);
+    case 128: return mass_d<4>(a, s);
+    case 192: return mass_d<6>(a, s);
+    case 256: return mass_d<8>(a, s);
+    case 512: return mass_d<16>(a, s);
+    case 576: return mass_d<18>(a, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+// ------------------------------------------------------------ index loss
+
+namespace {
+
+constexpr int kLossThreads = 256;
+
+__device__ __forceinline__ float wave_sum(float x) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) x += __shfl_xor(x, off);
+  return x;
+}
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor(x, off));
+  return x;
+}
+
+// One wave a row, the row's N entries per lane in registers, so that scores
+// and mass are read once and the gradient is written once.  With p = softmax
+// and t = mass / sum, each term t (ln t - ln p) - t + p is non-negative and
+// their sum is the loss (both t and p sum to 1): no cancellation between large terms.
+template <int N, bool VEC>
+__global__ void __launch_bounds__(kLossThreads) index_loss_kernel(LossArgs a) {
+  const int lane = threadIdx.x & 63;
+  constexpr int W = kLossThreads / kWave;
+  for (int64_t i = (int64_t)blockIdx.x * W + (threadIdx.x >> 6); i < a.n; i += (int64_t)gridDim.x * W) {
+    const int64_t at = i * a.k;
+    float s[N], t[N];
+    // entry j of this lane: pieces of four (VEC), or every 64th
+    auto entry = [&](int e) { return VEC ? (e >> 2) * 256 + lane * 4 + (e & 3) : e * 64 + lane; };
+    if constexpr (VEC) {
+#pragma unroll
+      for (int c = 0; c < N / 4; ++c) {
+        const int j = c * 256 + lane * 4;
+        const bool in = j < a.k;  // k is a multiple of four
+        const f32x4 sv = in ? *reinterpret_cast<const f32x4*>(a.score + at + j) : f32x4{};
+        const f32x4 tv = in ? *reinterpret_cast<const f32x4*>(a.mass + at + j) : f32x4{};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[4 * c + e] = in ? sv[e] : -__builtin_inff();
+          t[4 * c + e] = tv[e];
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const int j = entry(e);
+        s[e] = j < a.k ? a.score[at + j] : -__builtin_inff();
+        t[e] = j < a.k ? a.mass[at + j] : 0.0f;
+      }
+    }
+    float top = -__builtin_inff(), total = 0.0f;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const bool live = !(s[e] == -__builtin_inff());
+      t[e] = live ? t[e] : 0.0f;  // dead entries hold anything
+      top = fmaxf(top, s[e]);
+      total += t[e];
+    }
+    top = wave_max(top);
+    total = wave_sum(total);
+    const bool none = total == 0.0f;  // also a row without a live entry
+    const float ref = top == -__builtin_inff() ? 0.0f : top;
+    float sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      s[e] -= ref;
+      sum += expf(s[e]);
+    }
+    sum = wave_sum(sum);
+    const float up = total < 0x1p-100f ? 0x1p100f : 1.0f;  // keeps 1 / total finite
+    const float lsum = logf(sum), rsum = 1.0f / sum, rtotal = 1.0f / (total * up);
+    const float w = a.weight ? a.weight[i] : 1.0f;
+    float loss = 0.0f;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const float p = expf(s[e]) * rsum, q = t[e] * up * rtotal;
+      const float kl = q > 0.0f ? q * (logf(q) - (s[e] - lsum)) : q;
+      loss += kl - q + p;
+      t[e] = w * (p - q);
+    }
+    loss = wave_sum(loss);
+    if (a.loss && lane == 0) a.loss[i] = none ? 0.0f : w * loss;
+    if (a.dscore) {
+      if constexpr (VEC) {
+#pragma unroll
+        for (int c = 0; c < N / 4; ++c) {
+          const int j = c * 256 + lane * 4;
+          if (j >= a.k) continue;
+          f32x4 v;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = none ? 0.0f : t[4 * c + e];
+          *reinterpret_cast<f32x4*>(a.dscore + at + j) = v;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const int j = entry(e);
+          if (j < a.k) a.dscore[at + j] = none ? 0.0f : t[e];
+        }
+      }
+    }
+  }
+}
+
+template <bool VEC>
+hipError_t index_loss_vec(const LossArgs& a, hipStream_t s) {
+  const int64_t w = kLossThreads / kWave;
+  const dim3 grid((unsigned)std::min<int64_t>((a.n + w - 1) / w, int64_t(1) << 22)), block(kLossThreads);
+  if (a.k <= 256) hipLaunchKernelGGL((index_loss_kernel<4, VEC>), grid, block, 0, s, a);
+  else if (a.k <= 512) hipLaunchKernelGGL((index_loss_kernel<8, VEC>), grid, block, 0, s, a);
+  else if (a.k <= 1024) hipLaunchKernelGGL((index_loss_kernel<16, VEC>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((index_loss_kernel<32, VEC>), grid, block, 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_index_loss(const LossArgs& a, hipStream_t s) {
+  if (a.n <= 0) return hipSuccess;
+  auto off = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 != 0; };
+  const bool vec = a.k % 4 == 0 && !off(a.score) && !off(a.mass) && !off(a.dscore);
+  return vec ? index_loss_vec<true>(a, s) : index_loss_vec<false>(a, s);
+}
+
+}  // namespace hk

@@ -268,6 +268,173 @@ int hytopk_backward(const hytopk_problem* p, const void* q, const void* q_scale,
                     const float* d_score, float* dq, float* dw, float* dk,
                     void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Around the selection: what makes the indexer's queries and keys, and what
+ * turns the replayed scores into the backward's upstream gradient.
+ *
+ *   rotary positions -> quantised rows in the storage formats above
+ *     -> hytopk_select -> hytopk_replay
+ *     -> attention mass (the target) -> index loss and d_score
+ *     -> hytopk_backward -> transposed rotation of dq and dk
+ *
+ * All of them are asynchronous on `stream`, launch kernels only (no copy, memset or
+ * synchronisation: they can be recorded in a HIP graph after one eager call)
+ * and hold no state between calls.  n = 0 is a valid call that does nothing.
+ * ------------------------------------------------------------------------- */
+
+/* Element types of the rows that the rotation and the cache calls read and write. */
+typedef enum {
+  HYTOPK_ROWS_BF16 = 0,
+  HYTOPK_ROWS_FP32 = 1
+} hytopk_rows_dtype;
+
+/* Rows [n][heads][d] in device memory: element (i, h, e) at
+ * data[i * token_stride + h * head_stride + e] (strides in elements, >= 0; the
+ * last axis is contiguous).  Rows that a call writes must not overlap each other:
+ * the smaller stride spans d elements or more, the larger one all of the other axis.
+ * Data is aligned to its element; 16-byte aligned data with strides that are
+ * multiples of 16 bytes is read and written 16 bytes at a time. */
+typedef struct {
+  void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+  int32_t dtype;  /* hytopk_rows_dtype */
+  int32_t reserved;
+} hytopk_rows;
+
+typedef enum {
+  HYTOPK_ROTARY_HALF = 0,        /* pair i is elements (i, i + dim/2) of the rotated part */
+  HYTOPK_ROTARY_INTERLEAVED = 1  /* pair i is elements (2i, 2i + 1) */
+} hytopk_rotary_layout;
+
+typedef enum {
+  HYTOPK_SCALING_NONE = 0,
+  HYTOPK_SCALING_LINEAR = 1,  /* every frequency divided by `factor` */
+  HYTOPK_SCALING_NTK = 2,     /* base raised so that the slowest frequency is divided by `factor` */
+  HYTOPK_SCALING_YARN = 3     /* by wavelength: fast ones kept, slow ones divided, a ramp between;
+                                 the rotated part times 0.1 ln(factor) + 1 */
+} hytopk_rotary_scaling;
+
+/* A rotation of elements first .. first + dim - 1 of every head: at position
+ * p, pair i = (a, b) becomes gain * (a cos(p f_i) - b sin(p f_i),
+ * b cos(p f_i) + a sin(p f_i)); the other elements stay as they are. */
+typedef struct {
+  const double* freq;  /* device [dim/2]: f_i in radians a position, 8-byte aligned */
+  double gain;         /* factor on the rotated part */
+  int32_t dim;         /* rotated elements of a head, even, first + dim <= d */
+  int32_t first;
+  int32_t layout;      /* hytopk_rotary_layout */
+  int32_t reserved;
+} hytopk_rotary_plan;
+
+/* The frequencies and gain of a plan, computed on the host in 64 bits:
+ * f_i = base^(-2i/dim) for i = 0 .. dim/2 - 1, then `scaling` by `factor` (>= 1) for a
+ * model whose positions reached `original` before (read by YARN alone; it keeps
+ * frequencies that turn 32 times or more in it and divides those that turn
+ * once or less).  freq: host [dim/2]; gain: host. */
+int hytopk_rotary_frequencies(int32_t dim, double base, int32_t scaling, double factor,
+                              int64_t original, double* freq, double* gain);
+
+/* y = the rotation of x.  Token i sits at position q_pos[i] (device int32 [n])
+ * or, with q_pos NULL, q_start + i (below 2^31).  backward = 1 applies the transposed rotation
+ * (gain included): the gradient with respect to x from the gradient with
+ * respect to y.  Angles are reduced in 64 bits (exact to 32-bit rounding at any
+ * int32 position), products are fp32, rounded once to y's type.  x and y may
+ * be the same rows (same data, strides and type); otherwise their memory must
+ * not overlap.  heads, d >= 1 and heads * d < 2^31; dim <= 1024. */
+int hytopk_rotary(const hytopk_rotary_plan* plan, int64_t n, int32_t heads, int32_t d,
+                  const hytopk_rows* x, const hytopk_rows* y, const int32_t* q_pos,
+                  int64_t q_start, int32_t backward, void* stream);
+
+/* Rows in one of the storage formats: L rows of heads * d elements, laid out
+ * as hytopk_select takes k (heads = 1) or q: codes [L][heads][d] (bf16, E4M3
+ * bytes, or E2M1 nibbles in rows of d/2 bytes a head), 16-byte aligned; scale NULL for bf16,
+ * fp32 [L] for FP8 (one scale a row, over its heads), uint8 [L][heads][d/32] for MX;
+ * 4-byte aligned.  d is a multiple of 32 and heads * d <= 8192. */
+typedef struct {
+  void* codes;
+  void* scale;
+  int64_t L;      /* < 2^31 */
+  int32_t heads;
+  int32_t d;
+  int32_t dtype;  /* hytopk_dtype */
+  int32_t reserved;
+} hytopk_cache;
+
+/* Workspace bytes of hytopk_cache_write for n rows: 0 when it needs none
+ * (rows by `start`, or few rows), else L int32. */
+size_t hytopk_cache_write_workspace(const hytopk_cache* c, int64_t n, int32_t by_slot);
+
+/* Quantises rows x [n][heads][d] as they are written: row i goes to cache row
+ * slots[i] (device int32 [n]) or, with slots NULL, start + i (start + n <= L).
+ * A slot outside [0, L) is padding: nothing is written for it.  When several rows name
+ * one slot, the last of them is kept.  Other cache rows are left as they were.
+ * With a plan the rows are rotated first (as hytopk_rotary does, in fp32, not
+ * rounded in between).  Values are rounded to nearest, ties to even:
+ *   FP8   scale = max(amax / 448, 2^-126) in fp32 over the row (1 for a row of
+ *         zeros), code = E4M3(x / scale) of the exact quotient;
+ *   MX    per 32 elements of a head e = floor(log2(amax)) - 8 (E4M3) or - 2 (E2M1),
+ *         clamped to -127 .. 127, scale byte e + 127 (0 for a block of zeros),
+ *         code = x * 2^-e rounded, saturating at 448 or 6.
+ * x is finite: an infinity or NaN leaves its own row (FP8) or block (MX)
+ * unspecified.  x must not overlap the cache. */
+int hytopk_cache_write(const hytopk_cache* c, int64_t n, const hytopk_rows* x,
+                       const int32_t* slots, int64_t start, const hytopk_rotary_plan* plan,
+                       const int32_t* q_pos, int64_t q_start, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/* Reads cache rows back: out [n][heads][d] (contiguous, 16-byte aligned, type out_dtype) =
+ * code * scale of row slots[i], or start + i with slots NULL, rounded once.
+ * Slots outside [0, L) (the padding of a selection among them) give rows of zeros.  An E4M3 NaN
+ * code or a scale byte of 255 reads as NaN. */
+int hytopk_cache_read(const hytopk_cache* c, int64_t n, const int32_t* slots, int64_t start,
+                      void* out, int32_t out_dtype, void* stream);
+
+/* Attention over selected entries: query i's `heads` heads attend to the keys
+ * idx[i][0..k) of key head h / (heads / key_heads). */
+typedef struct {
+  int64_t L;            /* number of keys */
+  int64_t n;            /* number of queries */
+  int32_t heads;        /* attention heads */
+  int32_t key_heads;    /* divides heads */
+  int32_t d;            /* head dimension: 64, 96, 128, 192, 256, 512 or 576 */
+  int32_t k;            /* entries per query, <= 2048 */
+  float softmax_scale;  /* factor on q . k */
+  int32_t reserved;
+} hytopk_attention;
+
+/* Workspace bytes of hytopk_attention_mass without lse (0 on invalid input). */
+size_t hytopk_attention_mass_workspace(const hytopk_attention* p);
+
+/* The attention's probability mass at the selected entries, averaged over heads:
+ *   mass[i][j] = 1/heads sum_h exp(softmax_scale q[i][h] . k[idx[i][j]][g(h)] - lse[i][h])
+ * the target of the indexer's loss.  q [n][heads][d] and k [L][key_heads][d] are
+ * bf16, contiguous and 16-byte aligned; idx [n][k] int32; mass [n][k] fp32.
+ * lse [n][heads] fp32 is the attention's log-sum-exp (its own normaliser, over
+ * whatever keys it attended to); with lse NULL it is taken over the row's
+ * entries, so that each row sums to 1, and the workspace is required.
+ * An index outside [0, L) is padding: mass 0, no part in the sum; its key row is
+ * never read.  An index that stands twice counts twice.  Products are bf16 MFMA with fp32
+ * accumulation; maxima, sums and exponentials are fp32. 
+ * n < 2^24 and heads <= 1024, or HYTOPK_EUNSUPPORTED. */
+int hytopk_attention_mass(const hytopk_attention* p, const void* q, const void* k,
+                          const int32_t* idx, const float* lse, float* mass, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* The indexer's loss and its gradient: per query the divergence of the
+ * selection's softmax from the attention's mass, over the live entries of the
+ * row (score other than -inf; replay gives -inf at padding):
+ *   t = mass / sum(mass),  p = softmax(score),
+ *   loss[i] = weight[i] sum_j t_j (ln t_j - ln p_j),
+ *   d_score[i][j] = weight[i] (p_j - t_j): d loss[i] / d score[i][j]
+ * (the mass is a constant).  score, mass, d_score [n][k] fp32, loss [n] fp32,
+ * weight [n] fp32 or NULL (1).  Dead entries get 0, whatever their mass holds;
+ * a row without a live entry, or whose live mass sums to 0, gets loss 0 and
+ * gradient 0.  loss or d_score may be NULL; d_score may be score or mass
+ * itself.  1 <= k <= 2048. */
+int hytopk_index_loss(int64_t n, int32_t k, const float* score, const float* mass,
+                      const float* weight, float* loss, float* d_score, void* stream);
+
 const char* hytopk_status_string(int status);
 const char* hytopk_last_error(void);  /* thread-local; "" when none */
 
@@ -280,7 +447,8 @@ const char* hytopk_last_error(void);  /* thread-local; "" when none */
 /* Kernel tracing.  While enabled, every launch the library makes is bracketed
  * by a pair of hipEvents recorded on the caller's stream, and the elapsed time
  * is accumulated per phase name ("sample_tau", "score_compact", "check",
- * "cand_select", "score_rows", "row_topk", "replay", "bwd_query", "bwd_dk").  Process-wide; not for
+ * "cand_select", "score_rows", "row_topk", "replay", "bwd_query", "bwd_dk", "rotary",
+ * "cache_write", "cache_read", "attention_mass", "index_loss").  Process-wide; not for
  * use with concurrent calls on different streams. */
 typedef struct {
   char name[32];
