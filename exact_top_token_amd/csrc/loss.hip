@@ -7,6 +7,7 @@
 
 #include "common.h"
 #include "launch.h"
+#include "tile.h"
 
 namespace hk {
 
@@ -24,6 +25,13 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 __device__ __forceinline__ float2 join(float2 a, float2 b) {
   const float m = fmaxf(a.x, b.x);
   return make_float2(m, a.y * exp2_fast(a.x - m) + b.y * exp2_fast(b.x - m));
+}
+
+// lse log2(e) as a rounded reference m and the factor 2^-(what the rounding left).
+__device__ __forceinline__ void lse_reference(float l, float& m, float& rl) {
+  constexpr float kHi = 1.44269502162933349609375f, kLo = 1.925963033500011e-8f;
+  m = l * kHi;
+  rl = fabsf(m) < 3.0e38f ? exp2_fast(-fmaf(l, kLo, fmaf(l, kHi, -m))) : 1.0f;
 }
 
 // How the heads of a query lie on 16-row tiles: each key head's heads padded to
@@ -138,11 +146,7 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(MassArgs a, int pass
         const int h = ht.head(c0 + (r >> 4), r & 15);
         float m = 0.0f, rl = 0.0f;
         if (h >= 0 && a.lse) {
-          // lse log2(e) as a rounded reference and the factor for what the rounding left
-          constexpr float kHi = 1.44269502162933349609375f, kLo = 1.925963033500011e-8f;
-          const float l = a.lse[(int64_t)q * a.heads + h];
-          m = l * kHi;
-          rl = fabsf(m) < 3.0e38f ? exp2_fast(-fmaf(l, kLo, fmaf(l, kHi, -m))) : 1.0f;
+          lse_reference(a.lse[(int64_t)q * a.heads + h], m, rl);
         } else if (h >= 0) {
           float2 p = make_float2(kNoMax, 0.0f);
           for (int sp = 0; sp < a.nsplit; ++sp)
@@ -266,6 +270,273 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(MassArgs a, int pass
   }
 }
 
+// The same with the key rows staged through LDS, for rows of 128 or 256 bytes.
+// A direct-to-LDS load fetches rows whole, where gathering the operand layout gives
+// every lane its own 16 bytes of another row.  Each wave owns a ring of kMassRing stages of
+// 16 rows and waits for its own loads by count; the q rows of a pass
+// (PT tiles of one key head) stay in registers.  The mass walks the wave's blocks
+// from the last to the first, so that the rows still in the ring and in the
+// caches are used again.
+constexpr int kMassRing = 3;
+
+template <int NK, int PT, int MODE>
+__global__ void __launch_bounds__(kMassThreads, 3) mass_staged_kernel(MassArgs a) {
+  constexpr int D = NK * 32, RB = D * 2, NCH = RB / 16, OPS = 16 * RB / 1024;
+  constexpr int KPI = 1024 / RB;  // rows of a load
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  const HeadTiles ht(a.heads, a.groups);
+  const int T = a.groups * ht.tiles;
+  uint8_t* ring = lds;                                                        // [ring][waves][16 rows]
+  float* ms = reinterpret_cast<float*>(ring + kMassRing * kMassWaves * 16 * RB);  // [PT * 16]
+  float* rs = ms + PT * 16;                                                   // [PT * 16]
+  float2* red = reinterpret_cast<float2*>(rs + PT * 16);                      // [waves][PT * 16]
+  int* ids = reinterpret_cast<int*>(red + kMassWaves * PT * 16);              // [split_len]
+  float* sums = reinterpret_cast<float*>(ids + a.split_len);                  // [split_len]
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 15, grp = lane >> 4;
+  const int q = [] {  // a contiguous run of queries per XCD
+    const int nx = 8, b = blockIdx.x, x = b % nx;
+    const int base = (int)gridDim.x / nx, extra = (int)gridDim.x % nx;
+    return x * base + min(x, extra) + b / nx;
+  }();
+  const int split = blockIdx.y;
+  const int j0 = split * a.split_len, nj = min(a.split_len, a.topk - j0);
+  const int njp = (nj + 15) & ~15;
+  for (int j = tid; j < njp; j += kMassThreads) {
+    const int id = j < nj ? a.idx[(int64_t)q * a.topk + j0 + j] : -1;
+    ids[j] = (unsigned)id < (unsigned)a.L ? id : -1;
+  }
+  const int nblk = njp / 16;
+  const int mine = wave < nblk ? (nblk - wave + kMassWaves - 1) / kMassWaves : 0;  // wave-uniform
+  uint8_t* const ring0 = ring + wave * 16 * RB;  // stage s: + s * kMassWaves * 16 * RB
+  constexpr int SLOT = kMassWaves * 16 * RB;
+  const int64_t row_bytes = (int64_t)a.groups * RB;
+  int dsw[OPS];  // load p fetches this chunk of its row (the stage's swizzle)
+#pragma unroll
+  for (int p = 0; p < OPS; ++p) dsw[p] = 16 * ((lane % NCH) ^ key_swz<NCH>(p * KPI + lane / NCH));
+  const uint8_t* kbase = reinterpret_cast<const uint8_t*>(a.k);
+  // the wave's i-th block, key head g, into its stage; padding fetches row 0, which no live entry uses
+  auto issue = [&](int i, int g, int stage) {
+#pragma unroll
+    for (int p = 0; p < OPS; ++p) {
+      const int id = ids[(wave + i * kMassWaves) * 16 + p * KPI + lane / NCH];
+      lds_dma16(kbase + max(id, 0) * row_bytes + g * RB + dsw[p], ring0 + stage * SLOT + p * 1024);
+    }
+  };
+  const uint32_t ring_at = lds_addr(ring0);
+  uint32_t chunk_at[NK];
+#pragma unroll
+  for (int s = 0; s < NK; ++s) chunk_at[s] = col * RB + (((4 * s + grp) ^ key_swz<NCH>(col)) * 16);
+  auto frags = [&](int stage, bf16x8* f) {
+    uint32_t ad[NK];
+    u32x4 r[NK];
+#pragma unroll
+    for (int s = 0; s < NK; ++s) ad[s] = ring_at + stage * SLOT + chunk_at[s];
+    lds_read_chunks<NK>(ad, r);
+#pragma unroll
+    for (int s = 0; s < NK; ++s) f[s] = __builtin_bit_cast(bf16x8, r[s]);
+  };
+  auto await = [&](int ahead) {  // all but the newest `ahead` stages have landed
+    static_assert(kMassRing == 3, "stages waited for");
+    if (ahead >= 2) HK_WAIT_VM(2 * OPS);
+    else if (ahead == 1) HK_WAIT_VM(OPS);
+    else HK_WAIT_VM(0);
+  };
+
+  for (int c0 = 0, g = 0, ta = 0; c0 < T;) {
+    const int nt = min(PT, ht.tiles - ta);  // tiles of this pass: ta .. ta + nt - 1 of key head g
+    const bool last = c0 + nt == T;
+    bf16x8 qf[PT][NK];
+#pragma unroll
+    for (int t = 0; t < PT; ++t) {
+      const int h = t < nt ? ht.head(c0 + t, col) : -1;
+      const uint16_t* p = a.q + ((int64_t)q * a.heads + max(h, 0)) * D + grp * 8;
+#pragma unroll
+      for (int s = 0; s < NK; ++s)
+        qf[t][s] = h >= 0 ? *reinterpret_cast<const bf16x8*>(p + s * 32) : bf16x8{};
+    }
+    if constexpr (MODE == 1) {
+      for (int r = tid; r < PT * 16; r += kMassThreads) {
+        const int h = (r >> 4) < nt ? ht.head(c0 + (r >> 4), r & 15) : -1;
+        float m = 0.0f, rl = 0.0f;
+        if (h >= 0 && a.lse) {
+          lse_reference(a.lse[(int64_t)q * a.heads + h], m, rl);
+        } else if (h >= 0) {
+          float2 p = make_float2(kNoMax, 0.0f);
+          for (int sp = 0; sp < a.nsplit; ++sp)
+            p = join(p, a.part[((int64_t)q * a.nsplit + sp) * (T * 16) + c0 * 16 + r]);
+          m = p.x;
+          rl = p.y == 0.0f ? 0.0f : 1.0f / p.y;
+        }
+        ms[r] = m;
+        rs[r] = rl;
+      }
+    }
+    __syncthreads();
+
+    if constexpr (MODE != 1) {
+      float m[PT], l[PT];
+#pragma unroll
+      for (int t = 0; t < PT; ++t) { m[t] = kNoMax; l[t] = 0.0f; }
+      HK_WAIT_VM(0);  // from here on the wave counts its stages' loads alone
+#pragma unroll
+      for (int s = 0; s < kMassRing - 1; ++s)
+        if (s < mine) issue(s, g, s);
+      for (int i = 0, stage = 0; i < mine; ++i) {
+        const int ahead = i + kMassRing - 1;
+        if (ahead < mine) issue(ahead, g, stage == 0 ? kMassRing - 1 : stage - 1);
+        await(min(kMassRing - 1, mine - 1 - i));
+        bf16x8 f[NK];
+        frags(stage, f);
+        const bool on = ids[(wave + i * kMassWaves) * 16 + col] >= 0;
+        const unsigned all = (unsigned)(__ballot(on) & 0xffffu);
+        const unsigned live = all >> (4 * grp);
+#pragma unroll
+        for (int t = 0; t < PT; ++t) {
+          f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int s = 0; s < NK; ++s)
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[s], qf[t][s], acc, 0, 0, 0);
+          if (all != 0xffffu) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (!((live >> e) & 1u)) acc[e] = a.scale2 < 0.0f ? __builtin_inff() : -__builtin_inff();
+          }
+          float y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = fmaf(acc[e], a.scale2, -m[t]);
+          const float over = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+          if (__any(over > kLazy)) {
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = acc[e] * a.scale2;
+            const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+            if (top > m[t] + kLazy) {
+              l[t] *= exp2_fast(m[t] - top);
+              m[t] = top;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = fmaf(acc[e], a.scale2, -m[t]);
+          }
+          l[t] += (exp2_fast(y[0]) + exp2_fast(y[1])) + (exp2_fast(y[2]) + exp2_fast(y[3]));
+        }
+        stage = stage == kMassRing - 1 ? 0 : stage + 1;
+      }
+#pragma unroll
+      for (int t = 0; t < PT; ++t) {
+        float2 p = make_float2(m[t], l[t]);
+        p = join(p, make_float2(__shfl_xor(p.x, 16), __shfl_xor(p.y, 16)));
+        p = join(p, make_float2(__shfl_xor(p.x, 32), __shfl_xor(p.y, 32)));
+        if (grp == 0) red[wave * PT * 16 + t * 16 + col] = p;
+      }
+      __syncthreads();
+      for (int r = tid; r < PT * 16; r += kMassThreads) {
+        float2 p = red[r];
+#pragma unroll
+        for (int w = 1; w < kMassWaves; ++w) p = join(p, red[w * PT * 16 + r]);
+        if constexpr (MODE == 0) {
+          if (r < nt * 16) a.part[((int64_t)q * a.nsplit + split) * (T * 16) + c0 * 16 + r] = p;
+        } else {
+          ms[r] = p.x;
+          rs[r] = (r >> 4) >= nt || ht.head(c0 + (r >> 4), r & 15) < 0 || p.y == 0.0f ? 0.0f : 1.0f / p.y;
+        }
+      }
+      __syncthreads();
+    }
+
+    if constexpr (MODE != 0) {
+      HK_WAIT_VM(0);
+      // Blocks from the last to the first; after the statistics of the same pass the last
+      // kMassRing of them still lie in the ring, block i in stage i % kMassRing.
+      int stage = mine ? (mine - 1) % kMassRing : 0;
+      int next = mine - 1;  // the next block to fetch
+      if constexpr (MODE == 2) next = max(-1, mine - 1 - kMassRing);
+      if constexpr (MODE == 1) {
+        for (int s = 0, st = stage; s < kMassRing - 1 && next >= 0; ++s, --next) {
+          issue(next, g, st);
+          st = st == 0 ? kMassRing - 1 : st - 1;
+        }
+      }
+      for (int i = mine - 1; i >= 0; --i) {
+        if constexpr (MODE == 1) {
+          if (next >= 0) {
+            issue(next, g, stage == kMassRing - 1 ? 0 : stage + 1);
+            --next;
+          }
+          await(min(kMassRing - 1, i));
+        } else {
+          await(min(kMassRing - 1, max(0, i - (next + 1))));
+        }
+        bf16x8 f[NK];
+        frags(stage, f);
+        if constexpr (MODE == 2) {
+          if (next >= 0) {  // this stage has been read: the block kMassRing before this one goes there
+            issue(next, g, stage);
+            --next;
+          }
+        }
+        float o = 0.0f;
+#pragma unroll
+        for (int t = 0; t < PT; ++t) {
+          f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int s = 0; s < NK; ++s)
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qf[t][s], f[s], acc, 0, 0, 0);
+          const f32x4 m = *reinterpret_cast<const f32x4*>(ms + t * 16 + 4 * grp);
+          const f32x4 r = *reinterpret_cast<const f32x4*>(rs + t * 16 + 4 * grp);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o = fmaf(exp2_fast(fmaf(acc[e], a.scale2, -m[e])), r[e], o);
+        }
+        o += __shfl_xor(o, 16);
+        o += __shfl_xor(o, 32);
+        const int j = (wave + i * kMassWaves) * 16 + col;
+        if (grp == 0) sums[j] = ids[j] >= 0 ? (c0 ? sums[j] + o : o) : 0.0f;
+        stage = stage == 0 ? kMassRing - 1 : stage - 1;
+      }
+      if (last) {
+        __syncthreads();
+        for (int j = tid; j < nj; j += kMassThreads)
+          a.mass[(int64_t)q * a.topk + j0 + j] = sums[j] * a.inv_heads;
+      }
+    }
+    c0 += nt;
+    ta += nt;
+    if (ta == ht.tiles) { ta = 0; ++g; }
+    if (!last) __syncthreads();
+  }
+}
+
+template <int NK, int PT, int MODE>
+hipError_t mass_staged_launch(const MassArgs& a, hipStream_t s) {
+  static LdsLimit lim;
+  const int lds = kMassRing * kMassWaves * 16 * NK * 64 + PT * 16 * (8 + 8 * kMassWaves) + a.split_len * 8;
+  hipError_t e = raise_dynamic_lds((const void*)mass_staged_kernel<NK, PT, MODE>, lds, lim);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((mass_staged_kernel<NK, PT, MODE>), dim3((unsigned)a.n, (unsigned)a.nsplit),
+                     dim3(kMassThreads), (size_t)lds, s, a);
+  return hipGetLastError();
+}
+
+template <int NK, int PT>
+hipError_t mass_staged_pt(const MassArgs& a, hipStream_t s) {
+  if (a.lse) return mass_staged_launch<NK, PT, 1>(a, s);
+  if (a.nsplit == 1) return mass_staged_launch<NK, PT, 2>(a, s);
+  hipError_t e = mass_staged_launch<NK, PT, 0>(a, s);
+  return e != hipSuccess ? e : mass_staged_launch<NK, PT, 1>(a, s);
+}
+
+// Tiles of a pass: those of a key head, up to four (q rows in 16 NK registers a tile).
+template <int NK>
+hipError_t mass_staged(const MassArgs& a, hipStream_t s) {
+  const int tiles = HeadTiles(a.heads, a.groups).tiles;
+  if (tiles == 1) return mass_staged_pt<NK, 1>(a, s);
+  if (tiles == 2) return mass_staged_pt<NK, 2>(a, s);
+  if (tiles == 3) return mass_staged_pt<NK, 3>(a, s);
+  return mass_staged_pt<NK, 4>(a, s);
+}
+
 template <int NK, int MODE>
 hipError_t mass_launch(const MassArgs& a, hipStream_t s) {
   static LdsLimit lim;
@@ -307,9 +578,9 @@ bool mass_supports(int d) {
 hipError_t launch_attention_mass(const MassArgs& a, int d, hipStream_t s) {
   if (a.n <= 0) return hipSuccess;
   switch (d) {
-    case 64: return mass_d<2>(a, s);
+    case 64: return mass_staged<2>(a, s);
     case 96: return mass_d<3>(a, s);
-    case 128: return mass_d<4>(a, s);
+    case 128: return mass_staged<4>(a, s);
     case 192: return mass_d<6>(a, s);
     case 256: return mass_d<8>(a, s);
     case 512: return mass_d<16>(a, s);
