@@ -486,15 +486,19 @@ _LAYOUTS = {"half": 0, "interleaved": 1}
 _SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 
-def _on(t):
-    """Makes the tensor's GPU the current one for a launch."""
-    import contextlib
-
+def _launch(device, fn, *args) -> None:
+    """Calls fn(*args, stream) on the device's current stream, with that device
+    current (a call's host time is most of a small operator's, so nothing here
+    builds a stream or a guard object that is not needed)."""
     import torch
-    dev = t.device
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+    index = device.index
+    if index == torch.cuda.current_device():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if rc != 0:
+        _check(rc)
 
 
 def _gpu(t, name: str) -> None:
@@ -505,14 +509,20 @@ def _gpu(t, name: str) -> None:
 def _rows_array(t, name: str):
     """[n][d] or [n][heads][d] rows of bf16 or fp32, any strides but the last."""
     import torch
-    if t.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
-    if t.dim() not in (2, 3):
+    dtype, stride = t.dtype, t.stride()
+    if dtype != torch.bfloat16 and dtype != torch.float32:
+        raise TypeError(f"{name} must be bfloat16 or float32, got {dtype}")
+    axes = len(stride)
+    if axes != 2 and axes != 3:
         raise ValueError(f"{name} must be [n][d] or [n][heads][d], got {tuple(t.shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if stride[-1] != 1 and t.shape[-1] > 1:
         raise ValueError(f"the last axis of {name} must be contiguous")
-    return RowsArray(t.data_ptr(), t.stride(0), t.stride(1) if t.dim() == 3 else 0,
-                     0 if t.dtype == torch.bfloat16 else 1, 0)
+    return RowsArray(t.data_ptr(), stride[0], stride[1] if axes == 3 else 0,
+                     0 if dtype == torch.bfloat16 else 1, 0)
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
 
 
 def _ints(t, name: str, n: int, device) -> None:
@@ -555,7 +565,7 @@ def _plan(rot, device):
         return None
     if rot.freq.device != device:
         raise ValueError(f"the rotary plan is on {rot.freq.device}, the rows on {device}")
-    return ctypes.byref(rot._plan)
+    return rot._plan
 
 
 def rotary(x, rot: Rotary, *, q_start: int = 0, q_pos=None, backward: bool = False, out=None,
@@ -568,18 +578,17 @@ def rotary(x, rot: Rotary, *, q_start: int = 0, q_pos=None, backward: bool = Fal
     lib = _LIB or load_library()
     _gpu(x, "x")
     xa = _rows_array(x, "x")
-    n, d = x.shape[0], x.shape[-1]
-    heads = x.shape[1] if x.dim() == 3 else 1
+    shape, device = x.shape, x.device
+    n, d = shape[0], shape[-1]
+    heads = shape[1] if len(shape) == 3 else 1
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+        out = x.new_empty(shape, dtype=out_dtype)
     elif out.shape != x.shape or out.device != x.device or out_dtype not in (None, out.dtype):
         raise ValueError(f"out must have x's shape {tuple(x.shape)} and device, and out_dtype")
     ya = _rows_array(out, "out")
-    _ints(q_pos, "q_pos", n, x.device)
-    with _on(x):
-        _check(lib.hytopk_rotary(_plan(rot, x.device), n, heads, d, ctypes.byref(xa),
-                                 ctypes.byref(ya), _ptr(q_pos), int(q_start), 1 if backward else 0,
-                                 _stream(x)))
+    _ints(q_pos, "q_pos", n, device)
+    _launch(device, lib.hytopk_rotary, _plan(rot, device), n, heads, d, xa, ya, _address(q_pos),
+            int(q_start), 1 if backward else 0)
     return out
 
 
@@ -589,27 +598,30 @@ def _cache(codes, scale, fmt):
     import torch
     _gpu(codes, "codes")
     code = _dtype_code(codes, fmt)
-    if codes.dim() not in (2, 3):
-        raise ValueError(f"codes must be [L][d] or [L][heads][d], got {tuple(codes.shape)}")
+    shape = codes.shape
+    axes = len(shape)
+    if axes != 2 and axes != 3:
+        raise ValueError(f"codes must be [L][d] or [L][heads][d], got {tuple(shape)}")
     if not codes.is_contiguous():
         raise ValueError("codes must be contiguous")
-    want = {BF16: (torch.bfloat16,), FP8_E4M3: (torch.uint8, torch.float8_e4m3fn)}.get(
-        code, (torch.uint8,))
-    if codes.dtype not in want:
-        raise ValueError(f"codes of this format must be {want[0]}, got {codes.dtype}")
-    L, last = codes.shape[0], codes.shape[-1]
-    heads = codes.shape[1] if codes.dim() == 3 else 1
+    dtype = codes.dtype
+    if dtype != (torch.bfloat16 if code == BF16 else torch.uint8) and not (
+            code == FP8_E4M3 and dtype == torch.float8_e4m3fn):
+        raise ValueError(f"codes of type {dtype} do not hold this format")
+    L, last = shape[0], shape[-1]
+    heads = shape[1] if axes == 3 else 1
     d = 2 * last if code == MXFP4_E2M1 else last
     if code == BF16:
         if scale is not None:
             raise ValueError("a bf16 cache takes no scale")
-    elif scale is None:
+        return Cache(codes.data_ptr(), None, L, heads, d, code, 0)
+    if scale is None:
         raise ValueError("fp8 and MX caches need scale")
-    elif code == FP8_E4M3:
+    if code == FP8_E4M3:
         _need(scale, "scale", (L,), torch.float32, codes.device)
     else:
-        _need(scale, "scale", tuple(codes.shape[:-1]) + (d // 32,), torch.uint8, codes.device)
-    return Cache(codes.data_ptr(), None if scale is None else scale.data_ptr(), L, heads, d, code, 0)
+        _need(scale, "scale", (*shape[:-1], d // 32), torch.uint8, codes.device)
+    return Cache(codes.data_ptr(), scale.data_ptr(), L, heads, d, code, 0)
 
 
 def cache_write_workspace_bytes(codes, scale, n: int, *, fmt=None) -> int:
@@ -631,23 +643,22 @@ def cache_write(x, codes, scale=None, *, fmt=None, start: int = 0, slots=None, r
     c = _cache(codes, scale, fmt)
     xa = _rows_array(x, "x")
     n = x.shape[0]
-    if x.device != codes.device:
-        raise ValueError(f"x is on {x.device}, the cache on {codes.device}")
-    if x.shape[-1] != c.d or (x.shape[1] if x.dim() == 3 else 1) != c.heads:
-        raise ValueError(f"x {tuple(x.shape)} does not fit cache rows of {c.heads} x {c.d}")
-    _ints(slots, "slots", n, x.device)
-    _ints(q_pos, "q_pos", n, x.device)
-    with _on(x):
-        if workspace is None and slots is not None:
-            need = int(lib.hytopk_cache_write_workspace(ctypes.byref(c), n, 1))
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-        if workspace is not None:
-            _workspace(workspace, x.device)
-        _check(lib.hytopk_cache_write(ctypes.byref(c), n, ctypes.byref(xa), _ptr(slots), int(start),
-                                      _plan(rotary, x.device), _ptr(q_pos), int(q_start),
-                                      _ptr(workspace),
-                                      0 if workspace is None else workspace.numel(), _stream(x)))
+    device, shape = x.device, x.shape
+    if device != codes.device:
+        raise ValueError(f"x is on {device}, the cache on {codes.device}")
+    if shape[-1] != c.d or (shape[1] if len(shape) == 3 else 1) != c.heads:
+        raise ValueError(f"x {tuple(shape)} does not fit cache rows of {c.heads} x {c.d}")
+    _ints(slots, "slots", n, device)
+    _ints(q_pos, "q_pos", n, device)
+    if workspace is None and slots is not None:
+        need = lib.hytopk_cache_write_workspace(c, n, 1)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    if workspace is not None:
+        _workspace(workspace, device)
+    _launch(device, lib.hytopk_cache_write, c, n, xa, _address(slots), int(start),
+            _plan(rotary, device), _address(q_pos), int(q_start), _address(workspace),
+            0 if workspace is None else workspace.numel())
 
 
 def quantize(x, fmt: str, *, rotary=None, q_start: int = 0, q_pos=None):
@@ -685,16 +696,18 @@ def cache_read(codes, scale=None, *, fmt=None, slots=None, start: int = 0, count
         raise ValueError(f"count {count} differs from the {n} slots")
     _ints(slots, "slots", n, codes.device)
     shape = (n, c.d) if codes.dim() == 2 else (n, c.heads, c.d)
+    device = codes.device
     if out is None:
         if n < 0:
             raise ValueError("start lies behind the cache")
-        out = torch.empty(shape, dtype=dtype or torch.bfloat16, device=codes.device)
-    _need(out, "out", shape, dtype or out.dtype, codes.device)
-    if out.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"rows are read as bfloat16 or float32, got {out.dtype}")
-    with _on(codes):
-        _check(lib.hytopk_cache_read(ctypes.byref(c), n, _ptr(slots), int(start), _ptr(out),
-                                     0 if out.dtype == torch.bfloat16 else 1, _stream(codes)))
+        out = codes.new_empty(shape, dtype=dtype or torch.bfloat16)
+    else:
+        _need(out, "out", shape, dtype or out.dtype, device)
+    dtype = out.dtype
+    if dtype != torch.bfloat16 and dtype != torch.float32:
+        raise TypeError(f"rows are read as bfloat16 or float32, got {dtype}")
+    _launch(device, lib.hytopk_cache_read, c, n, _address(slots), int(start), out.data_ptr(),
+            0 if dtype == torch.bfloat16 else 1)
     return out
 
 
@@ -705,15 +718,18 @@ def _attention(q, k, idx, softmax_scale) -> Attention:
     import torch
     if q.dim() != 3 or k.dim() not in (2, 3) or k.shape[-1] != q.shape[-1]:
         raise ValueError("shapes must be q [n][heads][d], k [L][key_heads][d] or [L][d]")
+    device = q.device
     for t, name in ((q, "q"), (k, "k")):
-        if t.dtype != torch.bfloat16 or not t.is_cuda or not t.is_contiguous() or t.device != q.device:
+        if t.dtype != torch.bfloat16 or not t.is_cuda or not t.is_contiguous() or t.device != device:
             raise ValueError(f"{name} must be contiguous bfloat16 on one GPU")
     n, heads, d = q.shape
+    rows = k.shape
     if idx.dim() != 2:
         raise ValueError("idx must be [n][k]")
-    _need(idx, "idx", (n, idx.shape[1]), torch.int32, q.device)
+    count = idx.shape[1]
+    _need(idx, "idx", (n, count), torch.int32, device)
     scale = d ** -0.5 if softmax_scale is None else float(softmax_scale)
-    return Attention(k.shape[0], n, heads, k.shape[1] if k.dim() == 3 else 1, d, idx.shape[1], scale, 0)
+    return Attention(rows[0], n, heads, rows[1] if len(rows) == 3 else 1, d, count, scale, 0)
 
 
 def attention_mass_workspace_bytes(q, k, idx) -> int:
@@ -731,20 +747,21 @@ def attention_mass(q, k, idx, *, softmax_scale=None, lse=None, workspace=None, o
     import torch
     lib = _LIB or load_library()
     p = _attention(q, k, idx, softmax_scale)
+    device = q.device
     if lse is not None:
-        _need(lse, "lse", (p.n, p.heads), torch.float32, q.device)
+        _need(lse, "lse", (p.n, p.heads), torch.float32, device)
     if out is None:
-        out = torch.empty((p.n, p.k), dtype=torch.float32, device=q.device)
-    _need(out, "out", (p.n, p.k), torch.float32, q.device)
-    with _on(q):
-        if workspace is None and lse is None:
-            need = int(lib.hytopk_attention_mass_workspace(ctypes.byref(p)))
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
-        if workspace is not None:
-            _workspace(workspace, q.device)
-        _check(lib.hytopk_attention_mass(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(idx), _ptr(lse),
-                                         _ptr(out), _ptr(workspace),
-                                         0 if workspace is None else workspace.numel(), _stream(q)))
+        out = q.new_empty((p.n, p.k), dtype=torch.float32)
+    else:
+        _need(out, "out", (p.n, p.k), torch.float32, device)
+    if workspace is None and lse is None:
+        workspace = torch.empty(max(lib.hytopk_attention_mass_workspace(p), 1), dtype=torch.uint8,
+                                device=device)
+    if workspace is not None:
+        _workspace(workspace, device)
+    _launch(device, lib.hytopk_attention_mass, p, q.data_ptr(), k.data_ptr(), idx.data_ptr(),
+            _address(lse), out.data_ptr(), _address(workspace),
+            0 if workspace is None else workspace.numel())
     return out
 
 
@@ -767,15 +784,14 @@ def index_loss(score, mass, *, weight=None, want=("loss", "d_score"), out=None):
     if weight is not None:
         _need(weight, "weight", (n,), torch.float32, dev)
     if out is None:
-        loss = torch.empty(n, dtype=torch.float32, device=dev) if "loss" in want else None
-        grad = torch.empty((n, k), dtype=torch.float32, device=dev) if "d_score" in want else None
+        loss = score.new_empty(n) if "loss" in want else None
+        grad = torch.empty_like(score) if "d_score" in want else None
     else:
         loss, grad = out
         if loss is not None:
             _need(loss, "out[0] (loss)", (n,), torch.float32, dev)
         if grad is not None:
             _need(grad, "out[1] (d_score)", (n, k), torch.float32, dev)
-    with _on(score):
-        _check(lib.hytopk_index_loss(n, k, _ptr(score), _ptr(mass), _ptr(weight), _ptr(loss),
-                                     _ptr(grad), _stream(score)))
+    _launch(dev, lib.hytopk_index_loss, n, k, score.data_ptr(), mass.data_ptr(), _address(weight),
+            _address(loss), _address(grad))
     return loss, grad

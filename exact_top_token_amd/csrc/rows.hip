@@ -97,15 +97,35 @@ __device__ __forceinline__ void store1(void* base, int64_t at, float v) {
 
 // ------------------------------------------------------------- rotation
 
+// Cosine and sine of t turns, |t| <= 1/2: the nearest quarter turn k is taken
+// off exactly, the rest |x| <= pi/4 goes through the Taylor series to x^9 and x^8
+// (truncated below 2e-9 and 3e-8), and k swaps and signs the two.
+__device__ __forceinline__ float2 turn_cos_sin(float t) {
+  const float k = rintf(4.0f * t);
+  const float x = fmaf(k, -0.25f, t) * 6.28318530717958648f;
+  const float z = x * x;
+  float s = fmaf(z, 1.0f / 362880.0f, -1.0f / 5040.0f);
+  s = fmaf(z, s, 1.0f / 120.0f);
+  s = fmaf(z, s, -1.0f / 6.0f);
+  s = fmaf(z * s, x, x);
+  float c = fmaf(z, 1.0f / 40320.0f, -1.0f / 720.0f);
+  c = fmaf(z, c, 1.0f / 24.0f);
+  c = fmaf(z, c, -0.5f);
+  c = fmaf(z, c, 1.0f);
+  const int q = (int)k;  // -2 .. 2
+  const float cc = q & 1 ? s : c, ss = q & 1 ? c : s;
+  return make_float2(__uint_as_float(__float_as_uint(cc) ^ (((unsigned)(q + 1) & 2u) << 30)),
+                     __uint_as_float(__float_as_uint(ss) ^ (((unsigned)q & 2u) << 30)));
+}
+
 // gain * (cos, sign * sin) of pos * f.  The angle in turns is formed and
 // reduced to [-1/2, 1/2] in 64 bits: at 2^31 positions its error is below
 // 1e-7 turns, at 2^20 below 1e-10, where 32 bits would keep none of it.
 __device__ __forceinline__ float2 rot_entry(const RotArgs& r, int i, int64_t pos) {
   double t = (double)pos * (r.freq[i] * 0.15915494309189533577);
   t -= rint(t);
-  float s, c;
-  sincospif(2.0f * (float)t, &s, &c);
-  return make_float2(c * r.gain, s * (r.gain * r.sign));
+  const float2 f = turn_cos_sin((float)t);
+  return make_float2(f.x * r.gain, f.y * (r.gain * r.sign));
 }
 
 // One half of a rotated pair: v cos -+ w sin.  Written as one product and one fused
@@ -114,11 +134,22 @@ __device__ __forceinline__ float2 rot_entry(const RotArgs& r, int i, int64_t pos
 __device__ __forceinline__ float rot_lo(float v, float w, float2 f) { return fmaf(v, f.x, -(w * f.y)); }
 __device__ __forceinline__ float rot_hi(float v, float w, float2 f) { return fmaf(v, f.x, w * f.y); }
 
-// The entries of tokens t0 .. t0 + nt - 1, once for all their heads: [nt][dim/2].
-__device__ __forceinline__ void rot_table(const RotArgs& r, int t0, int nt, float2* cs) {
+// u / by for u * by < 2^22 (the error of the rounded-up reciprocal stays below 1 / by).
+struct SmallDiv {
+  unsigned by, mul;
+  __host__ SmallDiv(unsigned d) : by(d), mul(((1u << 22) + d - 1) / d) {}
+  __device__ __forceinline__ unsigned operator()(unsigned u) const {
+    return (unsigned)(((uint64_t)u * mul) >> 22);
+  }
+};
+
+// The entries of tokens t0 .. t0 + nt - 1, once for all their heads: [nt][dim/2]
+// (at most 2,048 entries, or one token's).
+__device__ __forceinline__ void rot_table(const RotArgs& r, int64_t t0, int nt, float2* cs) {
   const int half = r.dim >> 1;
+  const unsigned mul = ((1u << 22) + half - 1) / half;
   for (int e = threadIdx.x; e < nt * half; e += blockDim.x) {
-    const int t = e / half, i = e - t * half;
+    const int t = (int)(((uint64_t)e * mul) >> 22), i = e - t * half;
     const int64_t pos = r.pos ? (int64_t)r.pos[t0 + t] : r.pos0 + t0 + t;
     cs[e] = rot_entry(r, i, pos);
   }
@@ -281,13 +312,11 @@ hipError_t launch_rotary(const RotaryArgs& a, int in_dtype, int out_dtype, hipSt
 
 namespace {
 
-// Four values, clamped to +-448, as E4M3 bytes (to nearest, ties to even).
+typedef short short2v __attribute__((ext_vector_type(2)));
+
+// Four values of at most 448 (or what rounds to it) as E4M3 bytes, to nearest, ties to even.
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  a = fminf(fmaxf(a, -448.0f), 448.0f);
-  b = fminf(fmaxf(b, -448.0f), 448.0f);
-  c = fminf(fmaxf(c, -448.0f), 448.0f);
-  d = fminf(fmaxf(d, -448.0f), 448.0f);
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
 }
 
@@ -320,14 +349,6 @@ __device__ __forceinline__ uint32_t e4m3x4_quotient(const float* x, float scale,
   return e4m3x4(q[0], q[1], q[2], q[3]);
 }
 
-// E2M1 code of v: magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6 (codes 0..7), to
-// nearest, ties to the even code, saturating at 6; bit 3 is the sign.
-__device__ __forceinline__ uint32_t e2m1(float v) {
-  const float a = fminf(fabsf(v), 6.0f);
-  const float c = a < 2.0f ? rintf(2.0f * a) : (a < 4.0f ? rintf(a) + 2.0f : rintf(0.5f * a) + 4.0f);
-  return (uint32_t)c | ((__float_as_uint(v) >> 31) << 3);
-}
-
 // Rotated values of elements e0 .. e0 + 7 of a head (v holds them unrotated;
 // `at` is the head's offset in x, cs the token's entries).
 template <int IN, bool VEC>
@@ -342,10 +363,11 @@ __device__ __forceinline__ void rotate8(const RotArgs& r, const void* x, int64_t
       const float2* c = cs + (lo ? e : e - half);
       float w[8];
       load8<IN, true>(x, at + e0 + (lo ? half : -half), w);  // the partners, in cache by now
+      const float side = lo ? -1.0f : 1.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 8; ++i) {  // rot_lo or rot_hi: the product's sign
         const float2 f = c[i];
-        v[i] = lo ? rot_lo(v[i], w[i], f) : rot_hi(v[i], w[i], f);
+        v[i] = fmaf(v[i], f.x, (w[i] * side) * f.y);
       }
     } else {
       const float2* c = cs + (e >> 1);
@@ -371,125 +393,155 @@ __device__ __forceinline__ void rotate8(const RotArgs& r, const void* x, int64_t
   }
 }
 
+// How the rows of a write lie on threads: P = 1 << log_p threads take a row, a
+// workgroup takes `rounds` times 256 / P rows at once.
+struct WriteGrid {
+  int log_p;
+  int rounds;
+  SmallDiv head;  // chunks of eight elements of a head
+};
+
+constexpr int kWriteEntries = 2048;  // cosines and sines of a workgroup's rows
+
 // Rows written into a cache.  P threads (a power of two, 4..256) take a row in
 // chunks of eight elements, K chunks each, so a row is read once and its
 // scale comes from registers: a lane reduction over the row (FP8), or over the four
 // lanes of a 32-element block (MX).
 template <int IN, int FMT, int K, bool VEC>
 __global__ void __launch_bounds__(kRowThreads)
-cache_write_kernel(CacheWriteArgs a, int log_p) {
-  __shared__ float2 cs[1024];
-  __shared__ float red[kRowThreads / kWave];
+cache_write_kernel(CacheWriteArgs a, WriteGrid g) {
+  __shared__ float2 cs[kWriteEntries];
+  __shared__ float red[2][kRowThreads / kWave];
   __shared__ int later[kRowThreads / 4];
-  const int P = 1 << log_p, RB = kRowThreads >> log_p;
+  const int log_p = g.log_p, P = 1 << log_p, RB = kRowThreads >> log_p;
   const int rl = threadIdx.x >> log_p, lr = threadIdx.x & (P - 1);
-  const int chunks = a.heads * a.d / 8;
-  for (int64_t tile = blockIdx.x; tile * RB < a.n; tile += gridDim.x) {
-    const int i0 = (int)(tile * RB);
-    const int i = rl < a.n - i0 ? i0 + rl : a.n;
-    const bool have = i < a.n;
-    if (tile != blockIdx.x) __syncthreads();  // LDS of the last rows is read
-
-    float v[K][8];
+  const int chunks = a.heads * g.head.by, half = a.rot.dim >> 1;
+  int64_t at[K];  // the chunk's head in a row of x
+  int e0[K];      // and its first element there
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = lr + k * P;
-      if (have && c < chunks) {
-        const int h = a.heads == 1 ? 0 : c * 8 / a.d, e0 = c * 8 - h * a.d;
-        load8<IN, VEC>(a.x, (int64_t)i * a.ts + (int64_t)h * a.hs + e0, v[k]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[k][j] = 0.0f;
-      }
-    }
-
-    // The row's place; -1 where nothing is written.
-    int64_t row = -1;
-    if (have) {
-      row = a.slots ? (int64_t)a.slots[i] : a.start + i;
-      if (row >= a.L || row < 0) row = -1;
-      if (row >= 0 && a.claim && a.claim[row] != i) row = -1;
-    }
-    if (a.slots && !a.claim) {  // few rows: look for a later row of the same slot
-      for (int t = threadIdx.x; t < RB; t += kRowThreads) later[t] = 0;
-      __syncthreads();
-      if (row >= 0) {
-        bool dup = false;
-        for (int j = i + 1 + lr; j < a.n; j += P) dup |= (int64_t)a.slots[j] == row;
-        if (dup) later[rl] = 1;
-      }
-      __syncthreads();
-      if (later[rl]) row = -1;
-    }
-
+  for (int k = 0; k < K; ++k) {
+    const unsigned c = (unsigned)(lr + k * P), h = g.head(c);
+    at[k] = (int64_t)h * a.hs;
+    e0[k] = (int)(c - h * g.head.by) * 8;
+  }
+  int flip = 0;
+  for (int64_t i0 = (int64_t)blockIdx.x * RB * g.rounds; i0 < a.n; i0 += (int64_t)gridDim.x * RB * g.rounds) {
+    const int tile = (int)min((int64_t)RB * g.rounds, a.n - i0);
     if (a.rot.freq) {
-      rot_table(a.rot, i0, min(RB, a.n - i0), cs);
+      __syncthreads();  // the last rows' entries are read
+      rot_table(a.rot, i0, tile, cs);
       __syncthreads();
-      const float2* my = cs + rl * (a.rot.dim >> 1);
+    }
+    for (int r0 = 0; r0 < tile; r0 += RB) {
+      const bool have = r0 + rl < tile;
+      const int64_t i = i0 + r0 + rl;
+      float v[K][8];
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (have && lr + k * P < chunks) {
+          load8<IN, VEC>(a.x, i * a.ts + at[k] + e0[k], v[k]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[k][j] = 0.0f;
+        }
+      }
+
+      // The row's place; -1 where nothing is written.
+      int64_t row = -1;
+      if (have) {
+        row = a.slots ? (int64_t)a.slots[i] : a.start + i;
+        if (row >= a.L || row < 0) row = -1;
+        if (row >= 0 && a.claim && a.claim[row] != i) row = -1;
+      }
+      if (a.slots && !a.claim) {  // few rows: look for a later row of the same slot
+        __syncthreads();
+        for (int t = threadIdx.x; t < RB; t += kRowThreads) later[t] = 0;
+        __syncthreads();
+        if (row >= 0) {
+          bool dup = false;
+          for (int j = (int)i + 1 + lr; j < a.n; j += P) dup |= (int64_t)a.slots[j] == row;
+          if (dup) later[rl] = 1;
+        }
+        __syncthreads();
+        if (later[rl]) row = -1;
+      }
+
+      if (a.rot.freq && have) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          if (lr + k * P < chunks)
+            rotate8<IN, VEC>(a.rot, a.x, i * a.ts + at[k], e0[k], cs + (r0 + rl) * half, v[k]);
+      }
+
+      float scale = 1.0f, inv = 1.0f;
+      if constexpr (FMT == kFP8) {
+        float m = 0.0f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[k][j]));
+        for (int off = min(P, kWave) >> 1; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+        if (P > kWave) {  // uniform over the launch
+          float* now = red[flip];  // the other half is read by waves still in the last round
+          flip ^= 1;
+          if (lane_id() == 0) now[threadIdx.x >> 6] = m;
+          __syncthreads();
+          const int w0 = rl * (P / kWave);
+          for (int w = 0; w < P / kWave; ++w) m = fmaxf(m, now[w0 + w]);
+        }
+        scale = m > 0.0f ? fmaxf(m / 448.0f, 0x1p-126f) : 1.0f;
+        inv = 1.0f / scale;
+        if (row >= 0 && lr == 0) static_cast<float*>(a.scale)[row] = scale;
+      }
+
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const int c = lr + k * P;
-        if (have && c < chunks) {
-          const int h = a.heads == 1 ? 0 : c * 8 / a.d, e0 = c * 8 - h * a.d;
-          rotate8<IN, VEC>(a.rot, a.x, (int64_t)i * a.ts + (int64_t)h * a.hs, e0, my, v[k]);
+        int e = 0;
+        if constexpr (FMT == kMXFP8 || FMT == kMXFP4) {
+          float m = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[k][j]));
+          m = fmaxf(m, __shfl_xor(m, 1));
+          m = fmaxf(m, __shfl_xor(m, 2));
+          // floor(log2(m)) - emax, clamped; frexp's exponent is floor(log2(m)) + 1
+          const int x = __builtin_amdgcn_frexp_expf(m) - 1 - (FMT == kMXFP8 ? 8 : 2);
+          e = m > 0.0f ? max(-127, min(127, x)) : -127;
         }
-      }
-    }
-
-    float scale = 1.0f, inv = 1.0f;
-    if constexpr (FMT == kFP8) {
-      float m = 0.0f;
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[k][j]));
-      for (int off = min(P, kWave) >> 1; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
-      if (P > kWave) {  // uniform over the launch
-        if (lane_id() == 0) red[threadIdx.x >> 6] = m;
-        __syncthreads();
-        const int w0 = rl * (P / kWave);
-        for (int w = 0; w < P / kWave; ++w) m = fmaxf(m, red[w0 + w]);
-      }
-      scale = m > 0.0f ? fmaxf(m / 448.0f, 0x1p-126f) : 1.0f;
-      inv = 1.0f / scale;
-      if (row >= 0 && lr == 0) static_cast<float*>(a.scale)[row] = scale;
-    }
-
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = lr + k * P;
-      int e = 0;
-      if constexpr (FMT == kMXFP8 || FMT == kMXFP4) {
-        float m = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[k][j]));
-        m = fmaxf(m, __shfl_xor(m, 1));
-        m = fmaxf(m, __shfl_xor(m, 2));
-        int x;
-        (void)frexpf(m, &x);  // floor(log2(m)) + 1
-        e = m > 0.0f ? max(-127, min(127, x - 1 - (FMT == kMXFP8 ? 8 : 2))) : -127;
-      }
-      if (row < 0 || c >= chunks) {
-        // nothing to write
-      } else if constexpr (FMT == kBF16) {
-        store8<kRowsBF16>(a.codes, (row * chunks + c) * 8, v[k]);
-      } else if constexpr (FMT == kFP8) {
-        const u32x2 w = {e4m3x4_quotient(v[k], scale, inv), e4m3x4_quotient(v[k] + 4, scale, inv)};
-        *reinterpret_cast<u32x2*>(a.codes + (row * chunks + c) * 8) = w;
-      } else {
-        if ((lr & 3) == 0)
-          static_cast<uint8_t*>(a.scale)[(row * chunks + c) >> 2] = (uint8_t)(e + 127);
-        float y[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = ldexpf(v[k][j], -e);
-        if constexpr (FMT == kMXFP8) {
-          const u32x2 w = {e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7])};
+        if (row < 0 || c >= chunks) {
+          // nothing to write
+        } else if constexpr (FMT == kBF16) {
+          store8<kRowsBF16>(a.codes, (row * chunks + c) * 8, v[k]);
+        } else if constexpr (FMT == kFP8) {
+          const u32x2 w = {e4m3x4_quotient(v[k], scale, inv), e4m3x4_quotient(v[k] + 4, scale, inv)};
           *reinterpret_cast<u32x2*>(a.codes + (row * chunks + c) * 8) = w;
         } else {
-          uint32_t w = 0;
+          if ((lr & 3) == 0)
+            static_cast<uint8_t*>(a.scale)[(row * chunks + c) >> 2] = (uint8_t)(e + 127);
+          // the conversions divide by this: the scale's exponent in an fp32
+          const float by = __uint_as_float((unsigned)(e + 127) << 23);
+          if constexpr (FMT == kMXFP8) {
+            const float top = ldexpf(448.0f, e);
+            u32x2 w;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) w |= e2m1(y[j]) << (4 * j);
-          *reinterpret_cast<uint32_t*>(a.codes + (row * chunks + c) * 4) = w;
+            for (int p = 0; p < 2; ++p) {
+              float y[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) y[j] = __builtin_amdgcn_fmed3f(v[k][4 * p + j], -top, top);
+              short2v t = {0, 0};
+              t = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(t, y[0], y[1], by, false);
+              t = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(t, y[2], y[3], by, true);
+              w[p] = __builtin_bit_cast(uint32_t, t);
+            }
+            *reinterpret_cast<u32x2*>(a.codes + (row * chunks + c) * 8) = w;
+          } else {  // saturates by itself
+            uint32_t w = 0;
+            w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[k][0], v[k][1], by, 0);
+            w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[k][2], v[k][3], by, 1);
+            w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[k][4], v[k][5], by, 2);
+            w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[k][6], v[k][7], by, 3);
+            *reinterpret_cast<uint32_t*>(a.codes + (row * chunks + c) * 4) = w;
+          }
         }
       }
     }
@@ -513,16 +565,21 @@ hipError_t cache_write_fmt(const CacheWriteArgs& a, bool vec, hipStream_t s) {
   const int chunks = a.heads * a.d / 8;
   int log_p = 2;
   while ((1 << log_p) < chunks && log_p < 8) ++log_p;
-  const int per = (chunks + (1 << log_p) - 1) >> log_p;
   const int rb = kRowThreads >> log_p;
-  const dim3 grid(row_blocks(a.n, rb)), block(kRowThreads);
+  // Rounds share the set-up and the entries of a workgroup's rows; as many (up to
+  // four) as leave 2,048 workgroups and fit the table.
+  int rounds = 1;
+  const int fit = a.rot.freq ? kWriteEntries / (rb * (a.rot.dim / 2)) : 4;
+  while (rounds < 4 && 2 * rounds <= fit && a.n / ((int64_t)rb * 2 * rounds) >= 2048) rounds *= 2;
+  const WriteGrid g{log_p, rounds, SmallDiv((unsigned)a.d / 8)};
+  const dim3 grid(row_blocks(a.n, rb * rounds)), block(kRowThreads);
+  const bool one = chunks <= 1 << log_p;
   if (vec) {
-    if (per == 1) hipLaunchKernelGGL((cache_write_kernel<IN, FMT, 1, true>), grid, block, 0, s, a, log_p);
-    else if (per == 2) hipLaunchKernelGGL((cache_write_kernel<IN, FMT, 2, true>), grid, block, 0, s, a, log_p);
-    else hipLaunchKernelGGL((cache_write_kernel<IN, FMT, 4, true>), grid, block, 0, s, a, log_p);
+    if (one) hipLaunchKernelGGL((cache_write_kernel<IN, FMT, 1, true>), grid, block, 0, s, a, g);
+    else hipLaunchKernelGGL((cache_write_kernel<IN, FMT, 4, true>), grid, block, 0, s, a, g);
   } else {
-    if (per == 1) hipLaunchKernelGGL((cache_write_kernel<IN, FMT, 1, false>), grid, block, 0, s, a, log_p);
-    else hipLaunchKernelGGL((cache_write_kernel<IN, FMT, 4, false>), grid, block, 0, s, a, log_p);
+    if (one) hipLaunchKernelGGL((cache_write_kernel<IN, FMT, 1, false>), grid, block, 0, s, a, g);
+    else hipLaunchKernelGGL((cache_write_kernel<IN, FMT, 4, false>), grid, block, 0, s, a, g);
   }
   return hipGetLastError();
 }
@@ -557,81 +614,117 @@ hipError_t launch_cache_write(const CacheWriteArgs& a, int in_dtype, int fmt, hi
 
 namespace {
 
-// Sixteen elements of a cache row.
+// Eight elements of a cache row, as stored.
 template <int FMT>
-__device__ __forceinline__ void decode16(const CacheReadArgs& a, int64_t row, int c, float* o) {
-  const int64_t e0 = row * a.row + c * 16;
-  if constexpr (FMT == kBF16) {
-    const u32x4* p = reinterpret_cast<const u32x4*>(a.codes + e0 * 2);
-    unpack_bf16(p[0], o);
-    unpack_bf16(p[1], o + 8);
-    return;
-  }
-  if constexpr (FMT == kFP8 || FMT == kMXFP8) {
-    const u32x4 w = *reinterpret_cast<const u32x4*>(a.codes + e0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], false);
-      const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], true);
-      o[4 * i] = lo[0];
-      o[4 * i + 1] = lo[1];
-      o[4 * i + 2] = hi[0];
-      o[4 * i + 3] = hi[1];
-    }
-  }
-  if constexpr (FMT == kMXFP4) {
-    const u32x2 w = *reinterpret_cast<const u32x2*>(a.codes + (e0 >> 1));
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const uint32_t n = (w[i >> 3] >> (4 * (i & 7))) & 15u, m = n & 7u;
-      // exponent and mantissa bits of the E2M1 code in an fp32 (code 1 is 0.5, the one subnormal)
-      const float f = m < 2u ? 0.5f * (float)m : __uint_as_float(((m >> 1) + 126u) << 23 | (m & 1u) << 22);
-      o[i] = (n & 8u) ? -f : f;
-    }
-  }
-  if constexpr (FMT == kFP8) {
-    const float s = static_cast<const float*>(a.scale)[row];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] *= s;
-  } else {
-    const int b = static_cast<const uint8_t*>(a.scale)[e0 >> 5];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] = b == 255 ? __builtin_nanf("") : ldexpf(o[i], b - 127);
-  }
-}
+struct Stored8 {
+  u32x4 w;    // bf16 uses all four words, E4M3 two, E2M1 one
+  float s;    // FP8: the row's scale
+  unsigned b;  // MX: the block's scale byte
 
-// Rows read back: a thread decodes sixteen elements.
+  __device__ __forceinline__ void load(const CacheReadArgs& a, int64_t row, int e) {
+    const int64_t e0 = row * a.row + e;
+    if constexpr (FMT == kBF16) {
+      w = *reinterpret_cast<const u32x4*>(a.codes + e0 * 2);
+    } else if constexpr (FMT == kMXFP4) {
+      w[0] = *reinterpret_cast<const uint32_t*>(a.codes + (e0 >> 1));
+    } else {
+      const u32x2 t = *reinterpret_cast<const u32x2*>(a.codes + e0);
+      w[0] = t[0];
+      w[1] = t[1];
+    }
+    if constexpr (FMT == kFP8) s = static_cast<const float*>(a.scale)[row];
+    if constexpr (FMT == kMXFP8 || FMT == kMXFP4) b = static_cast<const uint8_t*>(a.scale)[e0 >> 5];
+  }
+
+  __device__ __forceinline__ void decode(float* o) const {
+    if constexpr (FMT == kBF16) {
+      unpack_bf16(w, o);
+    } else if constexpr (FMT == kFP8) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], false);
+        const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], true);
+        o[4 * i] = lo[0] * s;
+        o[4 * i + 1] = lo[1] * s;
+        o[4 * i + 2] = hi[0] * s;
+        o[4 * i + 3] = hi[1] * s;
+      }
+    } else {
+      const float by = __uint_as_float(b << 23);  // 2^(b - 127): the conversions multiply by it
+      if constexpr (FMT == kMXFP8) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const auto lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[i], by, false);
+          const auto hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[i], by, true);
+          o[4 * i] = lo[0];
+          o[4 * i + 1] = lo[1];
+          o[4 * i + 2] = hi[0];
+          o[4 * i + 3] = hi[1];
+        }
+      } else {
+        const auto p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[0], by, 0);
+        const auto p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[0], by, 1);
+        const auto p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[0], by, 2);
+        const auto p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[0], by, 3);
+        o[0] = p0[0]; o[1] = p0[1]; o[2] = p1[0]; o[3] = p1[1];
+        o[4] = p2[0]; o[5] = p2[1]; o[6] = p3[0]; o[7] = p3[1];
+      }
+      if (b == 255u) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = __builtin_nanf("");
+      }
+    }
+  }
+};
+
+constexpr int kReadUnits = 4;  // pieces of eight elements a thread has in flight
+
+// Rows read back, `rows` of them a workgroup: a thread decodes eight elements at a time, so that
+// a wave stores one contiguous kilobyte of bf16.
 template <int OUT, int FMT>
-__global__ void __launch_bounds__(kRowThreads) cache_read_kernel(CacheReadArgs a, int rows) {
-  const int chunks = a.row / 16;
+__global__ void __launch_bounds__(kRowThreads) cache_read_kernel(CacheReadArgs a, int rows, SmallDiv pieces) {
   for (int64_t i0 = (int64_t)blockIdx.x * rows; i0 < a.n; i0 += (int64_t)gridDim.x * rows) {
-    const int nr = (int)min((int64_t)rows, a.n - i0);
-    for (int u = threadIdx.x; u < nr * chunks; u += kRowThreads) {
-      const int r = u / chunks, c = u - r * chunks;
+    const unsigned end = (unsigned)min((int64_t)rows, a.n - i0) * pieces.by;
+    Stored8<FMT> x[kReadUnits];
+    int64_t to[kReadUnits];
+    bool live[kReadUnits];
+#pragma unroll
+    for (int k = 0; k < kReadUnits; ++k) {
+      const unsigned u = threadIdx.x + k * kRowThreads;
+      const unsigned r = pieces(u), e = (u - r * pieces.by) * 8;
       const int64_t i = i0 + r;
-      const int64_t row = a.slots ? (int64_t)a.slots[i] : a.start + i;
-      float v[16];
-      if (row >= 0 && row < a.L) {
-        decode16<FMT>(a, row, c, v);
+      to[k] = u < end ? i * a.row + e : -1;
+      live[k] = false;
+      if (u < end) {
+        const int64_t row = a.slots ? (int64_t)a.slots[i] : a.start + i;
+        live[k] = row >= 0 && row < a.L;
+        if (live[k]) x[k].load(a, row, (int)e);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kReadUnits; ++k) {
+      if (to[k] < 0) continue;
+      float v[8];
+      if (live[k]) {
+        x[k].decode(v);
       } else {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = 0.0f;
+        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
       }
-      store8<OUT>(a.out, i * a.row + c * 16, v);
-      store8<OUT>(a.out, i * a.row + c * 16 + 8, v + 8);
+      store8<OUT>(a.out, to[k], v);
     }
   }
 }
 
 template <int OUT>
 hipError_t cache_read_out(const CacheReadArgs& a, int fmt, hipStream_t s) {
-  const int chunks = a.row / 16;
-  const int rows = std::max(1, 4 * kRowThreads / chunks);
+  const SmallDiv pieces((unsigned)a.row / 8);           // at most 1,024
+  const int rows = kReadUnits * kRowThreads / (int)pieces.by;  // whole rows, at least one
   const dim3 grid(row_blocks(a.n, rows)), block(kRowThreads);
-  if (fmt == kBF16) hipLaunchKernelGGL((cache_read_kernel<OUT, kBF16>), grid, block, 0, s, a, rows);
-  else if (fmt == kFP8) hipLaunchKernelGGL((cache_read_kernel<OUT, kFP8>), grid, block, 0, s, a, rows);
-  else if (fmt == kMXFP8) hipLaunchKernelGGL((cache_read_kernel<OUT, kMXFP8>), grid, block, 0, s, a, rows);
-  else if (fmt == kMXFP4) hipLaunchKernelGGL((cache_read_kernel<OUT, kMXFP4>), grid, block, 0, s, a, rows);
+  if (fmt == kBF16) hipLaunchKernelGGL((cache_read_kernel<OUT, kBF16>), grid, block, 0, s, a, rows, pieces);
+  else if (fmt == kFP8) hipLaunchKernelGGL((cache_read_kernel<OUT, kFP8>), grid, block, 0, s, a, rows, pieces);
+  else if (fmt == kMXFP8) hipLaunchKernelGGL((cache_read_kernel<OUT, kMXFP8>), grid, block, 0, s, a, rows, pieces);
+  else if (fmt == kMXFP4) hipLaunchKernelGGL((cache_read_kernel<OUT, kMXFP4>), grid, block, 0, s, a, rows, pieces);
   else return hipErrorInvalidValue;
   return hipGetLastError();
 }
