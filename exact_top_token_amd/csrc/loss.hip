@@ -611,7 +611,7 @@ __device__ __forceinline__ float wave_max(float x) {
 // and t = mass / sum, each term t (ln t - ln p) - t + p is non-negative and
 // their sum is the loss (both t and p sum to 1): no cancellation between large terms.
 template <int N, bool VEC>
-__global__ void __launch_bounds__(kLossThreads) index_loss_kernel(LossArgs a) {
+__global__ void __launch_bounds__(kLossThreads, 4) index_loss_kernel(LossArgs a) {
   const int lane = threadIdx.x & 63;
   constexpr int W = kLossThreads / kWave;
   for (int64_t i = (int64_t)blockIdx.x * W + (threadIdx.x >> 6); i < a.n; i += (int64_t)gridDim.x * W) {
@@ -652,21 +652,24 @@ __global__ void __launch_bounds__(kLossThreads) index_loss_kernel(LossArgs a) {
     total = wave_sum(total);
     const bool none = total == 0.0f;  // also a row without a live entry
     const float ref = top == -__builtin_inff() ? 0.0f : top;
+    // Powers and logarithms in base 2 (one instruction each): y = (s - max) log2(e).
     float sum = 0.0f;
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-      s[e] -= ref;
-      sum += expf(s[e]);
+      s[e] = (s[e] - ref) * 1.44269504088896341f;
+      sum += exp2_fast(s[e]);
     }
     sum = wave_sum(sum);
     const float up = total < 0x1p-100f ? 0x1p100f : 1.0f;  // keeps 1 / total finite
-    const float lsum = logf(sum), rsum = 1.0f / sum, rtotal = 1.0f / (total * up);
+    const float lsum = __builtin_amdgcn_logf(sum), rsum = 1.0f / sum, rtotal = 1.0f / (total * up);
     const float w = a.weight ? a.weight[i] : 1.0f;
     float loss = 0.0f;
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-      const float p = expf(s[e]) * rsum, q = t[e] * up * rtotal;
-      const float kl = q > 0.0f ? q * (logf(q) - (s[e] - lsum)) : q;
+      const float p = exp2_fast(s[e]) * rsum, q = t[e] * up * rtotal;
+      // the logarithm instruction takes no subnormals; their term is nothing
+      const float lq = __builtin_amdgcn_logf(fmaxf(q, 0x1p-126f));
+      const float kl = q == 0.0f ? 0.0f : q * ((lq - (s[e] - lsum)) * 0.693147180559945309f);
       loss += kl - q + p;
       t[e] = w * (p - q);
     }

@@ -12,14 +12,14 @@ namespace hk {
 
 namespace {
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 256;  // threads of a workgroup (a write of long rows takes up to 1,024)
 
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 
-// Workgroups along the rows: one per `per` rows, at most 2^22 (a launch holds
+// Workgroups along the rows: one per `per` rows, at most 2^21 (a launch holds
 // fewer than 2^32 threads); the kernels walk the rest.
 unsigned row_blocks(int64_t n, int64_t per) {
-  return (unsigned)std::min<int64_t>((n + per - 1) / per, int64_t(1) << 22);
+  return (unsigned)std::min<int64_t>((n + per - 1) / per, int64_t(1) << 21);
 }
 
 // ------------------------------------------------------- element access
@@ -43,7 +43,61 @@ __device__ __forceinline__ void unpack_bf16(const u32x4& v, float* o) {
   }
 }
 
-// Eight consecutive elements; VEC: 16-byte aligned.
+// Eight consecutive elements as stored; VEC: 16-byte aligned.
+template <int DT>
+struct Raw8 {
+  u32x4 w[DT == kRowsBF16 ? 1 : 2];
+
+  __device__ __forceinline__ void zero() {
+    for (u32x4& x : w) x = u32x4{0u, 0u, 0u, 0u};
+  }
+  template <bool VEC>
+  __device__ __forceinline__ void load(const void* base, int64_t at) {
+    if constexpr (DT == kRowsBF16) {
+      const uint16_t* p = static_cast<const uint16_t*>(base) + at;
+      if constexpr (VEC) {
+        w[0] = *reinterpret_cast<const u32x4*>(p);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[0][i] = (uint32_t)p[2 * i] | ((uint32_t)p[2 * i + 1] << 16);
+      }
+    } else {
+      const uint32_t* p = static_cast<const uint32_t*>(base) + at;
+      if constexpr (VEC) {
+        w[0] = *reinterpret_cast<const u32x4*>(p);
+        w[1] = *reinterpret_cast<const u32x4*>(p + 4);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i >> 2][i & 3] = p[i];
+      }
+    }
+  }
+  __device__ __forceinline__ void floats(float* o) const {
+    if constexpr (DT == kRowsBF16) {
+      unpack_bf16(w[0], o);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = __uint_as_float(w[i >> 2][i & 3]);
+    }
+  }
+  // The signs flipped where `flip` is all ones.
+  __device__ __forceinline__ void negate(uint32_t flip) {
+    const uint32_t m = flip & (DT == kRowsBF16 ? 0x80008000u : 0x80000000u);
+    for (u32x4& x : w) x ^= u32x4{m, m, m, m};
+  }
+  // What another lane of the wave holds.
+  __device__ __forceinline__ Raw8 of_lane(int lane) const {
+    Raw8 r;
+#pragma unroll
+    for (unsigned i = 0; i < sizeof(w) / sizeof(w[0]); ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        r.w[i][j] = (uint32_t)__builtin_amdgcn_ds_bpermute(lane * 4, (int)w[i][j]);
+    return r;
+  }
+};
+
+// Eight consecutive elements as floats.
 template <int DT, bool VEC>
 __device__ __forceinline__ void load8(const void* base, int64_t at, float* o) {
   if constexpr (DT == kRowsBF16) {
@@ -118,14 +172,14 @@ __device__ __forceinline__ float2 turn_cos_sin(float t) {
                      __uint_as_float(__float_as_uint(ss) ^ (((unsigned)q & 2u) << 30)));
 }
 
-// gain * (cos, sign * sin) of pos * f.  The angle in turns is formed and
+// gain * (cos, sign * sin) at position pos, f turns a position.  The angle is formed and
 // reduced to [-1/2, 1/2] in 64 bits: at 2^31 positions its error is below
 // 1e-7 turns, at 2^20 below 1e-10, where 32 bits would keep none of it.
-__device__ __forceinline__ float2 rot_entry(const RotArgs& r, int i, int64_t pos) {
-  double t = (double)pos * (r.freq[i] * 0.15915494309189533577);
+__device__ __forceinline__ float2 rot_entry(const RotArgs& r, double f, int64_t pos) {
+  double t = (double)pos * f;
   t -= rint(t);
-  const float2 f = turn_cos_sin((float)t);
-  return make_float2(f.x * r.gain, f.y * (r.gain * r.sign));
+  const float2 c = turn_cos_sin((float)t);
+  return make_float2(c.x * r.gain, c.y * (r.gain * r.sign));
 }
 
 // One half of a rotated pair: v cos -+ w sin.  Written as one product and one fused
@@ -143,15 +197,44 @@ struct SmallDiv {
   }
 };
 
+// A token's entries in LDS, [dim/2] float2.  With 16-byte access a thread reads W pairs at
+// once (eight of the half layout, four of the interleaved one), two to a 16-byte read: pair
+// 2 j + b of unit u lies in the (j * units + u)-th 16 bytes, so that neighbouring threads
+// read neighbouring pieces without bank conflicts (in plain order their 64-byte steps met
+// in the same banks, and the LDS bounded the quantised write: 66 us of 8,192 x 64 x 128).
+template <int W>
+__device__ __forceinline__ int rot_slot(int i, int half) {
+  if constexpr (W == 1) return i;
+  const int u = i / W, w = i % W;
+  return 2 * ((w >> 1) * (half / W) + u) + (w & 1);
+}
+template <int W>
+__device__ __forceinline__ void rot_read(const float2* cs, int half, int u, float2* f) {
+  const f32x4* p = reinterpret_cast<const f32x4*>(cs) + u;
+#pragma unroll
+  for (int j = 0; j < W / 2; ++j) {
+    const f32x4 v = p[j * (half / W)];
+    f[2 * j] = make_float2(v[0], v[1]);
+    f[2 * j + 1] = make_float2(v[2], v[3]);
+  }
+}
+
 // The entries of tokens t0 .. t0 + nt - 1, once for all their heads: [nt][dim/2]
 // (at most 2,048 entries, or one token's).
+template <int W>
 __device__ __forceinline__ void rot_table(const RotArgs& r, int64_t t0, int nt, float2* cs) {
   const int half = r.dim >> 1;
-  const unsigned mul = ((1u << 22) + half - 1) / half;
-  for (int e = threadIdx.x; e < nt * half; e += blockDim.x) {
-    const int t = (int)(((uint64_t)e * mul) >> 22), i = e - t * half;
-    const int64_t pos = r.pos ? (int64_t)r.pos[t0 + t] : r.pos0 + t0 + t;
-    cs[e] = rot_entry(r, i, pos);
+  // a thread keeps its pair, whose frequency it loads once, and walks over tokens
+  const int threads = blockDim.x, cols = min(half, threads), steps = threads / cols;
+  const int first = threadIdx.x / cols;
+  if (first >= steps) return;
+  for (int i = threadIdx.x - first * cols; i < half; i += cols) {
+    const double f = r.freq[i] * 0.15915494309189533577;  // turns a position
+    float2* to = cs + rot_slot<W>(i, half);
+    for (int t = first; t < nt; t += steps) {
+      const int64_t pos = r.pos ? (int64_t)r.pos[t0 + t] : r.pos0 + t0 + t;
+      to[t * half] = rot_entry(r, f, pos);
+    }
   }
 }
 
@@ -173,7 +256,7 @@ namespace {
 
 template <int IN, int OUT, int LAYOUT, bool VEC>
 __global__ void __launch_bounds__(kRowThreads) rotary_kernel(RotaryArgs a, RotaryGrid g) {
-  extern __shared__ float2 cs[];
+  extern __shared__ __attribute__((aligned(16))) float2 cs[];
   const RotArgs& r = a.rot;
   const int half = r.dim >> 1;
   const int h0 = blockIdx.y * g.hb, nh = min(g.hb, a.heads - h0);
@@ -184,7 +267,7 @@ __global__ void __launch_bounds__(kRowThreads) rotary_kernel(RotaryArgs a, Rotar
   for (int64_t tile = blockIdx.x; tile * g.tb < a.n; tile += gridDim.x) {
     const int t0 = (int)(tile * g.tb), nt = min(g.tb, a.n - t0);
     if (tile != blockIdx.x) __syncthreads();  // the last tile's entries are read
-    rot_table(r, t0, nt, cs);
+    rot_table<PW>(r, t0, nt, cs);
     __syncthreads();
     // Units wider than the workgroup (heads of many elements without 16-byte
     // access) are walked in steps of the workgroup.
@@ -207,7 +290,8 @@ __global__ void __launch_bounds__(kRowThreads) rotary_kernel(RotaryArgs a, Rotar
           float v[8];
           load8<IN, true>(a.x, xi, v);
           if (rot) {
-            const float2* c = cs + t * half + u * PW;
+            float2 c[8];
+            rot_read<PW>(cs + t * half, half, u, c);
             if constexpr (LAYOUT == kRotHalf) {
               float w[8];
               load8<IN, true>(a.x, xi + half, w);
@@ -349,47 +433,74 @@ __device__ __forceinline__ uint32_t e4m3x4_quotient(const float* x, float scale,
   return e4m3x4(q[0], q[1], q[2], q[3]);
 }
 
-// Rotated values of elements e0 .. e0 + 7 of a head (v holds them unrotated;
-// `at` is the head's offset in x, cs the token's entries).
-template <int IN, bool VEC>
-__device__ __forceinline__ void rotate8(const RotArgs& r, const void* x, int64_t at, int e0,
-                                        const float2* cs, float* v) {
-  const int half = r.dim >> 1;
-  const int e = e0 - r.first;
-  if constexpr (VEC) {  // all eight lie on one side of every border
-    if (e < 0 || e >= r.dim) return;
-    if (r.layout == kRotHalf) {
-      const bool lo = e < half;
-      const float2* c = cs + (lo ? e : e - half);
-      float w[8];
-      load8<IN, true>(x, at + e0 + (lo ? half : -half), w);  // the partners, in cache by now
-      const float side = lo ? -1.0f : 1.0f;
+// A thread's eight elements e0 .. e0 + 7 of a head, on one side of every border of the rotation.
+struct Eight {
+  bool in;        // in the rotated part
+  uint32_t flip;  // half layout: all ones in its first half, whose partners count negative
+  int other;      // half layout: how far the partners lie
+  int unit;       // its entries in LDS
+
+  template <int LAYOUT>
+  __device__ __forceinline__ void place(const RotArgs& r, int e0) {
+    const int half = r.dim >> 1, e = e0 - r.first;
+    in = e >= 0 && e < r.dim;
+    const bool lo = e < half;
+    flip = lo ? ~0u : 0u;
+    other = lo ? half : -half;
+    unit = LAYOUT == kRotHalf ? (lo ? e : e - half) >> 3 : e >> 3;
+  }
+};
+
+// Rotated values of eight elements v; w: their partners of the half layout, signed; f: the
+// entries of the unit.
+template <int LAYOUT>
+__device__ __forceinline__ void rotate_eight(const float* w, const float2* f, float* v) {
+  if constexpr (LAYOUT == kRotHalf) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {  // rot_lo or rot_hi: the product's sign
-        const float2 f = c[i];
-        v[i] = fmaf(v[i], f.x, (w[i] * side) * f.y);
-      }
-    } else {
-      const float2* c = cs + (e >> 1);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = c[i];
-        const float p = v[2 * i], q = v[2 * i + 1];
-        v[2 * i] = rot_lo(p, q, f);
-        v[2 * i + 1] = rot_hi(q, p, f);
-      }
-    }
+    for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], f[i].x, w[i] * f[i].y);  // rot_lo or rot_hi
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int ei = e + i;
-      if (ei < 0 || ei >= r.dim) continue;
-      const bool lo = r.layout == kRotHalf ? ei < half : (ei & 1) == 0;
-      const int off = r.layout == kRotHalf ? half : 1;
-      const float2 f = cs[r.layout == kRotHalf ? (lo ? ei : ei - half) : ei >> 1];
-      const float w = load1<IN>(x, at + e0 + i + (lo ? off : -off));
-      v[i] = lo ? rot_lo(v[i], w, f) : rot_hi(v[i], w, f);
+    for (int i = 0; i < 4; ++i) {
+      const float p = v[2 * i], q = v[2 * i + 1];
+      v[2 * i] = rot_lo(p, q, f[i]);
+      v[2 * i + 1] = rot_hi(q, p, f[i]);
     }
+  }
+}
+
+// The largest of m over groups of P neighbouring lanes (4 <= P <= 64): quads and
+// rows of 16 by lane permutations inside the vector instruction.
+template <int CTRL>
+__device__ __forceinline__ float max_dpp(float m) {
+  return fmaxf(m, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(m), CTRL, 0xf, 0xf, true)));
+}
+__device__ __forceinline__ float quad_max(float m) {
+  return max_dpp<0x4e>(max_dpp<0xb1>(m));  // neighbours, then pairs of neighbours
+}
+__device__ __forceinline__ float lanes_max(float m, int P) {
+  m = quad_max(m);
+  if (P > 4) m = max_dpp<0x141>(m);  // the other quad of eight lanes (mirrored)
+  if (P > 8) m = max_dpp<0x140>(m);  // the other eight of sixteen
+  if (P > 16) m = fmaxf(m, __shfl_xor(m, 16));
+  if (P > 32) m = fmaxf(m, __shfl_xor(m, 32));
+  return m;
+}
+
+// The same one element at a time, for any rotated part and alignment (cs: the token's entries in
+// plain order).
+template <int IN>
+__device__ __forceinline__ void rotate_each(const RotArgs& r, const void* x, int64_t at, int e0,
+                                            const float2* cs, float* v) {
+  const int half = r.dim >> 1;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int e = e0 - r.first + i;
+    if (e < 0 || e >= r.dim) continue;
+    const bool lo = r.layout == kRotHalf ? e < half : (e & 1) == 0;
+    const int off = r.layout == kRotHalf ? half : 1;
+    const float2 f = cs[r.layout == kRotHalf ? (lo ? e : e - half) : e >> 1];
+    const float w = load1<IN>(x, at + e0 + i + (lo ? off : -off));
+    v[i] = lo ? rot_lo(v[i], w, f) : rot_hi(v[i], w, f);
   }
 }
 
@@ -397,150 +508,202 @@ __device__ __forceinline__ void rotate8(const RotArgs& r, const void* x, int64_t
 // workgroup takes `rounds` times 256 / P rows at once.
 struct WriteGrid {
   int log_p;
+  int segs;       // steps of P pieces that a row takes
   int rounds;
+  int near;       // no head straddles two waves: partners are a lane's to give
   SmallDiv head;  // chunks of eight elements of a head
 };
 
+constexpr int kMaxWriteThreads = 1024;
 constexpr int kWriteEntries = 2048;  // cosines and sines of a workgroup's rows
 
-// Rows written into a cache.  P threads (a power of two, 4..256) take a row in
-// chunks of eight elements, K chunks each, so a row is read once and its
-// scale comes from registers: a lane reduction over the row (FP8), or over the four
-// lanes of a 32-element block (MX).
-template <int IN, int FMT, int K, bool VEC>
-__global__ void __launch_bounds__(kRowThreads)
+// Rows written into a cache.  P threads (a power of two, 4..256; up to 1,024 for FP8) take
+// a row in pieces of eight elements, K of them at a time, so a row is read once and its
+// scale comes from registers: a reduction over the row (FP8), or over the four
+// lanes of a 32-element block (MX).  K is 4 for rows of more than 256 pieces whose
+// heads repeat every P pieces (`same`): a thread's pieces then share their cosines and
+// sines, their place in the head and the row's set-up.  Other long rows are walked 256
+// pieces at a time (FP8: 1,024 threads a row).  8,192 x 64 x 128 to MXFP4, rotated: with
+// K = 4 47 us, one piece at a time 64 (bound by the instructions around the
+// elements), 1,024 threads a row 65 (waiting for each other).
+template <int IN, int FMT, int K, bool VEC, int LAYOUT>
+__global__ void __launch_bounds__(FMT == kFP8 && K == 1 ? kMaxWriteThreads : kRowThreads)
 cache_write_kernel(CacheWriteArgs a, WriteGrid g) {
-  __shared__ float2 cs[kWriteEntries];
-  __shared__ float red[2][kRowThreads / kWave];
+  __shared__ __attribute__((aligned(16))) float2 cs[kWriteEntries];
+  __shared__ float red[2][kMaxWriteThreads / kWave];
   __shared__ int later[kRowThreads / 4];
-  const int log_p = g.log_p, P = 1 << log_p, RB = kRowThreads >> log_p;
-  const int rl = threadIdx.x >> log_p, lr = threadIdx.x & (P - 1);
+  constexpr int KV = FMT == kFP8 ? K : 1;  // pieces whose values are held at once
+  const int log_p = g.log_p, P = 1 << log_p, RB = (int)blockDim.x >> log_p;
+  const int rl = threadIdx.x >> log_p;
   const int chunks = a.heads * g.head.by, half = a.rot.dim >> 1;
-  int64_t at[K];  // the chunk's head in a row of x
-  int e0[K];      // and its first element there
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const unsigned c = (unsigned)(lr + k * P), h = g.head(c);
-    at[k] = (int64_t)h * a.hs;
-    e0[k] = (int)(c - h * g.head.by) * 8;
-  }
+  // A thread's (first) piece of the row: chunk lr, eight elements from e0 of a head, at `at` in
+  // a row of x.  Piece k of K lies k P chunks and k `step` elements on.
+  struct Piece {
+    int lr, e0;
+    int64_t at;
+  };
+  const int64_t step = K > 1 ? (int64_t)g.head(P) * a.hs : 0;
+  auto piece = [&](int seg) {
+    Piece p;
+    p.lr = (int)(threadIdx.x & (P - 1)) + (seg << log_p);
+    const unsigned h = g.head((unsigned)p.lr);
+    p.e0 = (p.lr - (int)(h * g.head.by)) * 8;
+    p.at = (int64_t)h * a.hs + p.e0;
+    return p;
+  };
   int flip = 0;
   for (int64_t i0 = (int64_t)blockIdx.x * RB * g.rounds; i0 < a.n; i0 += (int64_t)gridDim.x * RB * g.rounds) {
     const int tile = (int)min((int64_t)RB * g.rounds, a.n - i0);
-    if (a.rot.freq) {
-      __syncthreads();  // the last rows' entries are read
-      rot_table(a.rot, i0, tile, cs);
-      __syncthreads();
-    }
-    for (int r0 = 0; r0 < tile; r0 += RB) {
+    Raw8<IN> raw[K];  // the next step's elements and slot, under way while this one is worked on
+    int slot = -1;
+    auto fetch = [&](const Piece& p, int r0) {
       const bool have = r0 + rl < tile;
-      const int64_t i = i0 + r0 + rl;
-      float v[K][8];
+      const int64_t at = (i0 + r0 + rl) * a.ts + p.at;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (have && lr + k * P < chunks) {
-          load8<IN, VEC>(a.x, i * a.ts + at[k] + e0[k], v[k]);
-        } else {
+        raw[k].zero();
+        if (have && p.lr + k * P < chunks) raw[k].template load<VEC>(a.x, at + k * step);
+      }
+      slot = -1;
+      if (have) slot = a.slots ? a.slots[i0 + r0 + rl] : (int)(a.start + i0) + r0 + rl;
+    };
+    Piece ahead = piece(0);
+    fetch(ahead, 0);
+    if (a.rot.freq) {
+      __syncthreads();  // the last rows' entries are read
+      rot_table<!VEC ? 1 : LAYOUT == kRotHalf ? 8 : 4>(a.rot, i0, tile, cs);
+      __syncthreads();
+    }
+    for (int r0 = 0, seg = 0; r0 < tile;) {
+      const bool have = r0 + rl < tile;
+      const int i = (int)i0 + r0 + rl;
+      const Piece my = ahead;
+      Raw8<IN> now[K];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[k][j] = 0.0f;
-        }
+      for (int k = 0; k < K; ++k) now[k] = raw[k];
+      // The row's place; negative where nothing is written.
+      int row = slot < a.L ? slot : -1;
+      const int r1 = r0;
+      if (++seg == g.segs) {
+        seg = 0;
+        r0 += RB;
       }
-
-      // The row's place; -1 where nothing is written.
-      int64_t row = -1;
-      if (have) {
-        row = a.slots ? (int64_t)a.slots[i] : a.start + i;
-        if (row >= a.L || row < 0) row = -1;
-        if (row >= 0 && a.claim && a.claim[row] != i) row = -1;
+      if (r0 < tile) {
+        if (g.segs > 1) ahead = piece(seg);
+        fetch(ahead, r0);
       }
+      if (a.claim && row >= 0 && a.claim[row] != i) row = -1;
       if (a.slots && !a.claim) {  // few rows: look for a later row of the same slot
         __syncthreads();
-        for (int t = threadIdx.x; t < RB; t += kRowThreads) later[t] = 0;
+        if ((int)threadIdx.x < RB) later[threadIdx.x] = 0;
         __syncthreads();
         if (row >= 0) {
           bool dup = false;
-          for (int j = (int)i + 1 + lr; j < a.n; j += P) dup |= (int64_t)a.slots[j] == row;
+          for (int j = i + 1 + (my.lr & (P - 1)); j < a.n; j += P) dup |= a.slots[j] == row;
           if (dup) later[rl] = 1;
         }
         __syncthreads();
         if (later[rl]) row = -1;
       }
 
-      if (a.rot.freq && have) {
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-          if (lr + k * P < chunks)
-            rotate8<IN, VEC>(a.rot, a.x, i * a.ts + at[k], e0[k], cs + (r0 + rl) * half, v[k]);
-      }
+      const float2* entries = cs + (have ? r1 + rl : 0) * half;
+      Eight part;
+      part.template place<LAYOUT>(a.rot, my.e0);
+      float2 f[8];
+      if (VEC && a.rot.freq && part.in) rot_read<LAYOUT == kRotHalf ? 8 : 4>(entries, half, part.unit, f);
+      // The k-th piece's values, rotated.
+      auto values = [&](int k, float* v) {
+        now[k].floats(v);
+        if (!a.rot.freq) return;
+        if constexpr (VEC) {
+          float w[8];
+          if constexpr (LAYOUT == kRotHalf) {
+            Raw8<IN> other = now[k];
+            if (g.near) other = now[k].of_lane(lane_id() + (part.in ? part.other / 8 : 0));
+            else if (part.in && have && my.lr + k * P < chunks)
+              other.template load<true>(a.x, (int64_t)i * a.ts + my.at + k * step + part.other);
+            other.negate(part.flip);
+            other.floats(w);
+          }
+          if (part.in) rotate_eight<LAYOUT>(w, f, v);
+        } else if (have && my.lr + k * P < chunks) {
+          rotate_each<IN>(a.rot, a.x, (int64_t)i * a.ts + my.at + k * step - my.e0, my.e0, entries, v);
+        }
+      };
 
+      float v[KV][8];
       float scale = 1.0f, inv = 1.0f;
       if constexpr (FMT == kFP8) {
         float m = 0.0f;
 #pragma unroll
-        for (int k = 0; k < K; ++k)
+        for (int k = 0; k < K; ++k) {
+          values(k, v[k]);
 #pragma unroll
           for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[k][j]));
-        for (int off = min(P, kWave) >> 1; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+        }
+        m = lanes_max(m, P);
         if (P > kWave) {  // uniform over the launch
-          float* now = red[flip];  // the other half is read by waves still in the last round
+          float* sums = red[flip];  // the other half is read by waves still in the last round
           flip ^= 1;
-          if (lane_id() == 0) now[threadIdx.x >> 6] = m;
+          if (lane_id() == 0) sums[threadIdx.x >> 6] = m;
           __syncthreads();
           const int w0 = rl * (P / kWave);
-          for (int w = 0; w < P / kWave; ++w) m = fmaxf(m, now[w0 + w]);
+          for (int w = 0; w < P / kWave; ++w) m = fmaxf(m, sums[w0 + w]);
         }
         scale = m > 0.0f ? fmaxf(m / 448.0f, 0x1p-126f) : 1.0f;
         inv = 1.0f / scale;
-        if (row >= 0 && lr == 0) static_cast<float*>(a.scale)[row] = scale;
+        if (row >= 0 && my.lr == 0) static_cast<float*>(a.scale)[row] = scale;
       }
 
+      const int64_t chunk0 = (int64_t)((uint64_t)(unsigned)row * (unsigned)chunks) + my.lr;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const int c = lr + k * P;
+        float* y = v[FMT == kFP8 ? k : 0];
+        if constexpr (FMT != kFP8) values(k, y);
         int e = 0;
         if constexpr (FMT == kMXFP8 || FMT == kMXFP4) {
           float m = 0.0f;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[k][j]));
-          m = fmaxf(m, __shfl_xor(m, 1));
-          m = fmaxf(m, __shfl_xor(m, 2));
+          for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(y[j]));
+          m = quad_max(m);
           // floor(log2(m)) - emax, clamped; frexp's exponent is floor(log2(m)) + 1
           const int x = __builtin_amdgcn_frexp_expf(m) - 1 - (FMT == kMXFP8 ? 8 : 2);
           e = m > 0.0f ? max(-127, min(127, x)) : -127;
         }
-        if (row < 0 || c >= chunks) {
+        const int64_t chunk = chunk0 + k * P;
+        if (row < 0 || my.lr + k * P >= chunks) {
           // nothing to write
         } else if constexpr (FMT == kBF16) {
-          store8<kRowsBF16>(a.codes, (row * chunks + c) * 8, v[k]);
+          store8<kRowsBF16>(a.codes, chunk * 8, y);
         } else if constexpr (FMT == kFP8) {
-          const u32x2 w = {e4m3x4_quotient(v[k], scale, inv), e4m3x4_quotient(v[k] + 4, scale, inv)};
-          *reinterpret_cast<u32x2*>(a.codes + (row * chunks + c) * 8) = w;
+          const u32x2 w = {e4m3x4_quotient(y, scale, inv), e4m3x4_quotient(y + 4, scale, inv)};
+          *reinterpret_cast<u32x2*>(a.codes + chunk * 8) = w;
         } else {
-          if ((lr & 3) == 0)
-            static_cast<uint8_t*>(a.scale)[(row * chunks + c) >> 2] = (uint8_t)(e + 127);
+          if ((my.lr & 3) == 0)
+            static_cast<uint8_t*>(a.scale)[chunk >> 2] = (uint8_t)(e + 127);
           // the conversions divide by this: the scale's exponent in an fp32
           const float by = __uint_as_float((unsigned)(e + 127) << 23);
-          if constexpr (FMT == kMXFP8) {
+          if constexpr (FMT == kMXFP8) {  // what lies over 448 would turn to NaN
             const float top = ldexpf(448.0f, e);
             u32x2 w;
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-              float y[4];
+              float z[4];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) y[j] = __builtin_amdgcn_fmed3f(v[k][4 * p + j], -top, top);
+              for (int j = 0; j < 4; ++j) z[j] = __builtin_amdgcn_fmed3f(y[4 * p + j], -top, top);
               short2v t = {0, 0};
-              t = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(t, y[0], y[1], by, false);
-              t = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(t, y[2], y[3], by, true);
+              t = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(t, z[0], z[1], by, false);
+              t = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(t, z[2], z[3], by, true);
               w[p] = __builtin_bit_cast(uint32_t, t);
             }
-            *reinterpret_cast<u32x2*>(a.codes + (row * chunks + c) * 8) = w;
+            *reinterpret_cast<u32x2*>(a.codes + chunk * 8) = w;
           } else {  // saturates by itself
             uint32_t w = 0;
-            w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[k][0], v[k][1], by, 0);
-            w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[k][2], v[k][3], by, 1);
-            w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[k][4], v[k][5], by, 2);
-            w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[k][6], v[k][7], by, 3);
-            *reinterpret_cast<uint32_t*>(a.codes + (row * chunks + c) * 4) = w;
+            w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, y[0], y[1], by, 0);
+            w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, y[2], y[3], by, 1);
+            w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, y[4], y[5], by, 2);
+            w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, y[6], y[7], by, 3);
+            *reinterpret_cast<uint32_t*>(a.codes + chunk * 4) = w;
           }
         }
       }
@@ -560,28 +723,34 @@ claim_kernel(const int* slots, int n, int L, int* claim, bool clear) {
   }
 }
 
-template <int IN, int FMT>
-hipError_t cache_write_fmt(const CacheWriteArgs& a, bool vec, hipStream_t s) {
-  const int chunks = a.heads * a.d / 8;
-  int log_p = 2;
-  while ((1 << log_p) < chunks && log_p < 8) ++log_p;
-  const int rb = kRowThreads >> log_p;
+template <int IN, int FMT, int K>
+hipError_t cache_write_k(const CacheWriteArgs& a, bool vec, int log_p, hipStream_t s) {
+  const int chunks = a.heads * a.d / 8, per = K << log_p;
+  const int segs = (chunks + per - 1) / per;
+  const int threads = std::max(kRowThreads, 1 << log_p), rb = threads >> log_p;
   // Rounds share the set-up and the entries of a workgroup's rows; as many (up to
   // four) as leave 2,048 workgroups and fit the table.
   int rounds = 1;
   const int fit = a.rot.freq ? kWriteEntries / (rb * (a.rot.dim / 2)) : 4;
   while (rounds < 4 && 2 * rounds <= fit && a.n / ((int64_t)rb * 2 * rounds) >= 2048) rounds *= 2;
-  const WriteGrid g{log_p, rounds, SmallDiv((unsigned)a.d / 8)};
-  const dim3 grid(row_blocks(a.n, rb * rounds)), block(kRowThreads);
-  const bool one = chunks <= 1 << log_p;
-  if (vec) {
-    if (one) hipLaunchKernelGGL((cache_write_kernel<IN, FMT, 1, true>), grid, block, 0, s, a, g);
-    else hipLaunchKernelGGL((cache_write_kernel<IN, FMT, 4, true>), grid, block, 0, s, a, g);
-  } else {
-    if (one) hipLaunchKernelGGL((cache_write_kernel<IN, FMT, 1, false>), grid, block, 0, s, a, g);
-    else hipLaunchKernelGGL((cache_write_kernel<IN, FMT, 4, false>), grid, block, 0, s, a, g);
-  }
+  const WriteGrid g{log_p, segs, rounds, kWave % (a.d / 8) == 0, SmallDiv((unsigned)a.d / 8)};
+  const dim3 grid(row_blocks(a.n, rb * rounds)), block((unsigned)threads);
+  if (!vec)  // the layout is a branch there
+    hipLaunchKernelGGL((cache_write_kernel<IN, FMT, K, false, kRotHalf>), grid, block, 0, s, a, g);
+  else if (a.rot.layout == kRotHalf)
+    hipLaunchKernelGGL((cache_write_kernel<IN, FMT, K, true, kRotHalf>), grid, block, 0, s, a, g);
+  else
+    hipLaunchKernelGGL((cache_write_kernel<IN, FMT, K, true, kRotInterleaved>), grid, block, 0, s, a, g);
   return hipGetLastError();
+}
+
+template <int IN, int FMT>
+hipError_t cache_write_fmt(const CacheWriteArgs& a, bool vec, hipStream_t s) {
+  const int chunks = a.heads * a.d / 8;
+  const bool four = chunks > kRowThreads && kRowThreads % (a.d / 8) == 0;
+  int log_p = 2;
+  while ((1 << log_p) < chunks && log_p < (FMT == kFP8 && !four ? 10 : 8)) ++log_p;
+  return four ? cache_write_k<IN, FMT, 4>(a, vec, log_p, s) : cache_write_k<IN, FMT, 1>(a, vec, log_p, s);
 }
 
 template <int IN>
