@@ -34,6 +34,14 @@ __device__ __forceinline__ void lse_reference(float l, float& m, float& rl) {
   rl = fabsf(m) < 3.0e38f ? exp2_fast(-fmaf(l, kLo, fmaf(l, kHi, -m))) : 1.0f;
 }
 
+// The sum over the four rows of 16 lanes, in each of them.
+__device__ __forceinline__ float add_rows(float x) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
 // How the heads of a query lie on 16-row tiles: each key head's heads padded to
 // whole tiles.
 struct HeadTiles {
@@ -272,26 +280,38 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(MassArgs a, int pass
 
 // The same with the key rows staged through LDS, for rows of 128 or 256 bytes.
 // A direct-to-LDS load fetches rows whole, where gathering the operand layout gives
-// every lane its own 16 bytes of another row.  Each wave owns a ring of kMassRing stages of
-// 16 rows and waits for its own loads by count; the q rows of a pass
-// (PT tiles of one key head) stay in registers.  The mass walks the wave's blocks
-// from the last to the first, so that the rows still in the ring and in the
-// caches are used again.
-constexpr int kMassRing = 3;
-
+// every lane its own 16 bytes of another row (from a cache that holds the keys the
+// one reaches 25 TB/s on this chip and the other 9.5).  Each wave owns two stages of 16 rows
+// and waits for its own loads by count; the q rows of a pass (PT tiles of one
+// key head) stay in registers.  With the statistics and the mass in one workgroup
+// (MODE 2) the mass walks the wave's blocks from the last to the first, so that the
+// rows still in LDS and in the caches are used again.
+//
+// What bounds it is the rate of instructions of a SIMD (per block of 16 entries and 64 heads of 128:
+// 16 MFMAs, 16 exponentials, 32 fused multiplies) and, where the keys come from the
+// memory-side cache, its 8.2 TB/s.  So waves count for more than loads in flight or
+// gathered bytes: two stages and three waves per SIMD measured 278 us (2,048 queries x 64
+// heads x 2,048 entries of 131,072 keys), three stages and two waves 300; eight waves a workgroup
+// that kept five of sixteen blocks' logits in registers and four stages in LDS,
+// for 44% fewer bytes, 301.
 template <int NK, int PT, int MODE>
 __global__ void __launch_bounds__(kMassThreads, 3) mass_staged_kernel(MassArgs a) {
   constexpr int D = NK * 32, RB = D * 2, NCH = RB / 16, OPS = 16 * RB / 1024;
   constexpr int KPI = 1024 / RB;  // rows of a load
+  constexpr int W = kMassWaves;
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   const HeadTiles ht(a.heads, a.groups);
   const int T = a.groups * ht.tiles;
-  uint8_t* ring = lds;                                                        // [ring][waves][16 rows]
-  float* ms = reinterpret_cast<float*>(ring + kMassRing * kMassWaves * 16 * RB);  // [PT * 16]
-  float* rs = ms + PT * 16;                                                   // [PT * 16]
-  float2* red = reinterpret_cast<float2*>(rs + PT * 16);                      // [waves][PT * 16]
-  int* ids = reinterpret_cast<int*>(red + kMassWaves * PT * 16);              // [split_len]
-  float* sums = reinterpret_cast<float*>(ids + a.split_len);                  // [split_len]
+  uint8_t* ring = lds;                                                // [2][waves][16 rows]
+  float* ms = reinterpret_cast<float*>(ring + 2 * W * 16 * RB);       // [PT * 16]
+  float* rs = ms + PT * 16;                                           // [PT * 16]
+  float2* red = reinterpret_cast<float2*>(rs + PT * 16);              // [waves][PT * 16]
+  uint64_t* live64 = reinterpret_cast<uint64_t*>(red + W * PT * 16);  // [split_len / 64] live entries
+  // [split_len] where an entry's key row begins, in 16-byte pieces (padding: row 0, which no live
+  // entry uses)
+  uint32_t* rows_at = reinterpret_cast<uint32_t*>(live64 + a.split_len / 64);
+  // [split_len] fp32 bits; with one pass each sum takes the place of its row, which is through by then
+  uint32_t* sums = rows_at + (T > PT ? a.split_len : 0);
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -303,51 +323,48 @@ __global__ void __launch_bounds__(kMassThreads, 3) mass_staged_kernel(MassArgs a
   }();
   const int split = blockIdx.y;
   const int j0 = split * a.split_len, nj = min(a.split_len, a.topk - j0);
-  const int njp = (nj + 15) & ~15;
-  for (int j = tid; j < njp; j += kMassThreads) {
+  for (int j = tid; j < a.split_len; j += kMassThreads) {  // whole waves: split_len is a multiple of 64
     const int id = j < nj ? a.idx[(int64_t)q * a.topk + j0 + j] : -1;
-    ids[j] = (unsigned)id < (unsigned)a.L ? id : -1;
+    const bool on = (unsigned)id < (unsigned)a.L;
+    const uint64_t live = __ballot(on);
+    rows_at[j] = on ? (uint32_t)id * (uint32_t)(a.groups * NCH) : 0u;
+    if (lane == 0) live64[j >> 6] = live;
   }
-  const int nblk = njp / 16;
-  const int mine = wave < nblk ? (nblk - wave + kMassWaves - 1) / kMassWaves : 0;  // wave-uniform
-  uint8_t* const ring0 = ring + wave * 16 * RB;  // stage s: + s * kMassWaves * 16 * RB
-  constexpr int SLOT = kMassWaves * 16 * RB;
-  const int64_t row_bytes = (int64_t)a.groups * RB;
+  const int nblk = (nj + 15) / 16;
+  const int mine = wave < nblk ? (nblk - wave + W - 1) / W : 0;  // wave-uniform
+  uint8_t* const ring0 = ring + wave * 16 * RB;  // stage s: + s * SLOT
+  constexpr int SLOT = W * 16 * RB;
   int dsw[OPS];  // load p fetches this chunk of its row (the stage's swizzle)
 #pragma unroll
   for (int p = 0; p < OPS; ++p) dsw[p] = 16 * ((lane % NCH) ^ key_swz<NCH>(p * KPI + lane / NCH));
-  const uint8_t* kbase = reinterpret_cast<const uint8_t*>(a.k);
-  // the wave's i-th block, key head g, into its stage; padding fetches row 0, which no live entry uses
-  auto issue = [&](int i, int g, int stage) {
+  typedef uint16_t __attribute__((may_alias)) live_bits;
+  const live_bits* live16 = reinterpret_cast<const live_bits*>(live64);
+  const uint32_t* my_rows = rows_at + wave * 16 + lane / NCH;
+  // the wave's i-th block, from kg (the key head's first byte), into its stage i % 2
+  auto issue = [&](int i, const uint8_t* kg) {
+    uint8_t* to = ring0 + (i & 1) * SLOT;
 #pragma unroll
-    for (int p = 0; p < OPS; ++p) {
-      const int id = ids[(wave + i * kMassWaves) * 16 + p * KPI + lane / NCH];
-      lds_dma16(kbase + max(id, 0) * row_bytes + g * RB + dsw[p], ring0 + stage * SLOT + p * 1024);
-    }
+    for (int p = 0; p < OPS; ++p)
+      lds_dma16(kg + dsw[p] + ((uint64_t)my_rows[i * W * 16 + p * KPI] << 4), to + p * 1024);
   };
   const uint32_t ring_at = lds_addr(ring0);
   uint32_t chunk_at[NK];
 #pragma unroll
-  for (int s = 0; s < NK; ++s) chunk_at[s] = col * RB + (((4 * s + grp) ^ key_swz<NCH>(col)) * 16);
-  auto frags = [&](int stage, bf16x8* f) {
+  for (int s = 0; s < NK; ++s) chunk_at[s] = ring_at + col * RB + (((4 * s + grp) ^ key_swz<NCH>(col)) * 16);
+  auto frags = [&](int i, bf16x8* f) {
     uint32_t ad[NK];
     u32x4 r[NK];
 #pragma unroll
-    for (int s = 0; s < NK; ++s) ad[s] = ring_at + stage * SLOT + chunk_at[s];
+    for (int s = 0; s < NK; ++s) ad[s] = chunk_at[s] + (i & 1) * SLOT;
     lds_read_chunks<NK>(ad, r);
 #pragma unroll
     for (int s = 0; s < NK; ++s) f[s] = __builtin_bit_cast(bf16x8, r[s]);
-  };
-  auto await = [&](int ahead) {  // all but the newest `ahead` stages have landed
-    static_assert(kMassRing == 3, "stages waited for");
-    if (ahead >= 2) HK_WAIT_VM(2 * OPS);
-    else if (ahead == 1) HK_WAIT_VM(OPS);
-    else HK_WAIT_VM(0);
   };
 
   for (int c0 = 0, g = 0, ta = 0; c0 < T;) {
     const int nt = min(PT, ht.tiles - ta);  // tiles of this pass: ta .. ta + nt - 1 of key head g
     const bool last = c0 + nt == T;
+    const uint8_t* kg = reinterpret_cast<const uint8_t*>(a.k) + g * RB;
     bf16x8 qf[PT][NK];
 #pragma unroll
     for (int t = 0; t < PT; ++t) {
@@ -381,48 +398,46 @@ __global__ void __launch_bounds__(kMassThreads, 3) mass_staged_kernel(MassArgs a
 #pragma unroll
       for (int t = 0; t < PT; ++t) { m[t] = kNoMax; l[t] = 0.0f; }
       HK_WAIT_VM(0);  // from here on the wave counts its stages' loads alone
-#pragma unroll
-      for (int s = 0; s < kMassRing - 1; ++s)
-        if (s < mine) issue(s, g, s);
-      for (int i = 0, stage = 0; i < mine; ++i) {
-        const int ahead = i + kMassRing - 1;
-        if (ahead < mine) issue(ahead, g, stage == 0 ? kMassRing - 1 : stage - 1);
-        await(min(kMassRing - 1, mine - 1 - i));
+      if (mine) issue(0, kg);
+      for (int i = 0; i < mine; ++i) {
+        if (i + 1 < mine) {
+          issue(i + 1, kg);
+          HK_WAIT_VM(OPS);
+        } else {
+          HK_WAIT_VM(0);
+        }
         bf16x8 f[NK];
-        frags(stage, f);
-        const bool on = ids[(wave + i * kMassWaves) * 16 + col] >= 0;
-        const unsigned all = (unsigned)(__ballot(on) & 0xffffu);
-        const unsigned live = all >> (4 * grp);
+        frags(i, f);
+        // lane: keys 4 grp .. + 3 of the block, head col of each tile
+        const unsigned all = __builtin_amdgcn_readfirstlane(live16[wave + i * W]), live = all >> (4 * grp);
 #pragma unroll
         for (int t = 0; t < PT; ++t) {
           f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int s = 0; s < NK; ++s)
             acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[s], qf[t][s], acc, 0, 0, 0);
-          if (all != 0xffffu) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (!((live >> e) & 1u)) acc[e] = a.scale2 < 0.0f ? __builtin_inff() : -__builtin_inff();
-          }
-          float y[4];
+          float y[4];  // padding takes no part, whatever its row holds
 #pragma unroll
           for (int e = 0; e < 4; ++e) y[e] = fmaf(acc[e], a.scale2, -m[t]);
+          if (all != 0xffffu) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = (live >> e) & 1u ? y[e] : -__builtin_inff();
+          }
           const float over = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
           if (__any(over > kLazy)) {
             float x[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = acc[e] * a.scale2;
+            for (int e = 0; e < 4; ++e) x[e] = (live >> e) & 1u ? acc[e] * a.scale2 : -__builtin_inff();
             const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
             if (top > m[t] + kLazy) {
               l[t] *= exp2_fast(m[t] - top);
               m[t] = top;
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = fmaf(acc[e], a.scale2, -m[t]);
+            for (int e = 0; e < 4; ++e) y[e] = (live >> e) & 1u ? fmaf(acc[e], a.scale2, -m[t]) : -__builtin_inff();
           }
           l[t] += (exp2_fast(y[0]) + exp2_fast(y[1])) + (exp2_fast(y[2]) + exp2_fast(y[3]));
         }
-        stage = stage == kMassRing - 1 ? 0 : stage + 1;
       }
 #pragma unroll
       for (int t = 0; t < PT; ++t) {
@@ -435,12 +450,13 @@ __global__ void __launch_bounds__(kMassThreads, 3) mass_staged_kernel(MassArgs a
       for (int r = tid; r < PT * 16; r += kMassThreads) {
         float2 p = red[r];
 #pragma unroll
-        for (int w = 1; w < kMassWaves; ++w) p = join(p, red[w * PT * 16 + r]);
+        for (int w = 1; w < W; ++w) p = join(p, red[w * PT * 16 + r]);
         if constexpr (MODE == 0) {
           if (r < nt * 16) a.part[((int64_t)q * a.nsplit + split) * (T * 16) + c0 * 16 + r] = p;
         } else {
+          const bool head = (r >> 4) < nt && ht.head(c0 + (r >> 4), r & 15) >= 0;
           ms[r] = p.x;
-          rs[r] = (r >> 4) >= nt || ht.head(c0 + (r >> 4), r & 15) < 0 || p.y == 0.0f ? 0.0f : 1.0f / p.y;
+          rs[r] = !head || p.y == 0.0f ? 0.0f : 1.0f / p.y;
         }
       }
       __syncthreads();
@@ -448,36 +464,29 @@ __global__ void __launch_bounds__(kMassThreads, 3) mass_staged_kernel(MassArgs a
 
     if constexpr (MODE != 0) {
       HK_WAIT_VM(0);
-      // Blocks from the last to the first; after the statistics of the same pass the last
-      // kMassRing of them still lie in the ring, block i in stage i % kMassRing.
-      int stage = mine ? (mine - 1) % kMassRing : 0;
-      int next = mine - 1;  // the next block to fetch
-      if constexpr (MODE == 2) next = max(-1, mine - 1 - kMassRing);
+      // Blocks from the last to the first, block i in stage i % 2; after the statistics of
+      // the same pass the last two still lie there.
       if constexpr (MODE == 1) {
-        for (int s = 0, st = stage; s < kMassRing - 1 && next >= 0; ++s, --next) {
-          issue(next, g, st);
-          st = st == 0 ? kMassRing - 1 : st - 1;
-        }
+        if (mine) issue(mine - 1, kg);
       }
       for (int i = mine - 1; i >= 0; --i) {
         if constexpr (MODE == 1) {
-          if (next >= 0) {
-            issue(next, g, stage == kMassRing - 1 ? 0 : stage + 1);
-            --next;
+          if (i > 0) {
+            issue(i - 1, kg);
+            HK_WAIT_VM(OPS);
+          } else {
+            HK_WAIT_VM(0);
           }
-          await(min(kMassRing - 1, i));
-        } else {
-          await(min(kMassRing - 1, max(0, i - (next + 1))));
+        } else if (i < mine - 2) {  // fetched since: one younger block at most
+          if (i > 0) HK_WAIT_VM(OPS);
+          else HK_WAIT_VM(0);
         }
         bf16x8 f[NK];
-        frags(stage, f);
+        frags(i, f);
         if constexpr (MODE == 2) {
-          if (next >= 0) {  // this stage has been read: the block kMassRing before this one goes there
-            issue(next, g, stage);
-            --next;
-          }
+          if (i >= 2) issue(i - 2, kg);  // into the stage that has just been read
         }
-        float o = 0.0f;
+        float o = 0.0f;  // lane: heads 4 grp .. + 3 of each tile, key col
 #pragma unroll
         for (int t = 0; t < PT; ++t) {
           f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -489,16 +498,17 @@ __global__ void __launch_bounds__(kMassThreads, 3) mass_staged_kernel(MassArgs a
 #pragma unroll
           for (int e = 0; e < 4; ++e) o = fmaf(exp2_fast(fmaf(acc[e], a.scale2, -m[e])), r[e], o);
         }
-        o += __shfl_xor(o, 16);
-        o += __shfl_xor(o, 32);
-        const int j = (wave + i * kMassWaves) * 16 + col;
-        if (grp == 0) sums[j] = ids[j] >= 0 ? (c0 ? sums[j] + o : o) : 0.0f;
-        stage = stage == 0 ? kMassRing - 1 : stage - 1;
+        o = add_rows(o);
+        if (grp == 0) {  // the wave's own entries: no other wave reads or writes them
+          const int blk = wave + i * W, j = blk * 16 + col;
+          const bool on = (live16[blk] >> col) & 1;
+          sums[j] = on ? __float_as_uint(c0 ? __uint_as_float(sums[j]) + o : o) : 0u;
+        }
       }
       if (last) {
         __syncthreads();
         for (int j = tid; j < nj; j += kMassThreads)
-          a.mass[(int64_t)q * a.topk + j0 + j] = sums[j] * a.inv_heads;
+          a.mass[(int64_t)q * a.topk + j0 + j] = __uint_as_float(sums[j]) * a.inv_heads;
       }
     }
     c0 += nt;
@@ -511,7 +521,9 @@ __global__ void __launch_bounds__(kMassThreads, 3) mass_staged_kernel(MassArgs a
 template <int NK, int PT, int MODE>
 hipError_t mass_staged_launch(const MassArgs& a, hipStream_t s) {
   static LdsLimit lim;
-  const int lds = kMassRing * kMassWaves * 16 * NK * 64 + PT * 16 * (8 + 8 * kMassWaves) + a.split_len * 8;
+  const bool passes = mass_rows(a.heads, a.groups) > PT * 16;
+  const int lds = 2 * kMassWaves * 16 * NK * 64 + PT * 16 * (8 + 8 * kMassWaves) + a.split_len / 8 +
+                  a.split_len * (passes ? 8 : 4);
   hipError_t e = raise_dynamic_lds((const void*)mass_staged_kernel<NK, PT, MODE>, lds, lim);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((mass_staged_kernel<NK, PT, MODE>), dim3((unsigned)a.n, (unsigned)a.nsplit),
@@ -527,7 +539,7 @@ hipError_t mass_staged_pt(const MassArgs& a, hipStream_t s) {
   return e != hipSuccess ? e : mass_staged_launch<NK, PT, 1>(a, s);
 }
 
-// Tiles of a pass: those of a key head, up to four (q rows in 16 NK registers a tile).
+// Tiles of a pass: those of a key head, up to four (q rows in 4 NK registers a tile).
 template <int NK>
 hipError_t mass_staged(const MassArgs& a, hipStream_t s) {
   const int tiles = HeadTiles(a.heads, a.groups).tiles;
@@ -560,6 +572,7 @@ hipError_t mass_d(const MassArgs& a, hipStream_t s) {
 
 }  // namespace
 
+
 int64_t mass_rows(int heads, int groups) { return (int64_t)groups * HeadTiles(heads, groups).tiles * 16; }
 
 // Splits of a query's entries so that few queries still fill the chip: about
@@ -577,10 +590,12 @@ bool mass_supports(int d) {
 
 hipError_t launch_attention_mass(const MassArgs& a, int d, hipStream_t s) {
   if (a.n <= 0) return hipSuccess;
+  // the staged kernels count key rows in 16-byte pieces of 32 bits: tables below 64 GiB
+  const bool pieces = (int64_t)a.L * a.groups * (d / 8) < int64_t(1) << 32;
   switch (d) {
-    case 64: return mass_staged<2>(a, s);
+    case 64: return pieces ? mass_staged<2>(a, s) : mass_d<2>(a, s);
     case 96: return mass_d<3>(a, s);
-    case 128: return mass_staged<4>(a, s);
+    case 128: return pieces ? mass_staged<4>(a, s) : mass_d<4>(a, s);
     case 192: return mass_d<6>(a, s);
     case 256: return mass_d<8>(a, s);
     case 512: return mass_d<16>(a, s);

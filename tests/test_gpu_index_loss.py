@@ -61,8 +61,34 @@ CASES = [  # n, k, heads, key heads, d, L
     (1, 1, 1, 1, 64, 5), (3, 17, 5, 1, 128, 100), (2, 64, 64, 1, 128, 300), (1, 2048, 64, 1, 128, 3000),
     (4, 333, 32, 4, 64, 400), (2, 100, 40, 8, 128, 200), (3, 65, 16, 16, 96, 90), (2, 129, 128, 1, 576, 200),
     (2, 40, 20, 1, 512, 64), (5, 250, 24, 2, 256, 300), (2, 500, 144, 1, 192, 600), (1, 130, 256, 2, 64, 140),
-    (70, 100, 8, 1, 64, 200), (1100, 20, 4, 2, 64, 64), (9, 16, 17, 1, 128, 40), (2, 15, 200, 200, 64, 33),
+    (70, 100, 8, 1, 64, 200), (1100, 20, 4, 2, 64, 64), (1030, 300, 33, 1, 64, 200), (1030, 90, 64, 1, 128, 100), (9, 16, 17, 1, 128, 40), (2, 15, 200, 200, 64, 33),
 ]
+
+
+LONG = [  # enough queries for one workgroup each, k up to the longest: (k, heads, key heads, d)
+    (2048, 64, 1, 128), (2047, 48, 1, 128), (1300, 16, 1, 64), (2000, 40, 2, 64), (777, 100, 1, 128),
+    (2048, 8, 2, 64), (1025, 30, 1, 128), (640, 128, 2, 64), (129, 64, 1, 64),
+]
+
+
+@pytest.mark.parametrize("case", LONG)
+def test_mass_of_long_rows_of_many_queries(hk, case):
+    """One workgroup a query (over 512 queries): statistics and mass together, some of the logits and
+    keys kept between them.  A few queries, padded ones among them, against the definition, every
+    row's sum, and the same rows computed for few queries (several workgroups each)."""
+    k, heads, groups, d = case
+    n, L = 1030, 3000
+    say(f"mass: {case} n={n}")
+    q, keys, idx = _inputs(n, k, heads, groups, d, L, sum(case), pad=0.5)
+    out = hk.attention_mass(q.cuda(), keys.cuda(), idx.cuda())
+    some = torch.tensor([0, 1, 2, 500, 1029])
+    _mass_check(out[some], q[some], keys, idx[some], d ** -0.5)
+    few = hk.attention_mass(q[some].cuda(), keys.cuda(), idx[some].cuda())
+    _mass_check(few, q[some], keys, idx[some], d ** -0.5)
+    live = (idx >= 0).any(1)
+    # a row's sum: k terms, each off by its bound above (below 2^-11 for these logits), and the sum itself
+    total = out.double().sum(1).cpu()
+    assert (total[live] - 1).abs().max() < 2.0 ** -11 and not total[~live].any()
 
 
 @pytest.mark.parametrize("case", CASES)
@@ -115,6 +141,13 @@ def test_mass_of_sharp_and_flat_rows(hk):
     _mass_check(out, q, keys, idx, 0.5)
     flat = hk.attention_mass(q.cuda(), keys.cuda(), idx.cuda(), softmax_scale=0.0)
     assert torch.allclose(flat.cpu(), torch.full((n, k), 1 / k), rtol=1e-5)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2])
+def test_mass_of_padded_rows_at_any_scale(hk, scale):
+    q, keys, idx = _inputs(5, 130, 24, 1, 128, 90, 15, pad=1.0)
+    idx[:, 3::7] = -1
+    _mass_check(hk.attention_mass(q.cuda(), keys.cuda(), idx.cuda(), softmax_scale=scale), q, keys, idx, scale)
 
 
 def test_mass_is_the_same_bits_every_time_and_for_any_batch(hk):
