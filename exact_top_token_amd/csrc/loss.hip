@@ -287,6 +287,9 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(MassArgs a, int pass
 // (MODE 2) the mass walks the wave's blocks from the last to the first, so that the
 // rows still in LDS and in the caches are used again.
 //
+// gw waves (1, 2 or 4) take key heads side by side, the others the blocks: with short splits of
+// several key heads the passes over them, each a few dependent loads long, run at once.
+//
 // What bounds it is the rate of instructions of a SIMD (per block of 16 entries and 64 heads of 128:
 // 16 MFMAs, 16 exponentials, 32 fused multiplies) and, where the keys come from the
 // memory-side cache, its 8.2 TB/s.  So waves count for more than loads in flight or
@@ -295,7 +298,7 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(MassArgs a, int pass
 // that kept five of sixteen blocks' logits in registers and four stages in LDS,
 // for 44% fewer bytes, 301.
 template <int NK, int PT, int MODE>
-__global__ void __launch_bounds__(kMassThreads, 3) mass_staged_kernel(MassArgs a) {
+__global__ void __launch_bounds__(kMassThreads, 3) mass_staged_kernel(MassArgs a, int gw) {
   constexpr int D = NK * 32, RB = D * 2, NCH = RB / 16, OPS = 16 * RB / 1024;
   constexpr int KPI = 1024 / RB;  // rows of a load
   constexpr int W = kMassWaves;
@@ -303,19 +306,23 @@ __global__ void __launch_bounds__(kMassThreads, 3) mass_staged_kernel(MassArgs a
   const HeadTiles ht(a.heads, a.groups);
   const int T = a.groups * ht.tiles;
   uint8_t* ring = lds;                                                // [2][waves][16 rows]
-  float* ms = reinterpret_cast<float*>(ring + 2 * W * 16 * RB);       // [PT * 16]
-  float* rs = ms + PT * 16;                                           // [PT * 16]
-  float2* red = reinterpret_cast<float2*>(rs + PT * 16);              // [waves][PT * 16]
+  float* ms = reinterpret_cast<float*>(ring + 2 * W * 16 * RB);       // [gw][PT * 16]
+  float* rs = ms + gw * PT * 16;                                      // [gw][PT * 16]
+  float2* red = reinterpret_cast<float2*>(rs + gw * PT * 16);         // [waves][PT * 16]
   uint64_t* live64 = reinterpret_cast<uint64_t*>(red + W * PT * 16);  // [split_len / 64] live entries
   // [split_len] where an entry's key row begins, in 16-byte pieces (padding: row 0, which no live
   // entry uses)
   uint32_t* rows_at = reinterpret_cast<uint32_t*>(live64 + a.split_len / 64);
-  // [split_len] fp32 bits; with one pass each sum takes the place of its row, which is through by then
+  // [gw][split_len] fp32 bits; with one pass each sum takes the place of its row, which is through by then
   uint32_t* sums = rows_at + (T > PT ? a.split_len : 0);
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, grp = lane >> 4;
+  const int gi = wave & (gw - 1), bi = wave / gw, bw = W / gw;
+  ms += gi * PT * 16;
+  rs += gi * PT * 16;
+  sums += gi * a.split_len;
   const int q = [] {  // a contiguous run of queries per XCD
     const int nx = 8, b = blockIdx.x, x = b % nx;
     const int base = (int)gridDim.x / nx, extra = (int)gridDim.x % nx;
@@ -331,7 +338,7 @@ __global__ void __launch_bounds__(kMassThreads, 3) mass_staged_kernel(MassArgs a
     if (lane == 0) live64[j >> 6] = live;
   }
   const int nblk = (nj + 15) / 16;
-  const int mine = wave < nblk ? (nblk - wave + W - 1) / W : 0;  // wave-uniform
+  const int have = bi < nblk ? (nblk - bi + bw - 1) / bw : 0;  // blocks of this wave: bi + i * bw
   uint8_t* const ring0 = ring + wave * 16 * RB;  // stage s: + s * SLOT
   constexpr int SLOT = W * 16 * RB;
   int dsw[OPS];  // load p fetches this chunk of its row (the stage's swizzle)
@@ -339,13 +346,13 @@ __global__ void __launch_bounds__(kMassThreads, 3) mass_staged_kernel(MassArgs a
   for (int p = 0; p < OPS; ++p) dsw[p] = 16 * ((lane % NCH) ^ key_swz<NCH>(p * KPI + lane / NCH));
   typedef uint16_t __attribute__((may_alias)) live_bits;
   const live_bits* live16 = reinterpret_cast<const live_bits*>(live64);
-  const uint32_t* my_rows = rows_at + wave * 16 + lane / NCH;
+  const uint32_t* my_rows = rows_at + bi * 16 + lane / NCH;
   // the wave's i-th block, from kg (the key head's first byte), into its stage i % 2
   auto issue = [&](int i, const uint8_t* kg) {
     uint8_t* to = ring0 + (i & 1) * SLOT;
 #pragma unroll
     for (int p = 0; p < OPS; ++p)
-      lds_dma16(kg + dsw[p] + ((uint64_t)my_rows[i * W * 16 + p * KPI] << 4), to + p * 1024);
+      lds_dma16(kg + dsw[p] + ((uint64_t)my_rows[i * bw * 16 + p * KPI] << 4), to + p * 1024);
   };
   const uint32_t ring_at = lds_addr(ring0);
   uint32_t chunk_at[NK];
@@ -361,9 +368,12 @@ __global__ void __launch_bounds__(kMassThreads, 3) mass_staged_kernel(MassArgs a
     for (int s = 0; s < NK; ++s) f[s] = __builtin_bit_cast(bf16x8, r[s]);
   };
 
-  for (int c0 = 0, g = 0, ta = 0; c0 < T;) {
-    const int nt = min(PT, ht.tiles - ta);  // tiles of this pass: ta .. ta + nt - 1 of key head g
-    const bool last = c0 + nt == T;
+  for (int gp = 0, ta = 0; gp < a.groups;) {
+    // tiles of this pass: ta .. ta + nt - 1 of key head g, c0 on of the query
+    const int g = gp + gi, c0 = g * ht.tiles + ta;
+    const bool in = g < a.groups, first = gp == 0 && ta == 0;
+    const int nt = in ? min(PT, ht.tiles - ta) : 0, mine = in ? have : 0;
+    const bool last = gp + gw >= a.groups && ta + PT >= ht.tiles;
     const uint8_t* kg = reinterpret_cast<const uint8_t*>(a.k) + g * RB;
     bf16x8 qf[PT][NK];
 #pragma unroll
@@ -375,7 +385,7 @@ __global__ void __launch_bounds__(kMassThreads, 3) mass_staged_kernel(MassArgs a
         qf[t][s] = h >= 0 ? *reinterpret_cast<const bf16x8*>(p + s * 32) : bf16x8{};
     }
     if constexpr (MODE == 1) {
-      for (int r = tid; r < PT * 16; r += kMassThreads) {
+      for (int r = bi * kWave + lane; r < PT * 16; r += bw * kWave) {  // the waves of this key head
         const int h = (r >> 4) < nt ? ht.head(c0 + (r >> 4), r & 15) : -1;
         float m = 0.0f, rl = 0.0f;
         if (h >= 0 && a.lse) {
@@ -409,7 +419,7 @@ __global__ void __launch_bounds__(kMassThreads, 3) mass_staged_kernel(MassArgs a
         bf16x8 f[NK];
         frags(i, f);
         // lane: keys 4 grp .. + 3 of the block, head col of each tile
-        const unsigned all = __builtin_amdgcn_readfirstlane(live16[wave + i * W]), live = all >> (4 * grp);
+        const unsigned all = __builtin_amdgcn_readfirstlane(live16[bi + i * bw]), live = all >> (4 * grp);
 #pragma unroll
         for (int t = 0; t < PT; ++t) {
           f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -447,10 +457,9 @@ __global__ void __launch_bounds__(kMassThreads, 3) mass_staged_kernel(MassArgs a
         if (grp == 0) red[wave * PT * 16 + t * 16 + col] = p;
       }
       __syncthreads();
-      for (int r = tid; r < PT * 16; r += kMassThreads) {
-        float2 p = red[r];
-#pragma unroll
-        for (int w = 1; w < W; ++w) p = join(p, red[w * PT * 16 + r]);
+      for (int r = bi * kWave + lane; r < PT * 16; r += bw * kWave) {
+        float2 p = red[gi * PT * 16 + r];
+        for (int w = 1; w < bw; ++w) p = join(p, red[(gi + w * gw) * PT * 16 + r]);
         if constexpr (MODE == 0) {
           if (r < nt * 16) a.part[((int64_t)q * a.nsplit + split) * (T * 16) + c0 * 16 + r] = p;
         } else {
@@ -500,20 +509,23 @@ __global__ void __launch_bounds__(kMassThreads, 3) mass_staged_kernel(MassArgs a
         }
         o = add_rows(o);
         if (grp == 0) {  // the wave's own entries: no other wave reads or writes them
-          const int blk = wave + i * W, j = blk * 16 + col;
+          const int blk = bi + i * bw, j = blk * 16 + col;
           const bool on = (live16[blk] >> col) & 1;
-          sums[j] = on ? __float_as_uint(c0 ? __uint_as_float(sums[j]) + o : o) : 0u;
+          sums[j] = on ? __float_as_uint(first ? o : __uint_as_float(sums[j]) + o) : 0u;
         }
       }
       if (last) {
         __syncthreads();
-        for (int j = tid; j < nj; j += kMassThreads)
-          a.mass[(int64_t)q * a.topk + j0 + j] = __uint_as_float(sums[j]) * a.inv_heads;
+        const uint32_t* all = sums - gi * a.split_len;
+        for (int j = tid; j < nj; j += kMassThreads) {
+          float o = __uint_as_float(all[j]);
+          for (int k = 1; k < gw; ++k) o += __uint_as_float(all[k * a.split_len + j]);
+          a.mass[(int64_t)q * a.topk + j0 + j] = o * a.inv_heads;
+        }
       }
     }
-    c0 += nt;
-    ta += nt;
-    if (ta == ht.tiles) { ta = 0; ++g; }
+    ta += PT;
+    if (ta >= ht.tiles) { ta = 0; gp += gw; }
     if (!last) __syncthreads();
   }
 }
@@ -521,13 +533,16 @@ __global__ void __launch_bounds__(kMassThreads, 3) mass_staged_kernel(MassArgs a
 template <int NK, int PT, int MODE>
 hipError_t mass_staged_launch(const MassArgs& a, hipStream_t s) {
   static LdsLimit lim;
-  const bool passes = mass_rows(a.heads, a.groups) > PT * 16;
-  const int lds = 2 * kMassWaves * 16 * NK * 64 + PT * 16 * (8 + 8 * kMassWaves) + a.split_len / 8 +
-                  a.split_len * (passes ? 8 : 4);
+  // Key heads side by side as long as their sums take no more LDS than one row of 2,048.
+  int gw = 1;
+  while (gw < kMassWaves && 2 * gw <= a.groups && 2 * gw * a.split_len <= 2048) gw *= 2;
+  const bool apart = mass_rows(a.heads, a.groups) > PT * 16;  // sums beside the rows
+  const int lds = 2 * kMassWaves * 16 * NK * 64 + PT * 16 * 8 * (gw + kMassWaves) + a.split_len / 8 +
+                  a.split_len * 4 * (apart ? 1 + gw : 1);
   hipError_t e = raise_dynamic_lds((const void*)mass_staged_kernel<NK, PT, MODE>, lds, lim);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((mass_staged_kernel<NK, PT, MODE>), dim3((unsigned)a.n, (unsigned)a.nsplit),
-                     dim3(kMassThreads), (size_t)lds, s, a);
+                     dim3(kMassThreads), (size_t)lds, s, a, gw);
   return hipGetLastError();
 }
 
