@@ -546,16 +546,16 @@ class Rotary:
             raise ValueError(f"unknown rotary layout {layout!r}")
         if scaling not in _SCALINGS:
             raise ValueError(f"unknown rotary scaling {scaling!r}")
+        dim, first, original = int(dim), int(first), int(original)
+        if not (0 < dim < 1 << 31 and 0 <= first < 1 << 31):
+            raise ValueError("dim must be > 0 and first >= 0, both below 2^31")
         lib = load_library()
-        freq = torch.empty(max(int(dim) // 2, 1), dtype=torch.float64)
+        freq = torch.empty(max(min(dim, 1024) // 2, 1), dtype=torch.float64)
         gain = ctypes.c_double()
-        _check(lib.hytopk_rotary_frequencies(int(dim), float(base), _SCALINGS[scaling],
-                                             float(factor), int(original), _ptr(freq),
-                                             ctypes.byref(gain)))
-        if int(first) < 0:
-            raise ValueError("first must be >= 0")
+        _check(lib.hytopk_rotary_frequencies(dim, float(base), _SCALINGS[scaling], float(factor),
+                                             original, _ptr(freq), ctypes.byref(gain)))
         self.freq = freq.to(device)
-        self.gain, self.dim, self.first, self.layout = gain.value, int(dim), int(first), layout
+        self.gain, self.dim, self.first, self.layout = gain.value, dim, first, layout
         self._plan = RotaryPlan(self.freq.data_ptr(), self.gain, self.dim, self.first,
                                 _LAYOUTS[layout], 0)
 

@@ -854,9 +854,12 @@ hk::RotArgs rot_args(const hytopk_rotary_plan* p, const int32_t* q_pos, int64_t 
   return r;
 }
 
-int64_t cache_code_bytes(const hytopk_cache* c) {
+// Whether memory lies in the cache's codes or scales.
+bool in_cache(const hytopk_cache* c, Extent m) {
   const int64_t e = c->L * c->heads * c->d;
-  return c->dtype == HYTOPK_BF16 ? 2 * e : (c->dtype == HYTOPK_MXFP4_E2M1 ? e / 2 : e);
+  const int64_t codes = c->dtype == HYTOPK_BF16 ? 2 * e : (c->dtype == HYTOPK_MXFP4_E2M1 ? e / 2 : e);
+  const int64_t scale = c->dtype == HYTOPK_BF16 ? 0 : (c->dtype == HYTOPK_FP8_E4M3 ? 4 * c->L : e / 32);
+  return overlap(m, extent(c->codes, codes)) || (scale && overlap(m, extent(c->scale, scale)));
 }
 
 // The geometry alone (what the workspace query knows).
@@ -999,7 +1002,7 @@ int hytopk_cache_write(const hytopk_cache* c, int64_t n, const hytopk_rows* x,
     if ((rc = check_rows(x, n, c->heads, c->d))) return rc;
     if (plan && ((rc = check_plan(plan, c->d)) || (rc = check_positions(n, q_pos, q_start)))) return rc;
     if (n == 0) return HYTOPK_OK;
-    if (overlap(extent(x, n, c->heads, c->d), extent(c->codes, cache_code_bytes(c))))
+    if (in_cache(c, extent(x, n, c->heads, c->d)))
       return fail(HYTOPK_EINVAL, "x overlaps the cache");
     const bool claim = wants_claim(n, slots != nullptr);
     if (claim && (rc = check_ws(workspace, workspace_bytes, hytopk_cache_write_workspace(c, n, 1)))) return rc;
@@ -1035,7 +1038,7 @@ int hytopk_cache_read(const hytopk_cache* c, int64_t n, const int32_t* slots, in
     if (!out) return fail(HYTOPK_EINVAL, "out is NULL");
     if (misaligned(out, 16)) return fail(HYTOPK_EINVAL, "out must be 16-byte aligned");
     const int64_t bytes = n * c->heads * c->d * (out_dtype == HYTOPK_ROWS_BF16 ? 2 : 4);
-    if (overlap(extent(out, bytes), extent(c->codes, cache_code_bytes(c))))
+    if (in_cache(c, extent(out, bytes)))
       return fail(HYTOPK_EINVAL, "out overlaps the cache");
     hk::CacheReadArgs a{};
     a.codes = static_cast<const uint8_t*>(c->codes);

@@ -278,8 +278,8 @@ int hytopk_backward(const hytopk_problem* p, const void* q, const void* q_scale,
  *     -> hytopk_backward -> transposed rotation of dq and dk
  *
  * All of them are asynchronous on `stream`, launch kernels only (no copy, memset or
- * synchronisation: they can be recorded in a HIP graph after one eager call)
- * and hold no state between calls.  n = 0 is a valid call that does nothing.
+ * synchronisation: they can be recorded in a HIP graph after one eager call
+ * with the same shapes) and hold no state between calls.  n = 0 is a valid call that does nothing.
  * ------------------------------------------------------------------------- */
 
 /* Element types of the rows that the rotation and the cache calls read and write. */

@@ -69,7 +69,8 @@ def _empty(fmt, L, heads, d, fill=0x55):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("shape", [(1, 1, 128), (5, 1, 32), (64, 1, 128), (33, 1, 96), (7, 64, 128), (3, 3, 160),
-                                   (20, 2, 64), (2, 1, 8192), (9, 5, 320), (1500, 1, 128), (6, 1, 576)])
+                                   (20, 2, 64), (2, 1, 8192), (9, 5, 320), (1500, 1, 128), (6, 1, 576), (5, 64, 96),
+                                   (3, 40, 160), (2, 13, 576), (9000, 4, 32), (70, 32, 128)])
 def test_codes_equal_the_reference_quantiser(hk, fmt, shape):
     say(f"cache: {fmt} {shape}")
     n, heads, d = shape
@@ -203,7 +204,8 @@ def test_rows_by_start_and_both_ends_of_the_cache(hk, fmt):
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 @pytest.mark.parametrize("shape", [(50, 1, 128, 64, 0), (9, 64, 128, 128, 0), (11, 2, 96, 36, 3), (300, 1, 64, 32, 32),
-                                   (4, 1, 2048, 1024, 512)])
+                                   (4, 1, 2048, 1024, 512), (11, 2, 96, 64, 16), (5, 64, 96, 64, 32), (3, 40, 160, 64, 0),
+                                   (70, 32, 128, 64, 64), (2, 32, 256, 256, 0), (4100, 4, 32, 16, 0), (9, 3, 256, 16, 240)])
 def test_rotated_rows(hk, fmt, layout, shape):
     n, heads, d, dim, first = shape
     say(f"cache: {fmt} rotated {shape} {layout}")
@@ -260,6 +262,27 @@ def test_strided_and_unaligned_rows(hk):
             assert torch.equal(got[0], want[0]) and (want[1] is None or torch.equal(got[1], want[1]))
     with pytest.raises(hk.HytopkError):  # rows that lie in the cache itself
         hk.cache_write(base, base.view(torch.bfloat16), fmt="bf16")
+
+
+def test_long_rows_by_slot(hk):
+    """Rows of 8,192 elements (several pieces a thread, or a workgroup of 1,024): slots, padding
+    and repeats, few rows and many."""
+    for fmt in FORMATS:
+        for heads, d, n in ((64, 128, 40), (64, 128, 1100), (64, 96, 30)):
+            x = _rows(n, heads, d, 17)
+            L = 1200
+            slots = np.random.default_rng(n).integers(-2, L, n).astype(np.int32)
+            codes, scale = _empty(fmt, L, heads, d)
+            want_c, want_s = _codes(codes).copy(), None if scale is None else scale.cpu().numpy().copy()
+            hk.cache_write(x.cuda(), codes, scale, fmt=fmt, slots=torch.from_numpy(slots).cuda())
+            rc, rs = _reference(x.float().numpy(), fmt)
+            for i in range(n):
+                if slots[i] >= 0:
+                    want_c[slots[i]] = rc[i]
+                    if rs is not None:
+                        want_s[slots[i]] = rs[i]
+            assert np.array_equal(_codes(codes), want_c), (fmt, heads, d, n)
+            assert scale is None or np.array_equal(scale.cpu().numpy(), want_s)
 
 
 def test_rows_behind_32_bit_offsets(hk):

@@ -62,6 +62,8 @@ CASES = [  # n, k, heads, key heads, d, L
     (4, 333, 32, 4, 64, 400), (2, 100, 40, 8, 128, 200), (3, 65, 16, 16, 96, 90), (2, 129, 128, 1, 576, 200),
     (2, 40, 20, 1, 512, 64), (5, 250, 24, 2, 256, 300), (2, 500, 144, 1, 192, 600), (1, 130, 256, 2, 64, 140),
     (70, 100, 8, 1, 64, 200), (1100, 20, 4, 2, 64, 64), (1030, 300, 33, 1, 64, 200), (1030, 90, 64, 1, 128, 100), (9, 16, 17, 1, 128, 40), (2, 15, 200, 200, 64, 33),
+    (1, 70, 256, 1, 576, 90), (1, 33, 256, 2, 576, 50), (1, 2048, 128, 1, 576, 500), (2, 50, 1024, 2, 64, 60),
+    (1, 40, 300, 3, 512, 60),
 ]
 
 
@@ -174,6 +176,22 @@ def test_mass_behind_32_bit_offsets(hk):
     assert torch.equal(far, hk.attention_mass(q.cuda(), few.cuda(), idx.cuda()))
 
 
+def test_mass_of_a_table_beyond_64_gib(hk):
+    if torch.cuda.mem_get_info()[0] < 90 << 30:
+        pytest.skip("needs 90 GiB of GPU memory")
+    L = (1 << 28) + 50
+    keys = torch.empty((L, 1, 128), dtype=torch.bfloat16, device="cuda")
+    q, few, _ = _inputs(3, 4, 20, 1, 128, 50, 14)
+    keys[0] = 0
+    keys[L - 50:] = few.cuda()
+    idx = torch.randint(0, 50, (3, 70), generator=torch.Generator().manual_seed(2), dtype=torch.int32)
+    idx[1, 30:] = -1
+    far = hk.attention_mass(q.cuda(), keys, torch.where(idx < 0, idx, idx + (L - 50)).cuda())
+    _mass_check(far, q, few, idx, 128 ** -0.5)
+    del keys
+    torch.cuda.empty_cache()
+
+
 def _loss_tolerance(score, mass, weight):
     """fp32 error bound of loss and gradient, U = 2^-24.  With r = max - score of
     an entry and k terms: p is off by p (r + 80 + k/16) U (its argument's rounding, the
@@ -261,6 +279,22 @@ def test_not_finite_rows_show_and_stay_alone(hk):
     loss, grad = hk.index_loss(score.cuda(), mass.cuda())
     assert torch.isnan(loss[1:3]).all() and torch.isnan(grad[1:3]).all()
     assert torch.isfinite(loss[[0, 3]]).all() and torch.isfinite(grad[[0, 3]]).all()
+
+
+def test_a_large_gradient_and_many_rows(hk):
+    """Over 32 MiB of gradient (stored past the caches), rows of every live count."""
+    g = torch.Generator().manual_seed(7)
+    n, k = 4200, 2048
+    score, mass = 2 * torch.randn((n, k), generator=g), torch.rand((n, k), generator=g)
+    score[torch.arange(k) >= torch.arange(n)[:, None]] = -float("inf")
+    loss, grad = hk.index_loss(score.cuda(), mass.cuda())
+    some = torch.tensor([0, 1, 2, 63, 64, 1000, 2047, 2048, 4199])
+    rl, rg = op.index_loss(score[some].double().numpy(), mass[some].double().numpy())
+    tl, tg = _loss_tolerance(score[some].double().numpy(), mass[some].double().numpy(), None)
+    assert np.all(np.abs(loss[some].double().cpu().numpy() - rl) <= tl)
+    assert np.all(np.abs(grad[some].double().cpu().numpy() - rg) <= tg)
+    # each row's gradient sums to 0: k terms within their bound
+    assert grad.double().sum(1).abs().max() < 2.0 ** -14
 
 
 def test_gradient_against_differences(hk):

@@ -113,7 +113,7 @@ def write(lib, c=None, n=4, x=None, slots=None, start=0, p=None, pos=None, ws=No
     (dict(c=cache(heads=65)), -2), (dict(c=cache(L=1 << 31)), -2), (dict(c=cache(heads=0)), -1),
     (dict(n=-1), -1), (dict(n=1 << 31), -2), (dict(start=-1), -1), (dict(start=997), -1), (dict(n=1001), -1),
     (dict(x=rows(data=None)), -1), (dict(x=rows(dtype=3)), -1), (dict(x=rows(data=FAKE)), -1),
-    (dict(slots=FAKE + 1), -1), (dict(p=plan(dim=130)), -1), (dict(p=plan(), pos=FAKE + 2), -1),
+    (dict(c=cache(scale=FAKE + (1 << 30) + 64)), -1), (dict(slots=FAKE + 1), -1), (dict(p=plan(dim=130)), -1), (dict(p=plan(), pos=FAKE + 2), -1),
     # more rows by slot than look for later ones by themselves take a workspace
     (dict(c=cache(L=1 << 20), n=2000, slots=FAKE), -3),
     (dict(c=cache(L=1 << 20), n=2000, slots=FAKE, ws=FAKE, wb=(4 << 20) - 1), -3),
@@ -201,6 +201,9 @@ def test_binding_refusals_without_a_gpu():
         hk.Rotary(64, scaling="cubic", device="cpu")
     with pytest.raises(hk.HytopkError):
         hk.Rotary(63, device="cpu")
+    for bad in (dict(dim=(1 << 32) + 64), dict(dim=64, first=-1), dict(dim=64, first=1 << 32), dict(dim=-2)):
+        with pytest.raises(ValueError):
+            hk.Rotary(**bad, device="cpu")
     with pytest.raises(ValueError):
         hk.cache_write(x, torch.zeros(8, 2, 128, dtype=torch.uint8), torch.ones(8))
     with pytest.raises(ValueError):
