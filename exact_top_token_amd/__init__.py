@@ -480,318 +480,16 @@ def backward(q, k, w, idx, d_score, *, q_scale=None, k_scale=None, q_start=None,
     return res
 
 
-# ----------------------------------------- rotary positions and the cache
-
-_LAYOUTS = {"half": 0, "interleaved": 1}
-_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
-
-
-def _launch(device, fn, *args) -> None:
-    """Calls fn(*args, stream) on the device's current stream, with that device
-    current (a call's host time is most of a small operator's, so nothing here
-    builds a stream or a guard object that is not needed)."""
-    import torch
-    index = device.index
-    if index == torch.cuda.current_device():
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    else:
-        with torch.cuda.device(device):
-            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
-    if rc != 0:
-        _check(rc)
+# The operators around the selection live in a module of their own, loaded on first use (it
+# imports torch, which the build does not need).
+_OPERATORS = ("Rotary", "rotary", "cache_write", "cache_read", "cache_write_workspace_bytes",
+              "quantize", "attention_mass", "attention_mass_workspace_bytes", "index_loss")
 
 
-def _gpu(t, name: str) -> None:
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on the GPU")
-
-
-def _rows_array(t, name: str):
-    """[n][d] or [n][heads][d] rows of bf16 or fp32, any strides but the last."""
-    import torch
-    dtype, stride = t.dtype, t.stride()
-    if dtype != torch.bfloat16 and dtype != torch.float32:
-        raise TypeError(f"{name} must be bfloat16 or float32, got {dtype}")
-    axes = len(stride)
-    if axes != 2 and axes != 3:
-        raise ValueError(f"{name} must be [n][d] or [n][heads][d], got {tuple(t.shape)}")
-    if stride[-1] != 1 and t.shape[-1] > 1:
-        raise ValueError(f"the last axis of {name} must be contiguous")
-    return RowsArray(t.data_ptr(), stride[0], stride[1] if axes == 3 else 0,
-                     0 if dtype == torch.bfloat16 else 1, 0)
-
-
-def _address(t):
-    return None if t is None else t.data_ptr()
-
-
-def _ints(t, name: str, n: int, device) -> None:
-    import torch
-    if t is not None:
-        _need(t, name, (n,), torch.int32, device)
-
-
-class Rotary:
-    """A rotation of elements ``first .. first + dim - 1`` of every head: the
-    frequencies (``freq``, float64 on the GPU) and the factor on the rotated
-    part (``gain``), made once and kept for every call.  ``layout`` pairs
-    elements (i, i + dim/2) ("half") or (2i, 2i + 1) ("interleaved");
-    ``scaling`` ("none", "linear", "ntk", "yarn") stretches the positions by
-    ``factor`` for a model whose positions reached ``original`` before."""
-
-    def __init__(self, dim: int, *, first: int = 0, layout: str = "half", base: float = 10000.0,
-                 scaling: str = "none", factor: float = 1.0, original: int = 0, device="cuda"):
-        import torch
-        if layout not in _LAYOUTS:
-            raise ValueError(f"unknown rotary layout {layout!r}")
-        if scaling not in _SCALINGS:
-            raise ValueError(f"unknown rotary scaling {scaling!r}")
-        dim, first, original = int(dim), int(first), int(original)
-        if not (0 < dim < 1 << 31 and 0 <= first < 1 << 31):
-            raise ValueError("dim must be > 0 and first >= 0, both below 2^31")
-        lib = load_library()
-        freq = torch.empty(max(min(dim, 1024) // 2, 1), dtype=torch.float64)
-        gain = ctypes.c_double()
-        _check(lib.hytopk_rotary_frequencies(dim, float(base), _SCALINGS[scaling], float(factor),
-                                             original, _ptr(freq), ctypes.byref(gain)))
-        self.freq = freq.to(device)
-        self.gain, self.dim, self.first, self.layout = gain.value, dim, first, layout
-        self._plan = RotaryPlan(self.freq.data_ptr(), self.gain, self.dim, self.first,
-                                _LAYOUTS[layout], 0)
-
-
-def _plan(rot, device):
-    if rot is None:
-        return None
-    if rot.freq.device != device:
-        raise ValueError(f"the rotary plan is on {rot.freq.device}, the rows on {device}")
-    return rot._plan
-
-
-def rotary(x, rot: Rotary, *, q_start: int = 0, q_pos=None, backward: bool = False, out=None,
-           out_dtype=None):
-    """Rotary positions of rows x [n][d] or [n][heads][d] (bf16 or fp32, any
-    strides but the last).  Token i sits at ``q_pos[i]`` (int32 [n] on the GPU) or
-    ``q_start + i``.  ``backward`` applies the transposed rotation, which
-    takes a gradient of the result to one of x.  ``out`` may be x itself."""
-    import torch
-    lib = _LIB or load_library()
-    _gpu(x, "x")
-    xa = _rows_array(x, "x")
-    shape, device = x.shape, x.device
-    n, d = shape[0], shape[-1]
-    heads = shape[1] if len(shape) == 3 else 1
-    if out is None:
-        out = x.new_empty(shape, dtype=out_dtype)
-    elif out.shape != x.shape or out.device != x.device or out_dtype not in (None, out.dtype):
-        raise ValueError(f"out must have x's shape {tuple(x.shape)} and device, and out_dtype")
-    ya = _rows_array(out, "out")
-    _ints(q_pos, "q_pos", n, device)
-    _launch(device, lib.hytopk_rotary, _plan(rot, device), n, heads, d, xa, ya, _address(q_pos),
-            int(q_start), 1 if backward else 0)
-    return out
-
-
-def _cache(codes, scale, fmt):
-    """codes [L][d] or [L][heads][d] (MXFP4: the last axis holds d/2 bytes) and
-    scales as ``select`` takes them."""
-    import torch
-    _gpu(codes, "codes")
-    code = _dtype_code(codes, fmt)
-    shape = codes.shape
-    axes = len(shape)
-    if axes != 2 and axes != 3:
-        raise ValueError(f"codes must be [L][d] or [L][heads][d], got {tuple(shape)}")
-    if not codes.is_contiguous():
-        raise ValueError("codes must be contiguous")
-    dtype = codes.dtype
-    if dtype != (torch.bfloat16 if code == BF16 else torch.uint8) and not (
-            code == FP8_E4M3 and dtype == torch.float8_e4m3fn):
-        raise ValueError(f"codes of type {dtype} do not hold this format")
-    L, last = shape[0], shape[-1]
-    heads = shape[1] if axes == 3 else 1
-    d = 2 * last if code == MXFP4_E2M1 else last
-    if code == BF16:
-        if scale is not None:
-            raise ValueError("a bf16 cache takes no scale")
-        return Cache(codes.data_ptr(), None, L, heads, d, code, 0)
-    if scale is None:
-        raise ValueError("fp8 and MX caches need scale")
-    if code == FP8_E4M3:
-        _need(scale, "scale", (L,), torch.float32, codes.device)
-    else:
-        _need(scale, "scale", (*shape[:-1], d // 32), torch.uint8, codes.device)
-    return Cache(codes.data_ptr(), scale.data_ptr(), L, heads, d, code, 0)
-
-
-def cache_write_workspace_bytes(codes, scale, n: int, *, fmt=None) -> int:
-    """Workspace bytes of a cache_write of n rows by slot (0: none)."""
-    return int(load_library().hytopk_cache_write_workspace(
-        ctypes.byref(_cache(codes, scale, fmt)), n, 1))
-
-
-def cache_write(x, codes, scale=None, *, fmt=None, start: int = 0, slots=None, rotary=None,
-                q_start: int = 0, q_pos=None, workspace=None) -> None:
-    """Quantise rows x ([n][d] or [n][heads][d], bf16 or fp32, any strides but the
-    last) into cache rows ``slots[i]`` (int32 [n] on the GPU; rows outside the
-    cache are padding and skipped; the last of several rows of one slot is
-    kept) or ``start + i``.  ``codes`` and ``scale`` are laid out as ``select`` takes them
-    (``fmt`` as there).  ``rotary`` (a Rotary) rotates the rows first, at positions
-    ``q_pos`` / ``q_start + i``."""
-    import torch
-    lib = _LIB or load_library()
-    c = _cache(codes, scale, fmt)
-    xa = _rows_array(x, "x")
-    n = x.shape[0]
-    device, shape = x.device, x.shape
-    if device != codes.device:
-        raise ValueError(f"x is on {device}, the cache on {codes.device}")
-    if shape[-1] != c.d or (shape[1] if len(shape) == 3 else 1) != c.heads:
-        raise ValueError(f"x {tuple(shape)} does not fit cache rows of {c.heads} x {c.d}")
-    _ints(slots, "slots", n, device)
-    _ints(q_pos, "q_pos", n, device)
-    if workspace is None and slots is not None:
-        need = lib.hytopk_cache_write_workspace(c, n, 1)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    if workspace is not None:
-        _workspace(workspace, device)
-    _launch(device, lib.hytopk_cache_write, c, n, xa, _address(slots), int(start),
-            _plan(rotary, device), _address(q_pos), int(q_start), _address(workspace),
-            0 if workspace is None else workspace.numel())
-
-
-def quantize(x, fmt: str, *, rotary=None, q_start: int = 0, q_pos=None):
-    """Rows x ([n][d] or [n][heads][d]) in a storage format of ``select``: new
-    (codes, scale), scale None for "bf16".  ``rotary`` as in ``cache_write``."""
-    import torch
-    if fmt not in _FMT:
-        raise ValueError(f"unknown format {fmt!r}")
-    _gpu(x, "x")
-    code, shape, d = _FMT[fmt], tuple(x.shape), x.shape[-1]
-    if code != BF16 and d % 32:
-        raise ValueError("quantised rows need d in multiples of 32")
-    codes = torch.empty(shape[:-1] + (d // 2 if code == MXFP4_E2M1 else d,), device=x.device,
-                        dtype=torch.bfloat16 if code == BF16 else torch.uint8)
-    scale = None
-    if code == FP8_E4M3:
-        scale = torch.empty(shape[0], dtype=torch.float32, device=x.device)
-    elif code != BF16:
-        scale = torch.empty(shape[:-1] + (d // 32,), dtype=torch.uint8, device=x.device)
-    if shape[0]:
-        cache_write(x, codes, scale, fmt=fmt, rotary=rotary, q_start=q_start, q_pos=q_pos)
-    return codes, scale
-
-
-def cache_read(codes, scale=None, *, fmt=None, slots=None, start: int = 0, count=None,
-               dtype=None, out=None):
-    """Cache rows decoded: rows ``slots`` (int32 [n] on the GPU; rows outside the cache read as
-    zeros) or ``start .. start + count - 1`` (to the end by default), as [n][d]
-    or [n][heads][d] of ``dtype`` (bf16 by default, or fp32)."""
-    import torch
-    lib = _LIB or load_library()
-    c = _cache(codes, scale, fmt)
-    n = slots.shape[0] if slots is not None else (c.L - int(start) if count is None else int(count))
-    if count is not None and n != count:
-        raise ValueError(f"count {count} differs from the {n} slots")
-    _ints(slots, "slots", n, codes.device)
-    shape = (n, c.d) if codes.dim() == 2 else (n, c.heads, c.d)
-    device = codes.device
-    if out is None:
-        if n < 0:
-            raise ValueError("start lies behind the cache")
-        out = codes.new_empty(shape, dtype=dtype or torch.bfloat16)
-    else:
-        _need(out, "out", shape, dtype or out.dtype, device)
-    dtype = out.dtype
-    if dtype != torch.bfloat16 and dtype != torch.float32:
-        raise TypeError(f"rows are read as bfloat16 or float32, got {dtype}")
-    _launch(device, lib.hytopk_cache_read, c, n, _address(slots), int(start), out.data_ptr(),
-            0 if dtype == torch.bfloat16 else 1)
-    return out
-
-
-# ------------------------------------------- the indexer's target and loss
-
-def _attention(q, k, idx, softmax_scale) -> Attention:
-    """q [n][heads][d], k [L][key_heads][d] or [L][d], idx [n][k]."""
-    import torch
-    if q.dim() != 3 or k.dim() not in (2, 3) or k.shape[-1] != q.shape[-1]:
-        raise ValueError("shapes must be q [n][heads][d], k [L][key_heads][d] or [L][d]")
-    device = q.device
-    for t, name in ((q, "q"), (k, "k")):
-        if t.dtype != torch.bfloat16 or not t.is_cuda or not t.is_contiguous() or t.device != device:
-            raise ValueError(f"{name} must be contiguous bfloat16 on one GPU")
-    n, heads, d = q.shape
-    rows = k.shape
-    if idx.dim() != 2:
-        raise ValueError("idx must be [n][k]")
-    count = idx.shape[1]
-    _need(idx, "idx", (n, count), torch.int32, device)
-    scale = d ** -0.5 if softmax_scale is None else float(softmax_scale)
-    return Attention(rows[0], n, heads, rows[1] if len(rows) == 3 else 1, d, count, scale, 0)
-
-
-def attention_mass_workspace_bytes(q, k, idx) -> int:
-    """Workspace bytes of attention_mass without lse."""
-    return int(load_library().hytopk_attention_mass_workspace(
-        ctypes.byref(_attention(q, k, idx, None))))
-
-
-def attention_mass(q, k, idx, *, softmax_scale=None, lse=None, workspace=None, out=None):
-    """The attention's probability at the selected entries idx [n][k], averaged
-    over heads (fp32 [n][k]; 0 at padding): the target of ``index_loss``.
-    q [n][heads][d] and k [L][key_heads][d] (or [L][d]) are the attention's, bf16;
-    ``softmax_scale`` is d ** -0.5 by default; ``lse`` (fp32 [n][heads]) is the attention's
-    log-sum-exp, by default taken over the row's entries."""
-    import torch
-    lib = _LIB or load_library()
-    p = _attention(q, k, idx, softmax_scale)
-    device = q.device
-    if lse is not None:
-        _need(lse, "lse", (p.n, p.heads), torch.float32, device)
-    if out is None:
-        out = q.new_empty((p.n, p.k), dtype=torch.float32)
-    else:
-        _need(out, "out", (p.n, p.k), torch.float32, device)
-    if workspace is None and lse is None:
-        workspace = torch.empty(max(lib.hytopk_attention_mass_workspace(p), 1), dtype=torch.uint8,
-                                device=device)
-    if workspace is not None:
-        _workspace(workspace, device)
-    _launch(device, lib.hytopk_attention_mass, p, q.data_ptr(), k.data_ptr(), idx.data_ptr(),
-            _address(lse), out.data_ptr(), _address(workspace),
-            0 if workspace is None else workspace.numel())
-    return out
-
-
-def index_loss(score, mass, *, weight=None, want=("loss", "d_score"), out=None):
-    """The indexer's loss per query and its gradient: the divergence of
-    softmax(score) from mass / sum(mass) over the entries whose score is not -inf,
-    times ``weight`` (fp32 [n], 1 by default).  score (``replay``'s) and mass
-    (``attention_mass``'s) are fp32 [n][k].  Returns (loss [n], d_score [n][k]),
-    None for one that ``want`` leaves out; ``backward`` takes d_score.  ``out`` gives
-    the two tensors instead (either may be None; d_score may be score or mass)."""
-    import torch
-    lib = _LIB or load_library()
-    _gpu(score, "score")
-    if score.dim() != 2:
-        raise ValueError("score must be [n][k]")
-    n, k = score.shape
-    dev = score.device
-    _need(score, "score", (n, k), torch.float32, dev)
-    _need(mass, "mass", (n, k), torch.float32, dev)
-    if weight is not None:
-        _need(weight, "weight", (n,), torch.float32, dev)
-    if out is None:
-        loss = score.new_empty(n) if "loss" in want else None
-        grad = torch.empty_like(score) if "d_score" in want else None
-    else:
-        loss, grad = out
-        if loss is not None:
-            _need(loss, "out[0] (loss)", (n,), torch.float32, dev)
-        if grad is not None:
-            _need(grad, "out[1] (d_score)", (n, k), torch.float32, dev)
-    _launch(dev, lib.hytopk_index_loss, n, k, score.data_ptr(), mass.data_ptr(), _address(weight),
-            _address(loss), _address(grad))
-    return loss, grad
+def __getattr__(name: str):
+    if name in _OPERATORS or name == "operators":
+        import importlib
+        mod = importlib.import_module(__name__ + ".operators")
+        globals().update({n: getattr(mod, n) for n in _OPERATORS})
+        return mod if name == "operators" else globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -190,11 +190,11 @@ def test_binding_refusals_without_a_gpu():
     with pytest.raises(ValueError):
         hk.rotary(x, r)
     with pytest.raises(TypeError):
-        hk._rows_array(x.half(), "x")
+        hk.operators._rows_array(x.half(), "x")
     with pytest.raises(ValueError):
-        hk._rows_array(x.transpose(1, 2), "x")
+        hk.operators._rows_array(x.transpose(1, 2), "x")
     with pytest.raises(ValueError):
-        hk._rows_array(x[0, 0], "x")
+        hk.operators._rows_array(x[0, 0], "x")
     with pytest.raises(ValueError):
         hk.Rotary(64, layout="pairs", device="cpu")
     with pytest.raises(ValueError):
