@@ -1060,7 +1060,7 @@ size_t hytopk_attention_mass_workspace(const hytopk_attention* p) {
   if (check_attention(p) != HYTOPK_OK) return 0;
   int nsplit = 1, len = 0;
   hk::mass_splits(p->n, p->k, nsplit, len);
-  const size_t parts = nsplit > 1 ? (size_t)p->n * nsplit * (size_t)hk::mass_rows(p->heads, p->key_heads) : 0;
+  const size_t parts = hk::mass_keeps_parts(p->d, nsplit) ? (size_t)p->n * nsplit * (size_t)hk::mass_rows(p->heads, p->key_heads) : 0;
   return align_up(std::max<size_t>(parts * sizeof(float2), 1));
 }
 

@@ -316,7 +316,7 @@ struct MassArgs {
   const uint16_t* k;   // bf16 [L][groups][d]
   const int* idx;      // [n][topk]
   const float* lse;    // [n][heads] natural, or null
-  float2* part;        // [n][nsplit][rows]: (max, sum) of each split (nsplit > 1, without lse)
+  float2* part;        // [n][nsplit][rows]: (max, sum) of each split (mass_keeps_parts, without lse)
   float* mass;         // [n][topk]
   int L, n, heads, groups, topk;
   float scale2;        // softmax scale * log2(e)
@@ -329,6 +329,7 @@ struct MassArgs {
 int64_t mass_rows(int heads, int groups);
 void mass_splits(int64_t n, int topk, int& nsplit, int& split_len);
 bool mass_supports(int d);
+bool mass_keeps_parts(int d, int nsplit);  // whether the statistics go through `part`
 hipError_t launch_attention_mass(const MassArgs& a, int d, hipStream_t s);
 
 struct LossArgs {

@@ -15,6 +15,7 @@ namespace {
 
 constexpr int kMassThreads = 256;
 constexpr int kMassWaves = kMassThreads / kWave;
+constexpr int kWideSteps = 16;     // k-steps of a row from which on a wave holds two blocks and no second buffer
 constexpr int kItemTiles = 8;      // head tiles whose softmax statistics a wave keeps in registers
 constexpr float kNoMax = -3.0e38f;  // maximum of nothing: finite, so that differences stay defined
 constexpr float kLazy = 8.0f;      // a maximum moves when exceeded by 2^8: sums stay below 2^19
@@ -56,19 +57,22 @@ struct HeadTiles {
   }
 };
 
-// LDS of a workgroup: per row of q, the row itself, (max, 1 / sum) and the
-// waves' (max, sum); per entry its index and, where there are several passes, its sum.
-constexpr int mass_row_bytes(int d) { return 2 * d + 8 + 8 * kMassWaves; }
+// LDS of a workgroup that gathers its keys into registers: per row of q the row itself,
+// (max, 1 / sum) for the mass and the waves' (max, sum) for the statistics; per entry its
+// index and, where there are several passes, its sum.
 constexpr int kLdsBytes = 160 * 1024;
 constexpr int kMassLongest = 2048;        // entries of a split, at most
 constexpr int kMassLdsSmall = 40 * 1024;  // enough passes to keep this where key heads allow it
+constexpr int mass_row_bytes(int d, int mode, int waves) {
+  return 2 * d + (mode != 0 ? 8 : 0) + (mode != 1 ? 8 * waves : 0);
+}
 
 // Tiles of a pass over a query's heads: whole key heads within kMassLdsSmall (their
 // keys differ, so passes cost nothing), or else as much of one key head
 // as the LDS holds (more than one pass then gathers its keys again).
-int mass_pass_tiles(int heads, int groups, int d) {
+int mass_pass_tiles(int heads, int groups, int row_bytes) {
   const HeadTiles ht(heads, groups);
-  const int tile = 16 * mass_row_bytes(d);
+  const int tile = 16 * row_bytes;
   if (groups == 1 && ht.tiles * tile <= kLdsBytes - 4 * kMassLongest) return ht.tiles;
   const int fit = (kLdsBytes - 8 * kMassLongest) / tile;
   const int small = kMassLdsSmall / tile / ht.tiles * ht.tiles;
@@ -78,12 +82,12 @@ int mass_pass_tiles(int heads, int groups, int d) {
 // MODE 0: (max, sum) of a split; 1: mass, from lse or from the splits' parts; 2: both at once
 // (one workgroup a query).
 //
-// A workgroup holds one query, its heads in passes of `pass` tiles: their q
+// A workgroup of W waves holds one query, its heads in passes of `pass` tiles: their q
 // rows lie in LDS in MFMA operand order (lane l of tile t, k-step s reads the 16
-// bytes at ((t * NK + s) * 64 + l) * 16), and each of its four waves takes every
-// fourth block of 16 entries, whose key rows it gathers from memory straight
-// into operand registers, one block ahead.  A key row is read once a pass for all heads
-// of its key head.
+// bytes at ((t * NK + s) * 64 + l) * 16), and each wave takes every W-th step of KB blocks
+// of 16 entries, whose key rows it gathers from memory straight into operand
+// registers, one step ahead with two buffers (BUF).  A key row is read once a pass for all
+// heads of its key head.
 //   statistics: D = K Q^T, so that a lane holds four keys of one head and
 //     keeps one (max, sum) per tile;
 //   mass: D = Q K^T, so that a lane holds four heads of one key and adds
@@ -91,18 +95,23 @@ int mass_pass_tiles(int heads, int groups, int d) {
 // The two gather the keys twice: the logits of a query (heads x k in fp32)
 // are as large as a CU's whole register file, and written out they
 // would be as many bytes as the key rows.
-template <int NK, int MODE>
-__global__ void __launch_bounds__(kMassThreads) mass_kernel(MassArgs a, int pass) {
+//
+// Rows of 1 KB and more fill a wave's registers with one block; there the reads of q from
+// LDS bound the kernel, so two blocks share each of them, without a second buffer, and
+// eight waves overlap gathers with products (2,048 queries x 128 heads of 576 x 1,024 entries with
+// lse: 453 us, one block with a second buffer and four waves 653).
+template <int NK, int MODE, int W, int KB, int BUF>
+__global__ void __launch_bounds__(W * kWave) mass_kernel(MassArgs a, int pass) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  constexpr int D = NK * 32;
+  constexpr int D = NK * 32, THREADS = W * kWave;
   const HeadTiles ht(a.heads, a.groups);
   const int T = a.groups * ht.tiles, cap = pass * 16;
   uint8_t* qs = lds;
-  float* ms = reinterpret_cast<float*>(qs + (size_t)cap * D * 2);  // [cap] reference exponent
-  float* rs = ms + cap;                                            // [cap] 1 / sum
-  float2* red = reinterpret_cast<float2*>(rs + cap);               // [waves][cap]
-  int* ids = reinterpret_cast<int*>(red + kMassWaves * cap);       // [split_len]
-  float* sums = reinterpret_cast<float*>(ids + a.split_len);       // [split_len], several passes only
+  float* ms = reinterpret_cast<float*>(qs + (size_t)cap * D * 2);           // [cap] reference exponent
+  float* rs = ms + (MODE != 0 ? cap : 0);                                   // [cap] 1 / sum
+  float2* red = reinterpret_cast<float2*>(rs + (MODE != 0 ? cap : 0));      // [waves][cap]
+  int* ids = reinterpret_cast<int*>(red + (MODE != 1 ? W * cap : 0));       // [split_len]
+  float* sums = reinterpret_cast<float*>(ids + a.split_len);                // [split_len], several passes only
 
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int col = lane & 15, grp = lane >> 4;
@@ -115,25 +124,27 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(MassArgs a, int pass
   }();
   const int split = blockIdx.y;
   const int j0 = split * a.split_len, nj = min(a.split_len, a.topk - j0);
-  const int njp = (nj + 15) & ~15;
-  for (int j = tid; j < njp; j += kMassThreads) {
+  for (int j = tid; j < a.split_len; j += THREADS) {
     const int id = j < nj ? a.idx[(int64_t)q * a.topk + j0 + j] : -1;
     ids[j] = (unsigned)id < (unsigned)a.L ? id : -1;
   }
-  const int nblk = njp / 16;
-  const int mine = wave < nblk ? (nblk - wave + kMassWaves - 1) / kMassWaves : 0;  // wave-uniform
+  const int nstep = (nj + 16 * KB - 1) / (16 * KB);
+  const int mine = wave < nstep ? (nstep - wave + W - 1) / W : 0;  // wave-uniform
   const int row_elems = a.groups * D;
-  auto gather = [&](int i, int g, bf16x8* f) -> int {  // the wave's i-th block, key head g
-    const int id = i < mine ? ids[(wave + i * kMassWaves) * 16 + col] : -1;
-    const uint16_t* p = a.k + (int64_t)max(id, 0) * row_elems + g * D + grp * 8;
-    if (id >= 0) {
+  // the wave's i-th step, key head g; id: the lane's entries (split_len covers every whole step)
+  auto gather = [&](int i, int g, bf16x8 (*f)[NK], int* id) {
 #pragma unroll
-      for (int s = 0; s < NK; ++s) f[s] = *reinterpret_cast<const bf16x8*>(p + s * 32);
-    } else {
+    for (int kb = 0; kb < KB; ++kb) {
+      id[kb] = i < mine ? ids[((wave + i * W) * KB + kb) * 16 + col] : -1;
+      const uint16_t* p = a.k + (int64_t)max(id[kb], 0) * row_elems + g * D + grp * 8;
+      if (id[kb] >= 0) {
 #pragma unroll
-      for (int s = 0; s < NK; ++s) f[s] = bf16x8{};
+        for (int s = 0; s < NK; ++s) f[kb][s] = *reinterpret_cast<const bf16x8*>(p + s * 32);
+      } else {
+#pragma unroll
+        for (int s = 0; s < NK; ++s) f[kb][s] = bf16x8{};
+      }
     }
-    return id;
   };
   auto qfrag = [&](int t, int s) {  // t: tile of the pass
     return *reinterpret_cast<const bf16x8*>(qs + ((t * NK + s) * 64 + lane) * 16);
@@ -143,7 +154,7 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(MassArgs a, int pass
     const int c1 = min(T, c0 + pass), rows = (c1 - c0) * 16;
     if (c0) __syncthreads();  // the last pass is through with the LDS
     const u32x4 zero = {0u, 0u, 0u, 0u};
-    for (int e = tid; e < rows * NK * 4; e += kMassThreads) {
+    for (int e = tid; e < rows * NK * 4; e += THREADS) {
       const int r = e / (NK * 4), c = e - r * (NK * 4);
       const int h = ht.head(c0 + (r >> 4), r & 15);
       u32x4 v = zero;
@@ -153,7 +164,7 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(MassArgs a, int pass
       *reinterpret_cast<u32x4*>(qs + slot * 16) = v;
     }
     if constexpr (MODE == 1) {
-      for (int r = tid; r < rows; r += kMassThreads) {
+      for (int r = tid; r < rows; r += THREADS) {
         const int h = ht.head(c0 + (r >> 4), r & 15);
         float m = 0.0f, rl = 0.0f;
         if (h >= 0 && a.lse) {
@@ -179,32 +190,46 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(MassArgs a, int pass
         float m[kItemTiles], l[kItemTiles];
 #pragma unroll
         for (int t = 0; t < kItemTiles; ++t) { m[t] = kNoMax; l[t] = 0.0f; }
-        bf16x8 f[2][NK];
-        int id[2];
-        id[0] = gather(0, g, f[0]);
-        for (int i0 = 0; i0 < mine; i0 += 2) {
+        bf16x8 f[BUF][KB][NK];
+        int id[BUF][KB];
+        if constexpr (BUF == 2) gather(0, g, f[0], id[0]);
+        for (int i0 = 0; i0 < mine; i0 += BUF) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
+          for (int u = 0; u < BUF; ++u) {
             if (i0 + u >= mine) break;  // wave-uniform
-            id[1 - u] = gather(i0 + u + 1, g, f[1 - u]);
-            const unsigned live = (unsigned)(__ballot(id[u] >= 0) & 0xffffu) >> (4 * grp);
+            if constexpr (BUF == 2) gather(i0 + u + 1, g, f[1 - u], id[1 - u]);
+            else gather(i0, g, f[0], id[0]);
+            unsigned live[KB];
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+              live[kb] = (unsigned)(__ballot(id[u][kb] >= 0) & 0xffffu) >> (4 * grp);
 #pragma unroll
             for (int t = 0; t < kItemTiles; ++t) {
               if (t >= nt) break;  // uniform
-              f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+              f32x4 acc[KB];
 #pragma unroll
-              for (int s = 0; s < NK; ++s)
-                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[u][s], qfrag(t0 - c0 + t, s), acc, 0, 0, 0);
-              float x[4];
+              for (int kb = 0; kb < KB; ++kb) acc[kb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-              for (int e = 0; e < 4; ++e) x[e] = (live >> e) & 1u ? acc[e] * a.scale2 : -__builtin_inff();
-              const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-              if (top > m[t] + kLazy) {
-                l[t] *= exp2_fast(m[t] - top);
-                m[t] = top;
+              for (int s = 0; s < NK; ++s) {
+                const bf16x8 qf = qfrag(t0 - c0 + t, s);
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb)
+                  acc[kb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[u][kb][s], qf, acc[kb], 0, 0, 0);
               }
 #pragma unroll
-              for (int e = 0; e < 4; ++e) l[t] += exp2_fast(x[e] - m[t]);
+              for (int kb = 0; kb < KB; ++kb) {
+                float x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  x[e] = (live[kb] >> e) & 1u ? acc[kb][e] * a.scale2 : -__builtin_inff();
+                const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+                if (top > m[t] + kLazy) {
+                  l[t] *= exp2_fast(m[t] - top);
+                  m[t] = top;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) l[t] += exp2_fast(x[e] - m[t]);
+              }
             }
           }
         }
@@ -219,10 +244,10 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(MassArgs a, int pass
         t0 += nt;
       }
       __syncthreads();
-      for (int r = tid; r < rows; r += kMassThreads) {
+      for (int r = tid; r < rows; r += THREADS) {
         float2 p = red[r];
 #pragma unroll
-        for (int w = 1; w < kMassWaves; ++w) p = join(p, red[w * cap + r]);
+        for (int w = 1; w < W; ++w) p = join(p, red[w * cap + r]);
         if constexpr (MODE == 0) {
           a.part[((int64_t)q * a.nsplit + split) * (T * 16) + c0 * 16 + r] = p;
         } else {
@@ -234,51 +259,92 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(MassArgs a, int pass
     }
 
     if constexpr (MODE != 0) {
-      // Steps: (block, key head of the pass), the key head innermost.
+      // Steps of (KB blocks, key head of the pass), the key head innermost.
       const int g0 = c0 / ht.tiles, g1 = (c1 + ht.tiles - 1) / ht.tiles;
       const int steps = mine * (g1 - g0);
-      bf16x8 f[2][NK];
-      float o = 0.0f;
-      int blk = 0, g = g0;   // of the step at hand
-      int nb = 0, ng = g0;   // of the step being gathered
-      auto next = [&](bf16x8* dst) {
-        gather(nb, ng, dst);
+      bf16x8 f[BUF][KB][NK];
+      int id[KB];
+      float o[KB];
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) o[kb] = 0.0f;
+      int step = 0, g = g0;  // at hand
+      int nb = 0, ng = g0;   // being gathered
+      auto next = [&](bf16x8 (*dst)[NK]) {
+        gather(nb, ng, dst, id);
         if (++ng == g1) { ng = g0; ++nb; }
       };
-      next(f[0]);
-      for (int i0 = 0; i0 < steps; i0 += 2) {
+      if constexpr (BUF == 2) next(f[0]);
+      for (int i0 = 0; i0 < steps; i0 += BUF) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < BUF; ++u) {
           if (i0 + u >= steps) break;  // wave-uniform
-          next(f[1 - u]);
+          if constexpr (BUF == 2) next(f[1 - u]);
+          else next(f[0]);
           const int ta = max(c0, g * ht.tiles) - c0, tb = min(c1, (g + 1) * ht.tiles) - c0;
           for (int t = ta; t < tb; ++t) {
-            f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+            f32x4 acc[KB];
 #pragma unroll
-            for (int s = 0; s < NK; ++s)
-              acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qfrag(t, s), f[u][s], acc, 0, 0, 0);
+            for (int kb = 0; kb < KB; ++kb) acc[kb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int s = 0; s < NK; ++s) {
+              const bf16x8 qf = qfrag(t, s);
+#pragma unroll
+              for (int kb = 0; kb < KB; ++kb)
+                acc[kb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qf, f[u][kb][s], acc[kb], 0, 0, 0);
+            }
             const f32x4 m = *reinterpret_cast<const f32x4*>(ms + t * 16 + 4 * grp);
             const f32x4 r = *reinterpret_cast<const f32x4*>(rs + t * 16 + 4 * grp);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o = fmaf(exp2_fast(fmaf(acc[e], a.scale2, -m[e])), r[e], o);
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                o[kb] = fmaf(exp2_fast(fmaf(acc[kb][e], a.scale2, -m[e])), r[e], o[kb]);
           }
           if (++g == g1) {
             g = g0;
-            o += __shfl_xor(o, 16);
-            o += __shfl_xor(o, 32);
-            const int j = (wave + blk * kMassWaves) * 16 + col;
-            if (grp == 0) {  // the wave's own entries: no other wave reads or writes them
-              if (c0) o += sums[j];
-              if (c1 < T) sums[j] = o;
-              else if (j < nj) a.mass[(int64_t)q * a.topk + j0 + j] = ids[j] >= 0 ? o * a.inv_heads : 0.0f;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+              float sum = add_rows(o[kb]);
+              const int j = ((wave + step * W) * KB + kb) * 16 + col;
+              if (grp == 0) {  // the wave's own entries: no other wave reads or writes them
+                if (c0) sum += sums[j];
+                if (c1 < T) sums[j] = sum;
+                else if (j < nj) a.mass[(int64_t)q * a.topk + j0 + j] = ids[j] >= 0 ? sum * a.inv_heads : 0.0f;
+              }
+              o[kb] = 0.0f;
             }
-            o = 0.0f;
-            ++blk;
+            ++step;
           }
         }
       }
     }
   }
+}
+
+template <int NK, int MODE>
+hipError_t mass_launch(const MassArgs& a, hipStream_t s) {
+  constexpr bool wide = NK >= kWideSteps;
+  constexpr int W = wide ? 8 : 4, KB = wide ? 2 : 1, BUF = wide ? 1 : 2;
+  static LdsLimit lim;
+  constexpr int row = mass_row_bytes(NK * 32, MODE, W);
+  const int pass = mass_pass_tiles(a.heads, a.groups, row);
+  const bool several = pass < mass_rows(a.heads, a.groups) / 16;
+  const int lds = pass * 16 * row + a.split_len * (several ? 8 : 4);
+  hipError_t e = raise_dynamic_lds((const void*)mass_kernel<NK, MODE, W, KB, BUF>, lds, lim);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((mass_kernel<NK, MODE, W, KB, BUF>), dim3((unsigned)a.n, (unsigned)a.nsplit),
+                     dim3(W * kWave), (size_t)lds, s, a, pass);
+  return hipGetLastError();
+}
+
+template <int NK>
+hipError_t mass_d(const MassArgs& a, hipStream_t s) {
+  if (a.lse) return mass_launch<NK, 1>(a, s);
+  if constexpr (NK < kWideSteps) {
+    if (a.nsplit == 1) return mass_launch<NK, 2>(a, s);
+  }
+  hipError_t e = mass_launch<NK, 0>(a, s);
+  return e != hipSuccess ? e : mass_launch<NK, 1>(a, s);
 }
 
 // The same with the key rows staged through LDS, for rows of 128 or 256 bytes.
@@ -567,29 +633,7 @@ hipError_t mass_staged(const MassArgs& a, hipStream_t s) {
   return mass_staged_pt<NK, 4>(a, s);
 }
 
-template <int NK, int MODE>
-hipError_t mass_launch(const MassArgs& a, hipStream_t s) {
-  static LdsLimit lim;
-  const int pass = mass_pass_tiles(a.heads, a.groups, NK * 32);
-  const bool several = pass < mass_rows(a.heads, a.groups) / 16;
-  const int lds = pass * 16 * mass_row_bytes(NK * 32) + a.split_len * (several ? 8 : 4);
-  hipError_t e = raise_dynamic_lds((const void*)mass_kernel<NK, MODE>, lds, lim);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((mass_kernel<NK, MODE>), dim3((unsigned)a.n, (unsigned)a.nsplit),
-                     dim3(kMassThreads), (size_t)lds, s, a, pass);
-  return hipGetLastError();
-}
-
-template <int NK>
-hipError_t mass_d(const MassArgs& a, hipStream_t s) {
-  if (a.lse) return mass_launch<NK, 1>(a, s);
-  if (a.nsplit == 1) return mass_launch<NK, 2>(a, s);
-  hipError_t e = mass_launch<NK, 0>(a, s);
-  return e != hipSuccess ? e : mass_launch<NK, 1>(a, s);
-}
-
 }  // namespace
-
 
 int64_t mass_rows(int heads, int groups) { return (int64_t)groups * HeadTiles(heads, groups).tiles * 16; }
 
@@ -601,6 +645,8 @@ void mass_splits(int64_t n, int topk, int& nsplit, int& split_len) {
   split_len = (int)(((topk + want - 1) / want + 63) / 64 * 64);
   nsplit = (topk + split_len - 1) / split_len;
 }
+
+bool mass_keeps_parts(int d, int nsplit) { return nsplit > 1 || d / 32 >= kWideSteps; }
 
 bool mass_supports(int d) {
   return d == 64 || d == 96 || d == 128 || d == 192 || d == 256 || d == 512 || d == 576;
