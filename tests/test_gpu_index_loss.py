@@ -63,13 +63,14 @@ CASES = [  # n, k, heads, key heads, d, L
     (2, 40, 20, 1, 512, 64), (5, 250, 24, 2, 256, 300), (2, 500, 144, 1, 192, 600), (1, 130, 256, 2, 64, 140),
     (70, 100, 8, 1, 64, 200), (1100, 20, 4, 2, 64, 64), (1030, 300, 33, 1, 64, 200), (1030, 90, 64, 1, 128, 100), (9, 16, 17, 1, 128, 40), (2, 15, 200, 200, 64, 33),
     (1, 70, 256, 1, 576, 90), (1, 33, 256, 2, 576, 50), (1, 2048, 128, 1, 576, 500), (2, 50, 1024, 2, 64, 60),
-    (1, 40, 300, 3, 512, 60),
+    (1, 40, 300, 3, 512, 60), (2, 300, 96, 1, 128, 200), (2, 90, 80, 1, 64, 70), (1, 200, 144, 1, 128, 150),
+    (3, 33, 190, 2, 64, 40),
 ]
 
 
 LONG = [  # enough queries for one workgroup each, k up to the longest: (k, heads, key heads, d)
     (2048, 64, 1, 128), (2047, 48, 1, 128), (1300, 16, 1, 64), (2000, 40, 2, 64), (777, 100, 1, 128),
-    (2048, 8, 2, 64), (1025, 30, 1, 128), (640, 128, 2, 64), (129, 64, 1, 64),
+    (2048, 8, 2, 64), (1025, 30, 1, 128), (640, 128, 2, 64), (129, 64, 1, 64), (700, 90, 1, 64), (300, 128, 1, 128), (200, 270, 2, 128),
 ]
 
 
