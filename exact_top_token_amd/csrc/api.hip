@@ -1059,7 +1059,7 @@ int hytopk_cache_read(const hytopk_cache* c, int64_t n, const int32_t* slots, in
 size_t hytopk_attention_mass_workspace(const hytopk_attention* p) {
   if (check_attention(p) != HYTOPK_OK) return 0;
   int nsplit = 1, len = 0;
-  hk::mass_splits(p->n, p->k, nsplit, len);
+  hk::mass_splits(p->n, p->k, p->d, nsplit, len);
   const size_t parts = hk::mass_keeps_parts(p->d, nsplit) ? (size_t)p->n * nsplit * (size_t)hk::mass_rows(p->heads, p->key_heads) : 0;
   return align_up(std::max<size_t>(parts * sizeof(float2), 1));
 }
@@ -1090,7 +1090,7 @@ int hytopk_attention_mass(const hytopk_attention* p, const void* q, const void* 
     a.topk = p->k;
     a.scale2 = (float)((double)p->softmax_scale * 1.4426950408889634074);
     a.inv_heads = 1.0f / (float)p->heads;
-    hk::mass_splits(p->n, p->k, a.nsplit, a.split_len);
+    hk::mass_splits(p->n, p->k, p->d, a.nsplit, a.split_len);
     hipStream_t s = static_cast<hipStream_t>(stream);
     Span sp("attention_mass", s);
     HK_HIP(hk::launch_attention_mass(a, p->d, s), "attention mass launch");

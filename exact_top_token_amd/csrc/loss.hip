@@ -43,6 +43,17 @@ __device__ __forceinline__ float add_rows(float x) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
+// (max, sum) of a row over the splits' parts ([nsplit][rows], from the row's first one), by the four
+// lanes of a quad together.
+__device__ __forceinline__ float2 join_parts(const float2* part, int nsplit, int rows) {
+  const int sub = lane_id() & 3;
+  float2 p = make_float2(kNoMax, 0.0f);
+#pragma unroll 4
+  for (int sp = sub; sp < nsplit; sp += 4) p = join(p, part[(int64_t)sp * rows]);
+  p = join(p, make_float2(__shfl_xor(p.x, 1), __shfl_xor(p.y, 1)));
+  return join(p, make_float2(__shfl_xor(p.x, 2), __shfl_xor(p.y, 2)));
+}
+
 // How the heads of a query lie on 16-row tiles: each key head's heads padded to
 // whole tiles.
 struct HeadTiles {
@@ -164,20 +175,20 @@ __global__ void __launch_bounds__(W * kWave) mass_kernel(MassArgs a, int pass) {
       *reinterpret_cast<u32x4*>(qs + slot * 16) = v;
     }
     if constexpr (MODE == 1) {
-      for (int r = tid; r < rows; r += THREADS) {
-        const int h = ht.head(c0 + (r >> 4), r & 15);
+      for (int e = tid; e < rows * 4; e += THREADS) {  // a quad per row
+        const int r = e >> 2, h = ht.head(c0 + (r >> 4), r & 15);
         float m = 0.0f, rl = 0.0f;
         if (h >= 0 && a.lse) {
           lse_reference(a.lse[(int64_t)q * a.heads + h], m, rl);
         } else if (h >= 0) {
-          float2 p = make_float2(kNoMax, 0.0f);
-          for (int sp = 0; sp < a.nsplit; ++sp)
-            p = join(p, a.part[((int64_t)q * a.nsplit + sp) * (T * 16) + c0 * 16 + r]);
+          const float2 p = join_parts(a.part + (int64_t)q * a.nsplit * (T * 16) + c0 * 16 + r, a.nsplit, T * 16);
           m = p.x;
           rl = p.y == 0.0f ? 0.0f : 1.0f / p.y;
         }
-        ms[r] = m;
-        rs[r] = rl;
+        if ((e & 3) == 0) {
+          ms[r] = m;
+          rs[r] = rl;
+        }
       }
     }
     __syncthreads();
@@ -454,20 +465,20 @@ __global__ void __launch_bounds__(kMassThreads, PT > 4 ? 2 : 3) mass_staged_kern
         qf[t][s] = h >= 0 ? *reinterpret_cast<const bf16x8*>(p + s * 32) : bf16x8{};
     }
     if constexpr (MODE == 1) {
-      for (int r = bi * kWave + lane; r < PT * 16; r += bw * kWave) {  // the waves of this key head
-        const int h = (r >> 4) < nt ? ht.head(c0 + (r >> 4), r & 15) : -1;
+      for (int e = bi * kWave + lane; e < PT * 64; e += bw * kWave) {  // a quad per row, by this key head's waves
+        const int r = e >> 2, h = (r >> 4) < nt ? ht.head(c0 + (r >> 4), r & 15) : -1;
         float m = 0.0f, rl = 0.0f;
         if (h >= 0 && a.lse) {
           lse_reference(a.lse[(int64_t)q * a.heads + h], m, rl);
         } else if (h >= 0) {
-          float2 p = make_float2(kNoMax, 0.0f);
-          for (int sp = 0; sp < a.nsplit; ++sp)
-            p = join(p, a.part[((int64_t)q * a.nsplit + sp) * (T * 16) + c0 * 16 + r]);
+          const float2 p = join_parts(a.part + (int64_t)q * a.nsplit * (T * 16) + c0 * 16 + r, a.nsplit, T * 16);
           m = p.x;
           rl = p.y == 0.0f ? 0.0f : 1.0f / p.y;
         }
-        ms[r] = m;
-        rs[r] = rl;
+        if ((e & 3) == 0) {
+          ms[r] = m;
+          rs[r] = rl;
+        }
       }
     }
     __syncthreads();
@@ -602,9 +613,11 @@ __global__ void __launch_bounds__(kMassThreads, PT > 4 ? 2 : 3) mass_staged_kern
 template <int NK, int PT, int MODE>
 hipError_t mass_staged_launch(const MassArgs& a, hipStream_t s) {
   static LdsLimit lim;
-  // Key heads side by side as long as their sums take no more LDS than one row of 2,048.
+  // Key heads side by side where queries are few and their sums take no more LDS than one row of
+  // 2,048 (without lse, 301 queries x 4 key heads x 500 entries: 26 us against 32; 2,048 queries: 146
+  // against 127, for they fill the chip without).
   int gw = 1;
-  while (gw < kMassWaves && 2 * gw <= a.groups && 2 * gw * a.split_len <= 2048) gw *= 2;
+  while (a.n <= 512 && gw < kMassWaves && 2 * gw <= a.groups && 2 * gw * a.split_len <= 2048) gw *= 2;
   const bool apart = mass_rows(a.heads, a.groups) > PT * 16;  // sums beside the rows
   const int lds = 2 * kMassWaves * 16 * NK * 64 + PT * 16 * 8 * (gw + kMassWaves) + a.split_len / 8 +
                   a.split_len * 4 * (apart ? 1 + gw : 1);
@@ -642,11 +655,17 @@ hipError_t mass_staged(const MassArgs& a, hipStream_t s) {
 
 int64_t mass_rows(int heads, int groups) { return (int64_t)groups * HeadTiles(heads, groups).tiles * 16; }
 
-// Splits of a query's entries so that few queries still fill the chip: about
-// 1,024 workgroups, each with a block of 16 entries for every wave.
-void mass_splits(int64_t n, int topk, int& nsplit, int& split_len) {
+// Splits of a query's entries so that few queries still fill the chip, each with a block of 16
+// entries for every wave: about 256 workgroups where one fills a CU (wide heads), 1,024 of the
+// narrowest rows, 512 else.  64 queries x 64 heads of 128 x 2,048 with lse: 256, 512, 768, 1,024
+// workgroups 10.1, 9.9, 11.4, 14.5 us; 100 x 128 heads of 576 x 1,024: 34.6, 46.4, 57.8, 68.1;
+// 301 x 32 heads of 64 on 4 key heads x 500 of 4,096 keys: 512, 768, 1,024, 2,048 workgroups
+// 15.4, 10.8, 9.8, 9.7, and 301 x 64 heads on one key head x 2,000 of 131,072: 26.3, 19.7, 18.2,
+// 20.0.
+void mass_splits(int64_t n, int topk, int d, int& nsplit, int& split_len) {
   const int most = (topk + 63) / 64;
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(most, 1024 / std::max<int64_t>(1, n)));
+  const int64_t workgroups = d / 32 >= kWideSteps ? 256 : d <= 64 ? 1024 : 512;
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(most, workgroups / std::max<int64_t>(1, n)));
   split_len = (int)(((topk + want - 1) / want + 63) / 64 * 64);
   nsplit = (topk + split_len - 1) / split_len;
 }

@@ -350,9 +350,10 @@ hipError_t rotary_io(const RotaryArgs& a, bool vec, hipStream_t s) {
   RotaryGrid g;
   g.units = std::min(units, kRowThreads);
   g.rows = kRowThreads / g.units;
-  // Four rows a thread where that leaves over 1,024 workgroups, else one.
+  // Four rows a thread where that leaves 512 workgroups or more, else one: 8,192 x 64 x 128 53 us
+  // against 66, 1,000 x 64 x 128 8.4 against 9.7, but 300 x 64 x 128 5.0 against 4.6.
   const int64_t rows_all = (int64_t)a.n * a.heads;
-  const int per = rows_all / (4 * g.rows) >= 1024 ? 4 * g.rows : g.rows;
+  const int per = rows_all / (4 * g.rows) >= 512 ? 4 * g.rows : g.rows;
   g.hb = std::min(a.heads, per);
   if ((a.heads + g.hb - 1) / g.hb > 65535) g.hb = (a.heads + 65534) / 65535;
   g.tb = 1;
@@ -737,7 +738,8 @@ hipError_t cache_write_k(const CacheWriteArgs& a, bool vec, int log_p, hipStream
   const int segs = (chunks + per - 1) / per;
   const int threads = std::max(kRowThreads, 1 << log_p), rb = threads >> log_p;
   // Rounds share the set-up and the entries of a workgroup's rows; as many (up to
-  // four) as leave 2,048 workgroups and fit the table.
+  // four) as leave 2,048 workgroups and fit the table (8,192 x 64 x 128 to MXFP4 and back with
+  // 1, 2, 4, 16 rounds: 100, 85, 81, 79 us; 131,072 x 128 to MXFP8 and back 32.5, 29.4, 29.2, 29.0).
   int rounds = 1;
   const int fit = a.rot.freq ? kWriteEntries / (rb * (a.rot.dim / 2)) : 4;
   while (rounds < 4 && 2 * rounds <= fit && a.n / ((int64_t)rb * 2 * rounds) >= 2048) rounds *= 2;
@@ -854,7 +856,8 @@ struct Stored8 {
   }
 };
 
-constexpr int kReadUnits = 4;  // pieces of eight elements a thread has in flight
+// Pieces of eight elements a thread has in flight (eight: 91 us for 1M FP8 rows of 128 against 81).
+constexpr int kReadUnits = 4;
 
 // Rows read back, `rows` of them a workgroup: a thread decodes eight elements at a time, so that
 // a wave stores one contiguous kilobyte of bf16.
