@@ -816,6 +816,8 @@ Extent extent(const void* p, int64_t bytes) {
 }
 
 bool overlap(Extent a, Extent b) { return a.lo < b.hi && b.lo < a.hi; }
+// Whether `bytes` bytes at p (NULL: none) lie in m.
+bool touches(Extent m, const void* p, int64_t bytes) { return p && overlap(m, extent(p, bytes)); }
 
 int check_plan(const hytopk_rotary_plan* p, int32_t d) {
   if (!p) return fail(HYTOPK_EINVAL, "rotary plan is NULL");
@@ -827,7 +829,7 @@ int check_plan(const hytopk_rotary_plan* p, int32_t d) {
     return fail(HYTOPK_EINVAL, "unknown rotary layout");
   if (!p->freq) return fail(HYTOPK_EINVAL, "rotary freq is NULL");
   if (misaligned(p->freq, 8)) return fail(HYTOPK_EINVAL, "rotary freq must be 8-byte aligned");
-  if (!std::isfinite(p->gain)) return fail(HYTOPK_EINVAL, "the rotary gain must be finite");
+  if (!std::isfinite((float)p->gain)) return fail(HYTOPK_EINVAL, "the rotary gain must be finite in fp32");
   return HYTOPK_OK;
 }
 
@@ -859,8 +861,9 @@ bool in_cache(const hytopk_cache* c, Extent m) {
   const int64_t e = c->L * c->heads * c->d;
   const int64_t codes = c->dtype == HYTOPK_BF16 ? 2 * e : (c->dtype == HYTOPK_MXFP4_E2M1 ? e / 2 : e);
   const int64_t scale = c->dtype == HYTOPK_BF16 ? 0 : (c->dtype == HYTOPK_FP8_E4M3 ? 4 * c->L : e / 32);
-  return overlap(m, extent(c->codes, codes)) || (scale && overlap(m, extent(c->scale, scale)));
+  return touches(m, c->codes, codes) || (scale && touches(m, c->scale, scale));
 }
+bool in_cache(const hytopk_cache* c, const void* p, int64_t bytes) { return p && in_cache(c, extent(p, bytes)); }
 
 // The geometry alone (what the workspace query knows).
 int check_cache_shape(const hytopk_cache* c) {
@@ -894,16 +897,20 @@ int check_cache(const hytopk_cache* c, int64_t n, const int32_t* slots, int64_t 
 
 bool wants_claim(int64_t n, bool by_slot) { return by_slot && n > hk::kClaimRows; }
 
+// The softmax's scale in base 2.
+float log2_scale(const hytopk_attention* p) { return (float)((double)p->softmax_scale * 1.4426950408889634074); }
+
 int check_attention(const hytopk_attention* p) {
   if (!p) return fail(HYTOPK_EINVAL, "attention is NULL");
   if (p->L <= 0 || p->n < 0) return fail(HYTOPK_EINVAL, "L must be > 0 and n >= 0");
   if (p->heads <= 0 || p->key_heads <= 0 || p->heads % p->key_heads)
     return fail(HYTOPK_EINVAL, "key_heads must divide heads");
   if (p->k <= 0) return fail(HYTOPK_EINVAL, "k must be > 0");
-  if (!std::isfinite(p->softmax_scale)) return fail(HYTOPK_EINVAL, "softmax_scale must be finite");
+  if (!std::isfinite(log2_scale(p))) return fail(HYTOPK_EINVAL, "softmax_scale must be finite, in base 2 too");
   if (p->k > kMaxK) return fail(HYTOPK_EUNSUPPORTED, "k > 2048");
   if (p->L >= kMaxRows) return fail(HYTOPK_EUNSUPPORTED, "L >= 2^31");
-  if (p->n >= int64_t(1) << 24) return fail(HYTOPK_EUNSUPPORTED, "n >= 2^24");
+  // a launch holds fewer than 2^32 threads along the queries
+  if (p->n >= hk::mass_most_queries(p->d)) return fail(HYTOPK_EUNSUPPORTED, "n >= 2^24, or 2^23 with d > 256");
   if (!hk::mass_supports(p->d)) return fail(HYTOPK_EUNSUPPORTED, "d must be 64, 96, 128, 192, 256, 512 or 576");
   if (p->heads > 1024) return fail(HYTOPK_EUNSUPPORTED, "heads > 1024");
   return HYTOPK_OK;
@@ -930,6 +937,7 @@ int hytopk_rotary_frequencies(int32_t dim, double base, int32_t scaling, double 
     // base^(-(dim - 2)/dim) divided by factor is the slowest frequency of the raised base
     if (scaling == HYTOPK_SCALING_NTK) b *= std::pow(factor, (double)dim / std::max(dim - 2, 1));
     double lo = 0.0, width = 1.0;
+    bool slow = false;  // every pair turns once or less
     if (scaling == HYTOPK_SCALING_YARN) {
       // the pair that makes r turns in the original context
       auto pair = [&](double r) {
@@ -938,13 +946,14 @@ int hytopk_rotary_frequencies(int32_t dim, double base, int32_t scaling, double 
       lo = std::max(std::floor(pair(32.0)), 0.0);
       const double hi = std::min(std::ceil(pair(1.0)), (double)(dim - 1));
       width = std::max(hi - lo, 1e-3);
+      slow = pair(1.0) <= 0.0;
     }
     for (int i = 0; i < dim / 2; ++i) {
       const double f = std::pow(b, -2.0 * i / dim);
       if (scaling == HYTOPK_SCALING_LINEAR) {
         freq[i] = f / factor;
       } else if (scaling == HYTOPK_SCALING_YARN) {
-        const double r = std::min(std::max((i - lo) / width, 0.0), 1.0);
+        const double r = slow ? 1.0 : std::min(std::max((i - lo) / width, 0.0), 1.0);
         freq[i] = f * (1.0 - r) + f / factor * r;
       } else {
         freq[i] = f;
@@ -971,6 +980,9 @@ int hytopk_rotary(const hytopk_rotary_plan* plan, int64_t n, int32_t heads, int3
                       (heads == 1 || x->head_stride == y->head_stride);
     if (!same && overlap(extent(x, n, heads, d), extent(y, n, heads, d)))
       return fail(HYTOPK_EINVAL, "x and y overlap (y may be x itself)");
+    const Extent out = extent(y, n, heads, d);
+    if (touches(out, q_pos, 4 * n) || touches(out, plan->freq, 4 * (int64_t)plan->dim))
+      return fail(HYTOPK_EINVAL, "y overlaps the positions or the plan");
     hk::RotaryArgs a{};
     a.x = x->data;
     a.y = y->data;
@@ -988,8 +1000,13 @@ int hytopk_rotary(const hytopk_rotary_plan* plan, int64_t n, int32_t heads, int3
 }
 
 size_t hytopk_cache_write_workspace(const hytopk_cache* c, int64_t n, int32_t by_slot) {
-  if (check_cache_shape(c) != HYTOPK_OK || !wants_claim(n, by_slot != 0)) return 0;
-  return align_up((size_t)c->L * sizeof(int32_t));
+  size_t need = 0;
+  guarded([&]() -> int {
+    const int rc = check_cache_shape(c);
+    if (rc == HYTOPK_OK && wants_claim(n, by_slot != 0)) need = align_up((size_t)c->L * sizeof(int32_t));
+    return rc;
+  });
+  return need;
 }
 
 int hytopk_cache_write(const hytopk_cache* c, int64_t n, const hytopk_rows* x,
@@ -1006,6 +1023,9 @@ int hytopk_cache_write(const hytopk_cache* c, int64_t n, const hytopk_rows* x,
       return fail(HYTOPK_EINVAL, "x overlaps the cache");
     const bool claim = wants_claim(n, slots != nullptr);
     if (claim && (rc = check_ws(workspace, workspace_bytes, hytopk_cache_write_workspace(c, n, 1)))) return rc;
+    if (in_cache(c, slots, 4 * n) || (claim && in_cache(c, workspace, 4 * c->L)) ||
+        (plan && (in_cache(c, q_pos, 4 * n) || in_cache(c, plan->freq, 4 * (int64_t)plan->dim))))
+      return fail(HYTOPK_EINVAL, "the slots, the positions, the plan or the workspace overlap the cache");
     hk::CacheWriteArgs a{};
     a.x = x->data;
     a.ts = x->token_stride;
@@ -1040,6 +1060,7 @@ int hytopk_cache_read(const hytopk_cache* c, int64_t n, const int32_t* slots, in
     const int64_t bytes = n * c->heads * c->d * (out_dtype == HYTOPK_ROWS_BF16 ? 2 : 4);
     if (in_cache(c, extent(out, bytes)))
       return fail(HYTOPK_EINVAL, "out overlaps the cache");
+    if (touches(extent(out, bytes), slots, 4 * n)) return fail(HYTOPK_EINVAL, "out overlaps the slots");
     hk::CacheReadArgs a{};
     a.codes = static_cast<const uint8_t*>(c->codes);
     a.scale = c->scale;
@@ -1057,11 +1078,18 @@ int hytopk_cache_read(const hytopk_cache* c, int64_t n, const int32_t* slots, in
 }
 
 size_t hytopk_attention_mass_workspace(const hytopk_attention* p) {
-  if (check_attention(p) != HYTOPK_OK) return 0;
-  int nsplit = 1, len = 0;
-  hk::mass_splits(p->n, p->k, p->d, nsplit, len);
-  const size_t parts = hk::mass_keeps_parts(p->d, nsplit) ? (size_t)p->n * nsplit * (size_t)hk::mass_rows(p->heads, p->key_heads) : 0;
-  return align_up(std::max<size_t>(parts * sizeof(float2), 1));
+  size_t need = 0;
+  guarded([&]() -> int {
+    const int rc = check_attention(p);
+    if (rc) return rc;
+    int nsplit = 1, len = 0;
+    hk::mass_splits(p->n, p->k, p->d, nsplit, len);
+    const size_t parts =
+        hk::mass_keeps_parts(p->d, nsplit) ? (size_t)p->n * nsplit * (size_t)hk::mass_rows(p->heads, p->key_heads) : 0;
+    need = align_up(std::max<size_t>(parts * sizeof(float2), 1));
+    return HYTOPK_OK;
+  });
+  return need;
 }
 
 int hytopk_attention_mass(const hytopk_attention* p, const void* q, const void* k,
@@ -1075,7 +1103,14 @@ int hytopk_attention_mass(const hytopk_attention* p, const void* q, const void* 
     if (misaligned(q, 16) || misaligned(k, 16)) return fail(HYTOPK_EINVAL, "q and k must be 16-byte aligned");
     if (misaligned(idx, 4) || misaligned(lse, 4) || misaligned(mass, 4))
       return fail(HYTOPK_EINVAL, "idx, lse and mass must be 4-byte aligned");
-    if (!lse && (rc = check_ws(workspace, workspace_bytes, hytopk_attention_mass_workspace(p)))) return rc;
+    const size_t ws = lse ? 0 : hytopk_attention_mass_workspace(p);
+    if (!lse && (rc = check_ws(workspace, workspace_bytes, ws))) return rc;
+    const Extent out = extent(mass, 4 * p->n * p->k), part = extent(workspace, (int64_t)ws);
+    const int64_t qb = 2 * p->n * p->heads * p->d, kb = 2 * p->L * p->key_heads * p->d, ib = 4 * p->n * p->k;
+    if (touches(out, q, qb) || touches(out, k, kb) || touches(out, idx, ib) ||
+        touches(out, lse, 4 * p->n * p->heads) ||
+        (ws && (overlap(out, part) || touches(part, q, qb) || touches(part, k, kb) || touches(part, idx, ib))))
+      return fail(HYTOPK_EINVAL, "mass and the workspace must not overlap the inputs or each other");
     hk::MassArgs a{};
     a.q = static_cast<const uint16_t*>(q);
     a.k = static_cast<const uint16_t*>(k);
@@ -1088,7 +1123,7 @@ int hytopk_attention_mass(const hytopk_attention* p, const void* q, const void* 
     a.heads = p->heads;
     a.groups = p->key_heads;
     a.topk = p->k;
-    a.scale2 = (float)((double)p->softmax_scale * 1.4426950408889634074);
+    a.scale2 = log2_scale(p);
     a.inv_heads = 1.0f / (float)p->heads;
     hk::mass_splits(p->n, p->k, p->d, a.nsplit, a.split_len);
     hipStream_t s = static_cast<hipStream_t>(stream);
@@ -1110,6 +1145,14 @@ int hytopk_index_loss(int64_t n, int32_t k, const float* score, const float* mas
     for (const void* x : {(const void*)score, (const void*)mass, (const void*)weight,
                           (const void*)loss, (const void*)d_score})
       if (misaligned(x, 4)) return fail(HYTOPK_EINVAL, "arrays must be 4-byte aligned");
+    const int64_t rows = 4 * n, all = rows * k;
+    if (d_score && ((d_score != score && touches(extent(d_score, all), score, all)) ||
+                    (d_score != mass && touches(extent(d_score, all), mass, all)) ||
+                    touches(extent(d_score, all), weight, rows)))
+      return fail(HYTOPK_EINVAL, "d_score overlaps an input (it may be score or mass itself)");
+    if (loss && (touches(extent(loss, rows), score, all) || touches(extent(loss, rows), mass, all) ||
+                 touches(extent(loss, rows), weight, rows) || touches(extent(loss, rows), d_score, all)))
+      return fail(HYTOPK_EINVAL, "loss overlaps another array");
     hk::LossArgs a{score, mass, weight, loss, d_score, (int)n, k};
     hipStream_t s = static_cast<hipStream_t>(stream);
     Span sp("index_loss", s);

@@ -330,6 +330,7 @@ struct MassArgs {
 int64_t mass_rows(int heads, int groups);
 void mass_splits(int64_t n, int topk, int d, int& nsplit, int& split_len);
 bool mass_supports(int d);
+int64_t mass_most_queries(int d);  // a call has fewer
 bool mass_keeps_parts(int d, int nsplit);  // whether the statistics go through `part`
 hipError_t launch_attention_mass(const MassArgs& a, int d, hipStream_t s);
 

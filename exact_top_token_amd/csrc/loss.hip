@@ -676,6 +676,8 @@ bool mass_supports(int d) {
   return d == 64 || d == 96 || d == 128 || d == 192 || d == 256 || d == 512 || d == 576;
 }
 
+int64_t mass_most_queries(int d) { return int64_t(1) << (d / 32 >= kWideSteps ? 23 : 24); }
+
 hipError_t launch_attention_mass(const MassArgs& a, int d, hipStream_t s) {
   if (a.n <= 0) return hipSuccess;
   // the staged kernels count key rows in 16-byte pieces of 32 bits: tables below 64 GiB

@@ -377,7 +377,7 @@ size_t hytopk_cache_write_workspace(const hytopk_cache* c, int64_t n, int32_t by
  *         clamped to -127 .. 127, scale byte e + 127 (0 for a block of zeros),
  *         code = x * 2^-e rounded, saturating at 448 or 6.
  * x is finite: an infinity or NaN leaves its own row (FP8) or block (MX)
- * unspecified.  x must not overlap the cache. */
+ * unspecified.  Nothing that the call reads, nor its workspace, may overlap the cache. */
 int hytopk_cache_write(const hytopk_cache* c, int64_t n, const hytopk_rows* x,
                        const int32_t* slots, int64_t start, const hytopk_rotary_plan* plan,
                        const int32_t* q_pos, int64_t q_start, void* workspace,
@@ -415,8 +415,9 @@ size_t hytopk_attention_mass_workspace(const hytopk_attention* p);
  * entries, so that each row sums to 1, and the workspace is required.
  * An index outside [0, L) is padding: mass 0, no part in the sum; its key row is
  * never read.  An index that stands twice counts twice.  Products are bf16 MFMA with fp32
- * accumulation; maxima, sums and exponentials are fp32. 
- * n < 2^24 and heads <= 1024, or HYTOPK_EUNSUPPORTED. */
+ * accumulation; maxima, sums and exponentials are fp32.
+ * n < 2^24 (2^23 for d of 512 or 576) and heads <= 1024, or HYTOPK_EUNSUPPORTED.  mass and the
+ * workspace must not overlap the inputs or each other. */
 int hytopk_attention_mass(const hytopk_attention* p, const void* q, const void* k,
                           const int32_t* idx, const float* lse, float* mass, void* workspace,
                           size_t workspace_bytes, void* stream);
@@ -431,7 +432,7 @@ int hytopk_attention_mass(const hytopk_attention* p, const void* q, const void* 
  * weight [n] fp32 or NULL (1).  Dead entries get 0, whatever their mass holds;
  * a row without a live entry, or whose live mass sums to 0, gets loss 0 and
  * gradient 0.  loss or d_score may be NULL; d_score may be score or mass
- * itself.  1 <= k <= 2048. */
+ * itself, and nothing else that is written may overlap another array.  1 <= k <= 2048. */
 int hytopk_index_loss(int64_t n, int32_t k, const float* score, const float* mass,
                       const float* weight, float* loss, float* d_score, void* stream);
 

@@ -216,3 +216,55 @@ def test_binding_refusals_without_a_gpu():
         hk.attention_mass(x, torch.zeros(8, 128, dtype=torch.bfloat16), torch.zeros(4, 3, dtype=torch.int32))
     with pytest.raises(ValueError):
         hk.index_loss(torch.zeros(4, 3), torch.zeros(4, 3))
+
+
+def test_written_memory_stays_apart_from_what_is_read(lib):
+    """Every call refuses results that lie over its inputs, its plan or its workspace."""
+    y = rows(data=FAKE + (1 << 30))
+    assert rotary(lib, y=y, p=plan(freq=FAKE + (1 << 30) + 64)) == -1
+    assert rotary(lib, y=y, pos=FAKE + (1 << 30) + 2 * 4 * 8192 - 4) == -1  # the last row's last bytes
+    c = cache(L=1 << 20)  # 128 MiB of codes; its scales lie over their beginning
+    assert write(lib, c=c, slots=FAKE + 256) == -1
+    assert write(lib, c=c, p=plan(freq=FAKE + 256)) == -1
+    assert write(lib, c=c, p=plan(freq=FAKE + (1 << 29)), pos=FAKE + 512) == -1
+    assert write(lib, c=c, n=2000, slots=FAKE + (1 << 29), ws=FAKE + 256, wb=1 << 30) == -1
+    out = FAKE + (1 << 30)
+    assert lib.hytopk_cache_read(ctypes.byref(c), 4, out + 512, 0, out, 0, None) == -1
+
+    a = attention()
+    need = lib.hytopk_attention_mass_workspace(ctypes.byref(a))
+    q, k, idx, lse, mass, ws = (FAKE + (i << 28) for i in range(6))
+    call = lambda *v: lib.hytopk_attention_mass(ctypes.byref(a), *v, None)  # noqa: E731
+    for m in (q + 16, k + 16, idx, lse + 16):
+        assert call(q, k, idx, lse, m, None, 0) == -1
+    for w in (q, k, idx, mass):
+        assert call(q, k, idx, None, mass, w, need) == -1
+
+    score, mass, w, loss, d = (FAKE + (i << 28) for i in range(5))
+    call = lambda *v: lib.hytopk_index_loss(4, 100, *v, None)  # noqa: E731
+    for bad in (score + 16, mass - 16, w):
+        assert call(score, mass, w, loss, bad) == -1
+    for bad in (score, mass + 16, w, d + 1596):
+        assert call(score, mass, w, bad, d) == -1
+
+
+def test_limits_of_queries_and_scales(lib):
+    """A launch's threads bound the queries (wide heads take twice as many threads), and factors
+    must be finite as the kernels hold them."""
+    ws = lib.hytopk_attention_mass_workspace
+    assert ws(ctypes.byref(attention(n=(1 << 24) - 1, heads=1, d=256))) > 0
+    for d in (512, 576):
+        assert ws(ctypes.byref(attention(n=(1 << 23) - 1, heads=1, d=d))) > 0
+        a = attention(n=1 << 23, heads=1, d=d)
+        assert ws(ctypes.byref(a)) == 0
+        assert lib.hytopk_attention_mass(ctypes.byref(a), *([FAKE] * 6), 1 << 40, None) == -2
+    a = attention(scale=3e38)
+    assert lib.hytopk_attention_mass(ctypes.byref(a), *([FAKE] * 6), 1 << 40, None) == -1
+    assert rotary(lib, p=plan(gain=1e39)) == -1
+
+
+def test_yarn_of_a_context_shorter_than_a_turn():
+    """Positions below 2 pi leave every pair with less than one turn: all are divided."""
+    f = hk.Rotary(64, scaling="yarn", factor=8, original=6, device="cpu").freq
+    want = 10000.0 ** (-2 * torch.arange(32, dtype=torch.float64) / 64) / 8
+    assert torch.allclose(f, want, rtol=1e-14, atol=0)
