@@ -358,6 +358,62 @@ hipError_t mass_d(const MassArgs& a, hipStream_t s) {
   return e != hipSuccess ? e : mass_launch<NK, 1>(a, s);
 }
 
+constexpr int kBuckets = 64;
+
+// Inclusive sum over the wave's lanes up to each: within rows of 16, then over the rows.
+__device__ __forceinline__ int wave_prefix_incl(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);  // from 1, 2, 4, 8 lanes below
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);  // a row's last lane to the next row
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);  // lane 31 to the upper half
+  return x;
+}
+
+constexpr int kWaveWords = kMassLongest / kMassThreads;  // runs of 64 entries of a wave, at most
+
+// Orders a workgroup's entries by bucket, stably.  A wave holds `runs` runs of 64 of them, wave after
+// wave: key[c], or -1 for padding.  An entry goes to bucket key >> shift (below 63), padding to the last one;
+// place[c] is where it comes.  Returns the live entries.  Every wave counts its own entries, in its
+// own row of count [wave][bucket] (256 ints of LDS); one barrier, and every wave sums what precedes its part of
+// each bucket, a bucket a lane.
+__device__ __forceinline__ int order_entries(const int* key, int runs, int shift, int* count, int* place) {
+  static_assert(kBuckets == kWave, "a lane per bucket");
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  count[wave * kBuckets + lane] = 0;
+  auto bucket = [&](int c) { return key[c] >= 0 ? key[c] >> shift : kBuckets - 1; };
+#pragma unroll
+  for (int c = 0; c < kWaveWords; ++c) {
+    if (c >= runs) break;  // wave-uniform
+    const int b = bucket(c);
+    uint64_t same = ~0ull;  // lanes of the same bucket
+#pragma unroll
+    for (int bit = 0; bit < 6; ++bit) {
+      const uint64_t set = __ballot((b >> bit) & 1);
+      same &= (b >> bit) & 1 ? set : ~set;
+    }
+    const int rank = __builtin_amdgcn_mbcnt_hi((unsigned)(same >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)same, 0u));
+    int* to = &count[wave * kBuckets + b];
+    place[c] = *to + rank;
+    if (rank == 0) *to = place[c] + __builtin_popcountll(same);
+  }
+  __syncthreads();
+  int all = 0, lower = 0;  // of the lane's bucket; of the waves below
+#pragma unroll
+  for (int w = 0; w < kMassWaves; ++w) {
+    const int n = count[w * kBuckets + lane];
+    all += n;
+    lower += w < wave ? n : 0;
+  }
+  const int before = wave_prefix_incl(all) - all, mine = before + lower;
+#pragma unroll
+  for (int c = 0; c < kWaveWords; ++c) {
+    if (c < runs) place[c] += __shfl(mine, bucket(c));
+  }
+  return __builtin_amdgcn_readlane(before, kBuckets - 1);
+}
+
 // The same with the key rows staged through LDS, for rows of 128 or 256 bytes.
 // A direct-to-LDS load fetches rows whole, where gathering the operand layout gives
 // every lane its own 16 bytes of another row (from a cache that holds the keys the
@@ -378,8 +434,14 @@ hipError_t mass_d(const MassArgs& a, hipStream_t s) {
 // that kept five of sixteen blocks' logits in registers and four stages in LDS,
 // for 44% fewer bytes, 301.  Rows of 128 bytes: four stages 15.8 us against 14.8 (301 queries x 32
 // heads on 4 key heads x 500 entries of 131,072 keys, with lse).
-template <int NK, int PT, int MODE>
-__global__ void __launch_bounds__(kMassThreads, PT > 4 ? 2 : 3) mass_staged_kernel(MassArgs a, int gw) {
+//
+// With ORDER the entries are walked by key: 63 buckets of 2^order
+// keys, in the given order within one, padding last.  The workgroups of an XCD, which run side by
+// side, then pass over the same part of the keys at the same time and meet in its L2: 2,048 x 64 heads
+// of 128 x 2,048 of 131,072 keys 238 us against 264, with lse 135 against 150.  Blocks behind
+// the last live entry are left out.
+template <int NK, int PT, int MODE, bool ORDER>
+__global__ void __launch_bounds__(kMassThreads, PT > 4 ? 2 : 3) mass_staged_kernel(MassArgs a, int gw, int order) {
   constexpr int D = NK * 32, RB = D * 2, NCH = RB / 16, OPS = 16 * RB / 1024;
   constexpr int KPI = 1024 / RB;  // rows of a load
   constexpr int W = kMassWaves;
@@ -396,6 +458,8 @@ __global__ void __launch_bounds__(kMassThreads, PT > 4 ? 2 : 3) mass_staged_kern
   uint32_t* rows_at = reinterpret_cast<uint32_t*>(live64 + a.split_len / 64);
   // [gw][split_len] fp32 bits; with one pass each sum takes the place of its row, which is through by then
   uint32_t* sums = rows_at + (T > PT ? a.split_len : 0);
+  // [split_len] with ORDER: the entries' places in the row
+  uint16_t* place = reinterpret_cast<uint16_t*>(sums + gw * a.split_len);
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -403,7 +467,6 @@ __global__ void __launch_bounds__(kMassThreads, PT > 4 ? 2 : 3) mass_staged_kern
   const int gi = wave & (gw - 1), bi = wave / gw, bw = W / gw;
   ms += gi * PT * 16;
   rs += gi * PT * 16;
-  sums += gi * a.split_len;
   const int q = [] {  // a contiguous run of queries per XCD
     const int nx = 8, b = blockIdx.x, x = b % nx;
     const int base = (int)gridDim.x / nx, extra = (int)gridDim.x % nx;
@@ -411,15 +474,17 @@ __global__ void __launch_bounds__(kMassThreads, PT > 4 ? 2 : 3) mass_staged_kern
   }();
   const int split = blockIdx.y;
   const int j0 = split * a.split_len, nj = min(a.split_len, a.topk - j0);
-  for (int j = tid; j < a.split_len; j += kMassThreads) {  // whole waves: split_len is a multiple of 64
-    const int id = j < nj ? a.idx[(int64_t)q * a.topk + j0 + j] : -1;
-    const bool on = (unsigned)id < (unsigned)a.L;
-    const uint64_t live = __ballot(on);
-    rows_at[j] = on ? (uint32_t)id * (uint32_t)(a.groups * NCH) : 0u;
-    if (lane == 0) live64[j >> 6] = live;
-  }
-  const int nblk = (nj + 15) / 16;
-  const int have = bi < nblk ? (nblk - bi + bw - 1) / bw : 0;  // blocks of this wave: bi + i * bw
+  uint32_t* const all_sums = sums;
+  sums += gi * a.split_len;
+  const int words = a.split_len / 64;  // split_len is a multiple of 64
+  // blocks of this wave, bi + i * bw, up to the last live entry
+  auto blocks = [&] {
+    const uint64_t w = lane < words ? live64[lane] : 0, any = __ballot(w != 0);
+    if (!any) return 0;
+    const int top = 63 - __builtin_clzll(any);
+    const int nblk = top * 4 + (63 - __builtin_clzll(live64[top])) / 16 + 1;
+    return __builtin_amdgcn_readfirstlane(bi < nblk ? (nblk - bi + bw - 1) / bw : 0);
+  };
   uint8_t* const ring0 = ring + wave * 16 * RB;  // stage s: + s * SLOT
   constexpr int SLOT = W * 16 * RB;
   int dsw[OPS];  // load p fetches this chunk of its row (the stage's swizzle)
@@ -449,21 +514,24 @@ __global__ void __launch_bounds__(kMassThreads, PT > 4 ? 2 : 3) mass_staged_kern
     for (int s = 0; s < NK; ++s) f[s] = __builtin_bit_cast(bf16x8, r[s]);
   };
 
-  for (int gp = 0, ta = 0; gp < a.groups;) {
-    // tiles of this pass: ta .. ta + nt - 1 of key head g, c0 on of the query
-    const int g = gp + gi, c0 = g * ht.tiles + ta;
-    const bool in = g < a.groups, first = gp == 0 && ta == 0;
-    const int nt = in ? min(PT, ht.tiles - ta) : 0, mine = in ? have : 0;
-    const bool last = gp + gw >= a.groups && ta + PT >= ht.tiles;
-    const uint8_t* kg = reinterpret_cast<const uint8_t*>(a.k) + g * RB;
-    bf16x8 qf[PT][NK];
+  // The q rows of a pass, tiles ta on of key head gp + gi, and (MODE 1) their softmax statistics.
+  bf16x8 qf[PT][NK];
+  auto take = [&](int gp, int ta) {
+    const int g = gp + gi, c0 = g * ht.tiles + ta, nt = g < a.groups ? min(PT, ht.tiles - ta) : 0;
 #pragma unroll
     for (int t = 0; t < PT; ++t) {
       const int h = t < nt ? ht.head(c0 + t, col) : -1;
       const uint16_t* p = a.q + ((int64_t)q * a.heads + max(h, 0)) * D + grp * 8;
 #pragma unroll
-      for (int s = 0; s < NK; ++s)
-        qf[t][s] = h >= 0 ? *reinterpret_cast<const bf16x8*>(p + s * 32) : bf16x8{};
+      for (int s = 0; s < NK; ++s) qf[t][s] = *reinterpret_cast<const bf16x8*>(p + s * 32);
+    }
+    if (nt < PT || ht.per_group % 16) {  // rows of no head; apart, so that all loads are under way at once
+#pragma unroll
+      for (int t = 0; t < PT; ++t) {
+        if (t < nt && ht.head(c0 + t, col) >= 0) continue;
+#pragma unroll
+        for (int s = 0; s < NK; ++s) qf[t][s] = bf16x8{};
+      }
     }
     if constexpr (MODE == 1) {
       for (int e = bi * kWave + lane; e < PT * 64; e += bw * kWave) {  // a quad per row, by this key head's waves
@@ -482,7 +550,53 @@ __global__ void __launch_bounds__(kMassThreads, PT > 4 ? 2 : 3) mass_staged_kern
         }
       }
     }
-    __syncthreads();
+  };
+  // The entries into LDS.
+  const int* idx = a.idx + (int64_t)q * a.topk + j0;
+  auto row_of = [&](int key) { return key >= 0 ? (uint32_t)key * (uint32_t)(a.groups * NCH) : 0u; };
+  const int w0 = wave * words / W, runs = (wave + 1) * words / W - w0;  // the wave's: 64 w0 on
+  int key[kWaveWords];
+#pragma unroll
+  for (int c = 0; c < kWaveWords; ++c) key[c] = idx[min((w0 + c) * 64 + lane, nj - 1)];  // all under way at once
+  take(0, 0);
+#pragma unroll
+  for (int c = 0; c < kWaveWords; ++c) {
+    const bool on = (w0 + c) * 64 + lane < nj && (unsigned)key[c] < (unsigned)a.L;
+    key[c] = on ? key[c] : -1;
+  }
+  if constexpr (ORDER) {
+    int to[kWaveWords];
+    const int live = order_entries(key, runs, order, reinterpret_cast<int*>(ring), to);
+    const int left = live - tid * 64;
+    if (tid < words) live64[tid] = left >= 64 ? ~0ull : left > 0 ? (1ull << left) - 1 : 0;
+#pragma unroll
+    for (int c = 0; c < kWaveWords; ++c) {
+      if (c >= runs) break;  // wave-uniform
+      rows_at[to[c]] = row_of(key[c]);
+      place[to[c]] = (uint16_t)((w0 + c) * 64 + lane);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < kWaveWords; ++c) {
+      if (c >= runs) break;  // wave-uniform
+      const uint64_t live = __ballot(key[c] >= 0);
+      rows_at[(w0 + c) * 64 + lane] = row_of(key[c]);
+      if (lane == 0) live64[w0 + c] = live;
+    }
+  }
+  if (T > PT && MODE != 0) {  // what no block reaches
+    for (int j = tid; j < gw * a.split_len; j += kMassThreads) all_sums[j] = 0u;
+  }
+  __syncthreads();
+  const int have = blocks();
+
+  for (int gp = 0, ta = 0;;) {
+    // tiles of this pass: ta .. ta + nt - 1 of key head g, c0 on of the query
+    const int g = gp + gi, c0 = g * ht.tiles + ta;
+    const bool in = g < a.groups, first = gp == 0 && ta == 0;
+    const int nt = in ? min(PT, ht.tiles - ta) : 0, mine = in ? have : 0;
+    const bool last = gp + gw >= a.groups && ta + PT >= ht.tiles;
+    const uint8_t* kg = reinterpret_cast<const uint8_t*>(a.k) + g * RB;
 
     if constexpr (MODE != 1) {
       float m[PT], l[PT];
@@ -597,22 +711,57 @@ __global__ void __launch_bounds__(kMassThreads, PT > 4 ? 2 : 3) mass_staged_kern
       }
       if (last) {
         __syncthreads();
-        const uint32_t* all = sums - gi * a.split_len;
-        for (int j = tid; j < nj; j += kMassThreads) {
-          float o = __uint_as_float(all[j]);
-          for (int k = 1; k < gw; ++k) o += __uint_as_float(all[k * a.split_len + j]);
-          a.mass[(int64_t)q * a.topk + j0 + j] = o * a.inv_heads;
+        auto total = [&](int j) {
+          float o = __uint_as_float(all_sums[j]);
+          for (int k = 1; k < gw; ++k) o += __uint_as_float(all_sums[k * a.split_len + j]);
+          return o * a.inv_heads;
+        };
+        if constexpr (ORDER) {  // back to their places, within the LDS
+          float o[kWaveWords];
+          int to[kWaveWords];
+#pragma unroll
+          for (int c = 0; c < kWaveWords; ++c) {
+            const int j = tid + c * kMassThreads;
+            o[c] = j < a.split_len ? total(j) : 0.0f;
+            to[c] = j < a.split_len ? place[j] : -1;
+          }
+          __syncthreads();
+#pragma unroll
+          for (int c = 0; c < kWaveWords; ++c)
+            if (to[c] >= 0) all_sums[to[c]] = __float_as_uint(o[c]);
+          __syncthreads();
+          for (int j = tid; j < nj; j += kMassThreads)
+            a.mass[(int64_t)q * a.topk + j0 + j] = __uint_as_float(all_sums[j]);
+        } else {
+          for (int j = tid; j < nj; j += kMassThreads) a.mass[(int64_t)q * a.topk + j0 + j] = total(j);
         }
       }
     }
     ta += PT;
     if (ta >= ht.tiles) { ta = 0; gp += gw; }
-    if (!last) __syncthreads();
+    if (last) break;
+    __syncthreads();
+    take(gp, ta);
+    __syncthreads();
   }
 }
 
-template <int NK, int PT, int MODE>
-hipError_t mass_staged_launch(const MassArgs& a, hipStream_t s) {
+// Entries by key (in buckets of 2^order keys, 63 at most) where that saves more than it takes: queries
+// that fill the chip, long rows, keys beyond two L2s (8 MiB).  Given order against by key, 64 heads of
+// 128 on one key head, without lse: 2,048 queries x 2,048 entries of 131,072 keys 264 us, 238; x 1,024 135,
+// 128; x 512 70, 72; x 2,048 of 65,536 keys 231, 202; of 32,768 (8 MiB) 197, 199; 600 x 2,048 92, 83;
+// 301 x 2,048 54, 58; 8 key heads, 2,048 x 2,048 of 65,536 1,976, 1,328.  Passes of more than four
+// tiles run two waves per SIMD: 128 heads with lse 185, 187.
+template <int NK>
+int mass_order(const MassArgs& a) {
+  if (a.n <= 512 || a.topk < 1024 || (int64_t)a.L * a.groups * NK * 64 <= int64_t(8) << 20) return -1;
+  int order = 0;
+  while ((a.L - 1) >> order >= kBuckets - 1) ++order;
+  return order;
+}
+
+template <int NK, int PT, int MODE, bool ORDER>
+hipError_t mass_staged_launch(const MassArgs& a, int order, hipStream_t s) {
   static LdsLimit lim;
   // Key heads side by side where queries are few and their sums take no more LDS than one row of
   // 2,048 (without lse, 301 queries x 4 key heads x 500 entries: 26 us against 32; 2,048 queries: 146
@@ -621,20 +770,29 @@ hipError_t mass_staged_launch(const MassArgs& a, hipStream_t s) {
   while (a.n <= 512 && gw < kMassWaves && 2 * gw <= a.groups && 2 * gw * a.split_len <= 2048) gw *= 2;
   const bool apart = mass_rows(a.heads, a.groups) > PT * 16;  // sums beside the rows
   const int lds = 2 * kMassWaves * 16 * NK * 64 + PT * 16 * 8 * (gw + kMassWaves) + a.split_len / 8 +
-                  a.split_len * 4 * (apart ? 1 + gw : 1);
-  hipError_t e = raise_dynamic_lds((const void*)mass_staged_kernel<NK, PT, MODE>, lds, lim);
+                  a.split_len * 4 * (apart ? 1 + gw : 1) + (ORDER ? a.split_len * 2 : 0);
+  hipError_t e = raise_dynamic_lds((const void*)mass_staged_kernel<NK, PT, MODE, ORDER>, lds, lim);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((mass_staged_kernel<NK, PT, MODE>), dim3((unsigned)a.n, (unsigned)a.nsplit),
-                     dim3(kMassThreads), (size_t)lds, s, a, gw);
+  hipLaunchKernelGGL((mass_staged_kernel<NK, PT, MODE, ORDER>), dim3((unsigned)a.n, (unsigned)a.nsplit),
+                     dim3(kMassThreads), (size_t)lds, s, a, gw, order);
   return hipGetLastError();
+}
+
+template <int NK, int PT, int MODE>
+hipError_t mass_staged_mode(const MassArgs& a, hipStream_t s) {
+  if constexpr (PT <= 4 && MODE != 0) {
+    const int order = mass_order<NK>(a);
+    if (order >= 0) return mass_staged_launch<NK, PT, MODE, true>(a, order, s);
+  }
+  return mass_staged_launch<NK, PT, MODE, false>(a, -1, s);
 }
 
 template <int NK, int PT>
 hipError_t mass_staged_pt(const MassArgs& a, hipStream_t s) {
-  if (a.lse) return mass_staged_launch<NK, PT, 1>(a, s);
-  if (a.nsplit == 1) return mass_staged_launch<NK, PT, 2>(a, s);
-  hipError_t e = mass_staged_launch<NK, PT, 0>(a, s);
-  return e != hipSuccess ? e : mass_staged_launch<NK, PT, 1>(a, s);
+  if (a.lse) return mass_staged_mode<NK, PT, 1>(a, s);
+  if (a.nsplit == 1) return mass_staged_mode<NK, PT, 2>(a, s);
+  hipError_t e = mass_staged_mode<NK, PT, 0>(a, s);
+  return e != hipSuccess ? e : mass_staged_mode<NK, PT, 1>(a, s);
 }
 
 // Tiles of a pass: those of a key head, up to eight (q rows in 4 NK registers a tile).  From five on

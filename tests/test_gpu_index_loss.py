@@ -332,3 +332,60 @@ def test_loss_outputs_aliases_and_unaligned_rows(hk):
     assert torch.allclose(l2, loss, rtol=1e-5, atol=1e-6) and torch.allclose(g2, grad, rtol=1e-5, atol=1e-7)
     l0, g0 = hk.index_loss(score[:0], mass[:0])
     assert l0.shape == (0,) and g0.shape == (0, 64)
+
+
+BY_KEY = [  # rows long enough, of many queries on many keys, that their entries are walked by key:
+    # k, heads, key heads, d, L
+    (1024, 64, 1, 128, 33000), (2047, 5, 1, 64, 66001), (1500, 40, 4, 64, 20000), (2048, 48, 1, 128, 131072),
+    (1030, 100, 2, 128, 17000), (1777, 32, 1, 64, 70000), (1100, 17, 1, 128, 40000), (1200, 33, 3, 64, 30000),
+]
+
+
+@pytest.mark.parametrize("case", BY_KEY)
+def test_mass_of_entries_in_any_order(hk, case):
+    """Rows sorted by key, reversed, of one key, of one bucket, with padding of both signs anywhere, the last
+    key among them: each entry's mass comes back at its own place, and the same bits every time."""
+    k, heads, groups, d, L = case
+    n = 600
+    say(f"mass by key: {case}")
+    q, keys, idx = _inputs(n, k, heads, groups, d, L, sum(case) + 1, pad=0.0)
+    idx[0] = idx[0].sort().values
+    idx[1] = idx[1].sort(descending=True).values
+    idx[2] = L - 1
+    idx[3] = torch.arange(k, dtype=torch.int32) % 200
+    idx[4, ::3] = -7
+    idx[4, 1::5] = L
+    idx[5] = 2 ** 31 - 1
+    idx[6, :-1] = -1
+    idx[7, 1:] = -(2 ** 31)
+    idx[8] = L - 1 - torch.arange(k, dtype=torch.int32)
+    idx[9, 64:] = -1
+    g = torch.Generator().manual_seed(3)
+    lse = (torch.rand((n, heads), generator=g) * 3 + 8)
+    dev = [t.cuda() for t in (q, keys, idx)]
+    out = hk.attention_mass(*dev)
+    given = hk.attention_mass(*dev, lse=lse.cuda())
+    some = torch.cat([torch.arange(10), torch.tensor([300, n - 1])])
+    _mass_check(out[some], q[some], keys, idx[some], d ** -0.5)
+    _mass_check(given[some], q[some], keys, idx[some], d ** -0.5, lse[some])
+    assert torch.equal(out, hk.attention_mass(*dev)) and torch.equal(given, hk.attention_mass(*dev, lse=lse.cuda()))
+    dead = (idx < 0) | (idx >= L)
+    assert not out.cpu()[dead].any() and not given.cpu()[dead].any()
+
+
+@pytest.mark.parametrize("n,k,heads,groups,d", [(5, 700, 16, 1, 128), (600, 200, 32, 4, 64), (301, 500, 32, 4, 64), (3, 150, 200, 2, 64)])
+def test_mass_of_rows_that_end_early(hk, n, k, heads, groups, d):
+    """Blocks behind a row's last entry are left out: rows that end before, at and behind a block, and a
+    split without an entry."""
+    q, keys, idx = _inputs(n, k, heads, groups, d, 900, 77, pad=0.0)
+    ends = [0, 1, 15, 16, 17, 63, 64, 65, k - 1, k]
+    for i in range(n):
+        idx[i, ends[i % len(ends)]:] = -1
+    idx[min(n - 1, 2), k - 1] = 5  # one entry at the very end
+    lse = torch.full((n, heads), 9.0)
+    some = torch.arange(min(n, 12))
+    dev = [t.cuda() for t in (q, keys, idx)]
+    _mass_check(hk.attention_mass(*dev)[some], q[some], keys, idx[some], d ** -0.5)
+    given = hk.attention_mass(*dev, lse=lse.cuda())
+    _mass_check(given[some], q[some], keys, idx[some], d ** -0.5, lse[some])
+    assert not given.cpu()[idx < 0].any()
