@@ -496,9 +496,11 @@ __global__ void __launch_bounds__(kMassThreads, PT > 4 ? 2 : 3) mass_staged_kern
   // the wave's i-th block, from kg (the key head's first byte), into its stage i % 2
   auto issue = [&](int i, const uint8_t* kg) {
     uint8_t* to = ring0 + (i & 1) * SLOT;
+    uint32_t at[OPS];  // read together, ahead of the loads
 #pragma unroll
-    for (int p = 0; p < OPS; ++p)
-      lds_dma16(kg + dsw[p] + ((uint64_t)my_rows[i * bw * 16 + p * KPI] << 4), to + p * 1024);
+    for (int p = 0; p < OPS; ++p) at[p] = my_rows[i * bw * 16 + p * KPI];
+#pragma unroll
+    for (int p = 0; p < OPS; ++p) lds_dma16(kg + dsw[p] + ((uint64_t)at[p] << 4), to + p * 1024);
   };
   const uint32_t ring_at = lds_addr(ring0);
   uint32_t chunk_at[NK];
@@ -615,34 +617,51 @@ __global__ void __launch_bounds__(kMassThreads, PT > 4 ? 2 : 3) mass_staged_kern
         frags(i, f);
         // lane: keys 4 grp .. + 3 of the block, head col of each tile
         const unsigned all = __builtin_amdgcn_readfirstlane(live16[bi + i * bw]), live = all >> (4 * grp);
+        // Tiles in pairs whose products are under way together, one branch a pair for a maximum that moves
+        // and a copy of it all for blocks with padding (a branch a tile for each: 96 heads of 128 298 us against
+        // 272, 64 heads 232 against 228).
+        constexpr int TG = PT % 2 ? PT : 2;
+        auto add = [&](auto padded) {
 #pragma unroll
-        for (int t = 0; t < PT; ++t) {
-          f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+          for (int t0 = 0; t0 < PT; t0 += TG) {
+            f32x4 acc[TG];
 #pragma unroll
-          for (int s = 0; s < NK; ++s)
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[s], qf[t][s], acc, 0, 0, 0);
-          float y[4];  // padding takes no part, whatever its row holds
+            for (int u = 0; u < TG; ++u) acc[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) y[e] = fmaf(acc[e], a.scale2, -m[t]);
-          if (all != 0xffffu) {
+            for (int s = 0; s < NK; ++s)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = (live >> e) & 1u ? y[e] : -__builtin_inff();
-          }
-          const float over = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
-          if (__any(over > kLazy)) {
-            float x[4];
+              for (int u = 0; u < TG; ++u)
+                acc[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[s], qf[t0 + u][s], acc[u], 0, 0, 0);
+            // padding takes no part, whatever its row holds
+            auto value = [&](int u, int e) {
+              const float y = fmaf(acc[u][e], a.scale2, -m[t0 + u]);
+              return !padded.value || ((live >> e) & 1u) ? y : -__builtin_inff();
+            };
+            float over = -__builtin_inff();
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = (live >> e) & 1u ? acc[e] * a.scale2 : -__builtin_inff();
-            const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-            if (top > m[t] + kLazy) {
-              l[t] *= exp2_fast(m[t] - top);
-              m[t] = top;
+            for (int u = 0; u < TG; ++u)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) over = fmaxf(over, value(u, e));
+            if (__any(over > kLazy)) {
+#pragma unroll
+              for (int u = 0; u < TG; ++u) {
+                float top = -__builtin_inff();
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  top = !padded.value || ((live >> e) & 1u) ? fmaxf(top, acc[u][e] * a.scale2) : top;
+                if (top > m[t0 + u] + kLazy) {
+                  l[t0 + u] *= exp2_fast(m[t0 + u] - top);
+                  m[t0 + u] = top;
+                }
+              }
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = (live >> e) & 1u ? fmaf(acc[e], a.scale2, -m[t]) : -__builtin_inff();
+            for (int u = 0; u < TG; ++u)
+              l[t0 + u] += (exp2_fast(value(u, 0)) + exp2_fast(value(u, 1))) + (exp2_fast(value(u, 2)) + exp2_fast(value(u, 3)));
           }
-          l[t] += (exp2_fast(y[0]) + exp2_fast(y[1])) + (exp2_fast(y[2]) + exp2_fast(y[3]));
-        }
+        };
+        if (all == 0xffffu) add(std::false_type{});
+        else add(std::true_type{});
       }
 #pragma unroll
       for (int t = 0; t < PT; ++t) {
