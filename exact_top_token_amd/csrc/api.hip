@@ -847,12 +847,10 @@ hk::RotArgs rot_args(const hytopk_rotary_plan* p, const int32_t* q_pos, int64_t 
   if (!p) return r;
   r.freq = p->freq;
   r.pos = q_pos;
-  r.pos0 = q_start;
+  r.pos0 = (int)q_start;  // below 2^31
   r.gain = (float)p->gain;
-  r.sign = backward ? -1.0f : 1.0f;
+  r.turn = backward ? -r.gain : r.gain;
   r.dim = p->dim;
-  r.first = p->first;
-  r.layout = p->layout;
   return r;
 }
 
@@ -991,10 +989,11 @@ int hytopk_rotary(const hytopk_rotary_plan* plan, int64_t n, int32_t heads, int3
     a.n = (int)n;
     a.heads = heads;
     a.d = d;
+    a.first = plan->first;
     a.rot = rot_args(plan, q_pos, q_start, backward != 0);
     hipStream_t s = static_cast<hipStream_t>(stream);
     Span sp("rotary", s);
-    HK_HIP(hk::launch_rotary(a, x->dtype, y->dtype, s), "rotary launch");
+    HK_HIP(hk::launch_rotary(a, plan->layout, x->dtype, y->dtype, s), "rotary launch");
     return HYTOPK_OK;
   });
 }
@@ -1031,18 +1030,17 @@ int hytopk_cache_write(const hytopk_cache* c, int64_t n, const hytopk_rows* x,
     a.ts = x->token_stride;
     a.hs = x->head_stride;
     a.n = (int)n;
-    a.heads = c->heads;
-    a.d = c->d;
+    a.first = plan ? plan->first : 0;
     a.rot = rot_args(plan, q_pos, q_start, false);
     a.codes = static_cast<uint8_t*>(c->codes);
     a.scale = c->scale;
     a.L = (int)c->L;
     a.slots = slots;
-    a.start = start;
+    a.start = (int)start;
     a.claim = claim ? static_cast<int*>(workspace) : nullptr;
     hipStream_t s = static_cast<hipStream_t>(stream);
     Span sp("cache_write", s);
-    HK_HIP(hk::launch_cache_write(a, x->dtype, c->dtype, s), "cache write launch");
+    HK_HIP(hk::launch_cache_write(a, c->heads, c->d, plan ? plan->layout : 0, x->dtype, c->dtype, s), "cache write launch");
     return HYTOPK_OK;
   });
 }
@@ -1066,7 +1064,7 @@ int hytopk_cache_read(const hytopk_cache* c, int64_t n, const int32_t* slots, in
     a.scale = c->scale;
     a.L = (int)c->L;
     a.slots = slots;
-    a.start = start;
+    a.start = (int)start;
     a.n = (int)n;
     a.row = c->heads * c->d;
     a.out = out;

@@ -256,56 +256,55 @@ size_t bwd_sort_hist_count(int64_t N);
 constexpr int kRowsBF16 = 0, kRowsFP32 = 1;            // hytopk_rows_dtype
 constexpr int kRotHalf = 0, kRotInterleaved = 1;       // hytopk_rotary_layout
 
+// What a launch takes on the host grows from 2.8 to 3.6 us where a kernel's arguments pass 112 bytes,
+// the grid's and block's sizes (gridDim, blockDim: about 70 bytes) among them.  The kernels of rows.hip
+// and loss.hip are often shorter than that, so their arguments stay within it and they read neither.
+
 // A rotation (freq == null: none) and the tokens' positions.
 struct RotArgs {
   const double* freq;  // [dim/2] radians a position
   const int* pos;      // [n] positions, or null (pos0 + i)
-  int64_t pos0;
-  float gain;
-  float sign;          // 1, or -1 for the transposed rotation
+  int pos0;
+  float gain;          // factor on the cosines
+  float turn;          // factor on the sines: gain, or -gain for the transposed rotation
   int dim;
-  int first;
-  int layout;
 };
 
 struct RotaryArgs {
   const void* x;
   void* y;
   int64_t xts, xhs, yts, yhs;  // token and head strides in elements
-  int n, heads, d;
   RotArgs rot;
+  int n, heads, d, first;      // first: where the rotated part begins
 };
 
-hipError_t launch_rotary(const RotaryArgs& a, int in_dtype, int out_dtype, hipStream_t s);
+hipError_t launch_rotary(const RotaryArgs& a, int layout, int in_dtype, int out_dtype, hipStream_t s);
 
 struct CacheWriteArgs {
   const void* x;
   int64_t ts, hs;
-  int n, heads, d;
-  RotArgs rot;
   uint8_t* codes;
   void* scale;
-  int L;
   const int* slots;    // [n] cache rows, or null (start + i)
-  int64_t start;
   int* claim;          // [L] last row naming each slot, or null (each row looks for a later one)
+  RotArgs rot;
+  int n, L, start, first;
 };
 
 // Rows up to this many look for a later row of the same slot by themselves; more take
 // `claim`.  FP8 rows of 128 on the GPU: 512, 1,024, 2,048 rows 6.8, 9.6, 15.5 us looking and
 // 8.0 claiming, whose two more launches take the host another 5 us.
 constexpr int kClaimRows = 1024;
-hipError_t launch_cache_write(const CacheWriteArgs& a, int in_dtype, int fmt, hipStream_t s);
+hipError_t launch_cache_write(const CacheWriteArgs& a, int heads, int d, int layout, int in_dtype, int fmt,
+                              hipStream_t s);
 
 struct CacheReadArgs {
   const uint8_t* codes;
   const void* scale;
-  int L;
   const int* slots;
-  int64_t start;
-  int n;
-  int row;             // elements of a row (heads * d)
   void* out;
+  int L, start, n;
+  int row;             // elements of a row (heads * d)
 };
 
 hipError_t launch_cache_read(const CacheReadArgs& a, int out_dtype, int fmt, hipStream_t s);

@@ -13,6 +13,8 @@ namespace hk {
 
 namespace {
 
+static_assert(sizeof(MassArgs) + 2 * sizeof(int) <= 112, "launches");
+
 constexpr int kMassThreads = 256;
 constexpr int kMassWaves = kMassThreads / kWave;
 constexpr int kWideSteps = 16;     // k-steps of a row from which on a wave holds two blocks and no second buffer
@@ -128,9 +130,9 @@ __global__ void __launch_bounds__(W * kWave) mass_kernel(MassArgs a, int pass) {
   const int col = lane & 15, grp = lane >> 4;
   // Workgroups go to the 8 XCDs in turn; each XCD takes a contiguous run of
   // queries, whose selections overlap, so that their keys meet in its L2.
-  const int q = [] {
+  const int q = [&] {
     const int nx = 8, b = blockIdx.x, x = b % nx;
-    const int base = (int)gridDim.x / nx, extra = (int)gridDim.x % nx;
+    const int base = a.n / nx, extra = a.n % nx;
     return x * base + min(x, extra) + b / nx;
   }();
   const int split = blockIdx.y;
@@ -467,9 +469,9 @@ __global__ void __launch_bounds__(kMassThreads, PT > 4 ? 2 : 3) mass_staged_kern
   const int gi = wave & (gw - 1), bi = wave / gw, bw = W / gw;
   ms += gi * PT * 16;
   rs += gi * PT * 16;
-  const int q = [] {  // a contiguous run of queries per XCD
+  const int q = [&] {  // a contiguous run of queries per XCD
     const int nx = 8, b = blockIdx.x, x = b % nx;
-    const int base = (int)gridDim.x / nx, extra = (int)gridDim.x % nx;
+    const int base = a.n / nx, extra = a.n % nx;
     return x * base + min(x, extra) + b / nx;
   }();
   const int split = blockIdx.y;
@@ -877,6 +879,7 @@ hipError_t launch_attention_mass(const MassArgs& a, int d, hipStream_t s) {
 namespace {
 
 constexpr int kLossThreads = 256;
+constexpr int64_t kMostLossBlocks = int64_t(1) << 22;  // workgroups walk the rest in steps of so many
 
 __device__ __forceinline__ float wave_sum(float x) {
 #pragma unroll
@@ -897,7 +900,7 @@ template <int N, bool VEC, bool PAST>
 __global__ void __launch_bounds__(kLossThreads, 4) index_loss_kernel(LossArgs a) {
   const int lane = threadIdx.x & 63;
   constexpr int W = kLossThreads / kWave;
-  for (int64_t i = (int64_t)blockIdx.x * W + (threadIdx.x >> 6); i < a.n; i += (int64_t)gridDim.x * W) {
+  for (int64_t i = (int64_t)blockIdx.x * W + (threadIdx.x >> 6); i < a.n; i += kMostLossBlocks * W) {
     const int64_t at = i * a.k;
     float s[N], t[N];
     // entry j of this lane: pieces of four (VEC), or every 64th
@@ -985,7 +988,7 @@ __global__ void __launch_bounds__(kLossThreads, 4) index_loss_kernel(LossArgs a)
 template <bool VEC, bool PAST>
 hipError_t index_loss_vec(const LossArgs& a, hipStream_t s) {
   const int64_t w = kLossThreads / kWave;
-  const dim3 grid((unsigned)std::min<int64_t>((a.n + w - 1) / w, int64_t(1) << 22)), block(kLossThreads);
+  const dim3 grid((unsigned)std::min<int64_t>((a.n + w - 1) / w, kMostLossBlocks)), block(kLossThreads);
   if (a.k <= 256) hipLaunchKernelGGL((index_loss_kernel<4, VEC, PAST>), grid, block, 0, s, a);
   else if (a.k <= 512) hipLaunchKernelGGL((index_loss_kernel<8, VEC, PAST>), grid, block, 0, s, a);
   else if (a.k <= 1024) hipLaunchKernelGGL((index_loss_kernel<16, VEC, PAST>), grid, block, 0, s, a);

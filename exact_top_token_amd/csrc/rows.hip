@@ -17,9 +17,10 @@ constexpr int kRowThreads = 256;  // threads of a workgroup (a write of long row
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 
 // Workgroups along the rows: one per `per` rows, at most 2^21 (a launch holds
-// fewer than 2^32 threads); the kernels walk the rest.
+// fewer than 2^32 threads); the kernels walk the rest in steps of so many.
+constexpr int64_t kMostBlocks = int64_t(1) << 21;
 unsigned row_blocks(int64_t n, int64_t per) {
-  return (unsigned)std::min<int64_t>((n + per - 1) / per, int64_t(1) << 21);
+  return (unsigned)std::min<int64_t>((n + per - 1) / per, kMostBlocks);
 }
 
 // ------------------------------------------------------- element access
@@ -180,14 +181,14 @@ __device__ __forceinline__ float2 turn_cos_sin(float t) {
                      __uint_as_float(__float_as_uint(ss) ^ (((unsigned)q & 2u) << 30)));
 }
 
-// gain * (cos, sign * sin) at position pos, f turns a position.  The angle is formed and
+// (gain cos, turn sin) at position pos, f turns a position.  The angle is formed and
 // reduced to [-1/2, 1/2] in 64 bits: at 2^31 positions its error is below
 // 1e-7 turns, at 2^20 below 1e-10, where 32 bits would keep none of it.
 __device__ __forceinline__ float2 rot_entry(const RotArgs& r, double f, int64_t pos) {
   double t = (double)pos * f;
   t -= rint(t);
   const float2 c = turn_cos_sin((float)t);
-  return make_float2(c.x * r.gain, c.y * (r.gain * r.sign));
+  return make_float2(c.x * r.gain, c.y * r.turn);
 }
 
 // One half of a rotated pair: v cos -+ w sin.  Written as one product and one fused
@@ -199,7 +200,8 @@ __device__ __forceinline__ float rot_hi(float v, float w, float2 f) { return fma
 // u / by for u * by < 2^22 (the error of the rounded-up reciprocal stays below 1 / by).
 struct SmallDiv {
   unsigned by, mul;
-  __host__ SmallDiv(unsigned d) : by(d), mul(((1u << 22) + d - 1) / d) {}
+  __host__ __device__ SmallDiv(unsigned d, unsigned m) : by(d), mul(m) {}
+  __host__ explicit SmallDiv(unsigned d) : SmallDiv(d, ((1u << 22) + d - 1) / d) {}
   __device__ __forceinline__ unsigned operator()(unsigned u) const {
     return (unsigned)(((uint64_t)u * mul) >> 22);
   }
@@ -230,17 +232,17 @@ __device__ __forceinline__ void rot_read(const float2* cs, int half, int u, floa
 // The entries of tokens t0 .. t0 + nt - 1, once for all their heads: [nt][dim/2]
 // (at most 2,048 entries, or one token's).
 template <int W>
-__device__ __forceinline__ void rot_table(const RotArgs& r, int64_t t0, int nt, float2* cs) {
+__device__ __forceinline__ void rot_table(const RotArgs& r, int64_t t0, int nt, int threads, float2* cs) {
   const int half = r.dim >> 1;
   // a thread keeps its pair, whose frequency it loads once, and walks over tokens
-  const int threads = blockDim.x, cols = min(half, threads), steps = threads / cols;
+  const int cols = min(half, threads), steps = threads / cols;
   const int first = threadIdx.x / cols;
   if (first >= steps) return;
   for (int i = threadIdx.x - first * cols; i < half; i += cols) {
     const double f = r.freq[i] * 0.15915494309189533577;  // turns a position
     float2* to = cs + rot_slot<W>(i, half);
     for (int t = first; t < nt; t += steps) {
-      const int64_t pos = r.pos ? (int64_t)r.pos[t0 + t] : r.pos0 + t0 + t;
+      const int64_t pos = r.pos ? (int64_t)r.pos[t0 + t] : (int64_t)r.pos0 + t0 + t;
       to[t * half] = rot_entry(r, f, pos);
     }
   }
@@ -255,10 +257,11 @@ __device__ __forceinline__ void rot_table(const RotArgs& r, int64_t t0, int nt, 
 // access (VEC), eight pairs of the half layout (two 16-byte pieces), four pairs of
 // the interleaved one, or eight elements outside the rotated part; else one pair or one element.
 struct RotaryGrid {
-  int tb, hb;    // tokens and heads of a workgroup
-  int units;     // units of a head
-  int rows;      // (token, head) rows in flight: threads / units
+  uint16_t tb, hb;    // tokens and heads of a workgroup: at most 1,024 and 32,768
+  uint16_t units;     // units of a head, at most 256
+  uint16_t rows;      // (token, head) rows in flight: threads / units
 };
+static_assert(sizeof(RotaryArgs) + sizeof(RotaryGrid) <= 112, "launches");
 
 namespace {
 
@@ -267,15 +270,15 @@ __global__ void __launch_bounds__(kRowThreads) rotary_kernel(RotaryArgs a, Rotar
   extern __shared__ __attribute__((aligned(16))) float2 cs[];
   const RotArgs& r = a.rot;
   const int half = r.dim >> 1;
-  const int h0 = blockIdx.y * g.hb, nh = min(g.hb, a.heads - h0);
+  const int h0 = blockIdx.y * g.hb, nh = min((int)g.hb, a.heads - h0);
   const int ts = g.rows / nh, hs = g.rows - ts * nh;
   constexpr int W = VEC ? 8 : 1;                            // elements of a copy unit
   constexpr int PW = VEC ? (LAYOUT == kRotHalf ? 8 : 4) : 1;  // pairs of a rotated unit
   const int nrot = half / PW;
-  for (int64_t tile = blockIdx.x; tile * g.tb < a.n; tile += gridDim.x) {
-    const int t0 = (int)(tile * g.tb), nt = min(g.tb, a.n - t0);
+  for (int64_t tile = blockIdx.x; tile * g.tb < a.n; tile += kMostBlocks) {
+    const int t0 = (int)(tile * g.tb), nt = min((int)g.tb, a.n - t0);
     if (tile != blockIdx.x) __syncthreads();  // the last tile's entries are read
-    rot_table<PW>(r, t0, nt, cs);
+    rot_table<PW>(r, t0, nt, kRowThreads, cs);
     __syncthreads();
     // Units wider than the workgroup (heads of many elements without 16-byte
     // access) are walked in steps of the workgroup.
@@ -285,10 +288,10 @@ __global__ void __launch_bounds__(kRowThreads) rotary_kernel(RotaryArgs a, Rotar
       const bool rot = u < nrot;
       int e;  // the unit's first element in the head
       if (rot) {
-        e = r.first + (LAYOUT == kRotHalf ? u * PW : 2 * u * PW);
+        e = a.first + (LAYOUT == kRotHalf ? u * PW : 2 * u * PW);
       } else {
         e = (u - nrot) * W;
-        if (e >= r.first) e += r.dim;
+        if (e >= a.first) e += r.dim;
       }
       int t = row / nh, h = row - t * nh;
       while (t < nt) {
@@ -343,27 +346,25 @@ __global__ void __launch_bounds__(kRowThreads) rotary_kernel(RotaryArgs a, Rotar
 }
 
 template <int IN, int OUT>
-hipError_t rotary_io(const RotaryArgs& a, bool vec, hipStream_t s) {
+hipError_t rotary_io(const RotaryArgs& a, int layout, bool vec, hipStream_t s) {
   const RotArgs& r = a.rot;
-  const int pw = vec ? (r.layout == kRotHalf ? 8 : 4) : 1, w = vec ? 8 : 1;
-  const int units = r.dim / 2 / pw + (a.d - r.dim) / w;
-  RotaryGrid g;
-  g.units = std::min(units, kRowThreads);
-  g.rows = kRowThreads / g.units;
+  const int pw = vec ? (layout == kRotHalf ? 8 : 4) : 1, w = vec ? 8 : 1;
+  const int units = std::min(r.dim / 2 / pw + (a.d - r.dim) / w, kRowThreads);
+  const int rows = kRowThreads / units;
   // Four rows a thread where that leaves 512 workgroups or more, else one: 8,192 x 64 x 128 53 us
   // against 66, 1,000 x 64 x 128 8.4 against 9.7, but 300 x 64 x 128 5.0 against 4.6.
   const int64_t rows_all = (int64_t)a.n * a.heads;
-  const int per = rows_all / (4 * g.rows) >= 512 ? 4 * g.rows : g.rows;
-  g.hb = std::min(a.heads, per);
-  if ((a.heads + g.hb - 1) / g.hb > 65535) g.hb = (a.heads + 65534) / 65535;
-  g.tb = 1;
-  if (g.hb == a.heads) {
+  const int per = rows_all / (4 * rows) >= 512 ? 4 * rows : rows;
+  int hb = std::min(a.heads, per), tb = 1;
+  if ((a.heads + hb - 1) / hb > 65535) hb = (a.heads + 65534) / 65535;
+  if (hb == a.heads) {
     const int lds_tokens = std::max(1, 2048 / (r.dim / 2));  // at most 16 KiB of entries
-    g.tb = std::max(1, std::min(per / a.heads, lds_tokens));
+    tb = std::max(1, std::min(per / a.heads, lds_tokens));
   }
-  const dim3 grid(row_blocks(a.n, g.tb), (unsigned)((a.heads + g.hb - 1) / g.hb));
-  const size_t lds = (size_t)g.tb * (r.dim / 2) * sizeof(float2);
-  if (r.layout == kRotHalf) {
+  const RotaryGrid g{(uint16_t)tb, (uint16_t)hb, (uint16_t)units, (uint16_t)rows};
+  const dim3 grid(row_blocks(a.n, tb), (unsigned)((a.heads + hb - 1) / hb));
+  const size_t lds = (size_t)tb * (r.dim / 2) * sizeof(float2);
+  if (layout == kRotHalf) {
     if (vec) hipLaunchKernelGGL((rotary_kernel<IN, OUT, kRotHalf, true>), grid, dim3(kRowThreads), lds, s, a, g);
     else hipLaunchKernelGGL((rotary_kernel<IN, OUT, kRotHalf, false>), grid, dim3(kRowThreads), lds, s, a, g);
   } else {
@@ -383,22 +384,22 @@ bool aligned16(const void* p, int64_t ts, int64_t hs, int dtype) {
 // Whether the units of 16-byte access tile the head: pieces of eight elements
 // that lie wholly inside or outside the rotated part (and, in the half layout,
 // inside one half of it).
-bool rot_in_eights(const RotArgs& r, int d) {
-  return d % 8 == 0 && r.first % 8 == 0 && r.dim % (r.layout == kRotHalf ? 16 : 8) == 0;
+bool rot_in_eights(int dim, int first, int layout, int d) {
+  return d % 8 == 0 && first % 8 == 0 && dim % (layout == kRotHalf ? 16 : 8) == 0;
 }
 
 }  // namespace
 
-hipError_t launch_rotary(const RotaryArgs& a, int in_dtype, int out_dtype, hipStream_t s) {
+hipError_t launch_rotary(const RotaryArgs& a, int layout, int in_dtype, int out_dtype, hipStream_t s) {
   if (a.n <= 0) return hipSuccess;
-  const bool vec = rot_in_eights(a.rot, a.d) && aligned16(a.x, a.xts, a.xhs, in_dtype) &&
+  const bool vec = rot_in_eights(a.rot.dim, a.first, layout, a.d) && aligned16(a.x, a.xts, a.xhs, in_dtype) &&
                    aligned16(a.y, a.yts, a.yhs, out_dtype);
   if (in_dtype == kRowsBF16) {
-    return out_dtype == kRowsBF16 ? rotary_io<kRowsBF16, kRowsBF16>(a, vec, s)
-                                  : rotary_io<kRowsBF16, kRowsFP32>(a, vec, s);
+    return out_dtype == kRowsBF16 ? rotary_io<kRowsBF16, kRowsBF16>(a, layout, vec, s)
+                                  : rotary_io<kRowsBF16, kRowsFP32>(a, layout, vec, s);
   }
-  return out_dtype == kRowsBF16 ? rotary_io<kRowsFP32, kRowsBF16>(a, vec, s)
-                                : rotary_io<kRowsFP32, kRowsFP32>(a, vec, s);
+  return out_dtype == kRowsBF16 ? rotary_io<kRowsFP32, kRowsBF16>(a, layout, vec, s)
+                                : rotary_io<kRowsFP32, kRowsFP32>(a, layout, vec, s);
 }
 
 // --------------------------------------------------------- cache writing
@@ -450,9 +451,9 @@ struct Eight {
   int unit;       // its entries in LDS
 
   template <int LAYOUT>
-  __device__ __forceinline__ void place(const RotArgs& r, int e0) {
-    const int half = r.dim >> 1, e = e0 - r.first;
-    in = e >= 0 && e < r.dim;
+  __device__ __forceinline__ void place(int dim, int first, int e0) {
+    const int half = dim >> 1, e = e0 - first;
+    in = e >= 0 && e < dim;
     const bool lo = e < half;
     flip = lo ? ~0u : 0u;
     other = lo ? half : -half;
@@ -498,16 +499,16 @@ __device__ __forceinline__ float lanes_max(float m, int P) {
 // The same one element at a time, for any rotated part and alignment (cs: the token's entries in
 // plain order).
 template <int IN>
-__device__ __forceinline__ void rotate_each(const RotArgs& r, const void* x, int64_t at, int e0,
+__device__ __forceinline__ void rotate_each(int dim, int first, bool halves, const void* x, int64_t at, int e0,
                                             const float2* cs, float* v) {
-  const int half = r.dim >> 1;
+  const int half = dim >> 1;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int e = e0 - r.first + i;
-    if (e < 0 || e >= r.dim) continue;
-    const bool lo = r.layout == kRotHalf ? e < half : (e & 1) == 0;
-    const int off = r.layout == kRotHalf ? half : 1;
-    const float2 f = cs[r.layout == kRotHalf ? (lo ? e : e - half) : e >> 1];
+    const int e = e0 - first + i;
+    if (e < 0 || e >= dim) continue;
+    const bool lo = halves ? e < half : (e & 1) == 0;
+    const int off = halves ? half : 1;
+    const float2 f = cs[halves ? (lo ? e : e - half) : e >> 1];
     const float w = load1<IN>(x, at + e0 + i + (lo ? off : -off));
     v[i] = lo ? rot_lo(v[i], w, f) : rot_hi(v[i], w, f);
   }
@@ -516,12 +517,15 @@ __device__ __forceinline__ void rotate_each(const RotArgs& r, const void* x, int
 // How the rows of a write lie on threads: P = 1 << log_p threads take a row, a
 // workgroup takes `rounds` times 256 / P rows at once.
 struct WriteGrid {
-  int log_p;
-  int segs;       // steps of P pieces that a row takes
-  int rounds;
-  int near;       // no head straddles two waves: partners are a lane's to give
-  SmallDiv head;  // chunks of eight elements of a head
+  uint32_t pieces : 10;  // of eight elements of a head, less one
+  uint32_t heads : 8;    // less one
+  uint32_t log_p : 4;
+  uint32_t rounds : 3;
+  uint32_t near : 1;     // no head straddles two waves: partners are a lane's to give
+  uint32_t halves : 1;   // the layout, for rows without 16-byte access
+  uint32_t mul;          // SmallDiv of a head's pieces
 };
+static_assert(sizeof(CacheWriteArgs) + sizeof(WriteGrid) <= 112, "launches");
 
 constexpr int kMaxWriteThreads = 1024;
 constexpr int kWriteEntries = 2048;  // cosines and sines of a workgroup's rows
@@ -542,27 +546,29 @@ cache_write_kernel(CacheWriteArgs a, WriteGrid g) {
   __shared__ float red[2][kMaxWriteThreads / kWave];
   __shared__ int later[kRowThreads / 4];
   constexpr int KV = FMT == kFP8 ? K : 1;  // pieces whose values are held at once
-  const int log_p = g.log_p, P = 1 << log_p, RB = (int)blockDim.x >> log_p;
+  const SmallDiv head(g.pieces + 1u, g.mul);
+  const int log_p = g.log_p, P = 1 << log_p, threads = max(kRowThreads, P), RB = threads >> log_p;
   const int rl = threadIdx.x >> log_p;
-  const int chunks = a.heads * g.head.by, half = a.rot.dim >> 1;
+  const int chunks = (int)((g.heads + 1u) * head.by), half = a.rot.dim >> 1;
+  const int segs = (chunks + K * P - 1) / (K * P), rounds = g.rounds;  // steps of K P pieces that a row takes
   // A thread's (first) piece of the row: chunk lr, eight elements from e0 of a head, at `at` in
   // a row of x.  Piece k of K lies k P chunks and k `step` elements on.
   struct Piece {
     int lr, e0;
     int64_t at;
   };
-  const int64_t step = K > 1 ? (int64_t)g.head(P) * a.hs : 0;
+  const int64_t step = K > 1 ? (int64_t)head(P) * a.hs : 0;
   auto piece = [&](int seg) {
     Piece p;
     p.lr = (int)(threadIdx.x & (P - 1)) + (seg << log_p);
-    const unsigned h = g.head((unsigned)p.lr);
-    p.e0 = (p.lr - (int)(h * g.head.by)) * 8;
+    const unsigned h = head((unsigned)p.lr);
+    p.e0 = (p.lr - (int)(h * head.by)) * 8;
     p.at = (int64_t)h * a.hs + p.e0;
     return p;
   };
   int flip = 0;
-  for (int64_t i0 = (int64_t)blockIdx.x * RB * g.rounds; i0 < a.n; i0 += (int64_t)gridDim.x * RB * g.rounds) {
-    const int tile = (int)min((int64_t)RB * g.rounds, a.n - i0);
+  for (int64_t i0 = (int64_t)blockIdx.x * RB * rounds; i0 < a.n; i0 += kMostBlocks * RB * rounds) {
+    const int tile = (int)min((int64_t)RB * rounds, a.n - i0);
     Raw8<IN> raw[K];  // the next step's elements and slot, under way while this one is worked on
     int slot = -1;
     auto fetch = [&](const Piece& p, int r0) {
@@ -574,13 +580,13 @@ cache_write_kernel(CacheWriteArgs a, WriteGrid g) {
         if (have && p.lr + k * P < chunks) raw[k].template load<VEC>(a.x, at + k * step);
       }
       slot = -1;
-      if (have) slot = a.slots ? a.slots[i0 + r0 + rl] : (int)(a.start + i0) + r0 + rl;
+      if (have) slot = a.slots ? a.slots[i0 + r0 + rl] : a.start + (int)i0 + r0 + rl;
     };
     Piece ahead = piece(0);
     fetch(ahead, 0);
     if (a.rot.freq) {
       __syncthreads();  // the last rows' entries are read
-      rot_table<!VEC ? 1 : LAYOUT == kRotHalf ? 8 : 4>(a.rot, i0, tile, cs);
+      rot_table<!VEC ? 1 : LAYOUT == kRotHalf ? 8 : 4>(a.rot, i0, tile, threads, cs);
       __syncthreads();
     }
     for (int r0 = 0, seg = 0; r0 < tile;) {
@@ -593,12 +599,12 @@ cache_write_kernel(CacheWriteArgs a, WriteGrid g) {
       // The row's place; negative where nothing is written.
       int row = slot < a.L ? slot : -1;
       const int r1 = r0;
-      if (++seg == g.segs) {
+      if (++seg == segs) {
         seg = 0;
         r0 += RB;
       }
       if (r0 < tile) {
-        if (g.segs > 1) ahead = piece(seg);
+        if (segs > 1) ahead = piece(seg);
         fetch(ahead, r0);
       }
       if (a.claim && row >= 0 && a.claim[row] != i) row = -1;
@@ -617,7 +623,7 @@ cache_write_kernel(CacheWriteArgs a, WriteGrid g) {
 
       const float2* entries = cs + (have ? r1 + rl : 0) * half;
       Eight part;
-      part.template place<LAYOUT>(a.rot, my.e0);
+      part.template place<LAYOUT>(a.rot.dim, a.first, my.e0);
       float2 f[8];
       if (VEC && a.rot.freq && part.in) rot_read<LAYOUT == kRotHalf ? 8 : 4>(entries, half, part.unit, f);
       // The k-th piece's values, rotated.
@@ -636,7 +642,7 @@ cache_write_kernel(CacheWriteArgs a, WriteGrid g) {
           }
           if (part.in) rotate_eight<LAYOUT>(w, f, v);
         } else if (have && my.lr + k * P < chunks) {
-          rotate_each<IN>(a.rot, a.x, (int64_t)i * a.ts + my.at + k * step - my.e0, my.e0, entries, v);
+          rotate_each<IN>(a.rot.dim, a.first, g.halves, a.x, (int64_t)i * a.ts + my.at + k * step - my.e0, my.e0, entries, v);
         }
       };
 
@@ -723,8 +729,7 @@ cache_write_kernel(CacheWriteArgs a, WriteGrid g) {
 // claim[slot] = the last row that names the slot, for the slots named.
 __global__ void __launch_bounds__(kRowThreads)
 claim_kernel(const int* slots, int n, int L, int* claim, bool clear) {
-  for (int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x; i < n;
-       i += (int64_t)gridDim.x * kRowThreads) {
+  for (int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x; i < n; i += kMostBlocks * kRowThreads) {
     const int s = slots[i];
     if (s < 0 || s >= L) continue;
     if (clear) claim[s] = -1;
@@ -732,10 +737,14 @@ claim_kernel(const int* slots, int n, int L, int* claim, bool clear) {
   }
 }
 
+// A write's rows: heads of `pieces` pieces of eight elements, and the rotation's layout.
+struct WriteShape {
+  int heads, pieces, layout;
+  bool vec;
+};
+
 template <int IN, int FMT, int K>
-hipError_t cache_write_k(const CacheWriteArgs& a, bool vec, int log_p, hipStream_t s) {
-  const int chunks = a.heads * a.d / 8, per = K << log_p;
-  const int segs = (chunks + per - 1) / per;
+hipError_t cache_write_k(const CacheWriteArgs& a, const WriteShape& w, int log_p, hipStream_t s) {
   const int threads = std::max(kRowThreads, 1 << log_p), rb = threads >> log_p;
   // Rounds share the set-up and the entries of a workgroup's rows; as many (up to
   // four) as leave 2,048 workgroups and fit the table (8,192 x 64 x 128 to MXFP4 and back with
@@ -743,11 +752,18 @@ hipError_t cache_write_k(const CacheWriteArgs& a, bool vec, int log_p, hipStream
   int rounds = 1;
   const int fit = a.rot.freq ? kWriteEntries / (rb * (a.rot.dim / 2)) : 4;
   while (rounds < 4 && 2 * rounds <= fit && a.n / ((int64_t)rb * 2 * rounds) >= 2048) rounds *= 2;
-  const WriteGrid g{log_p, segs, rounds, kWave % (a.d / 8) == 0, SmallDiv((unsigned)a.d / 8)};
+  WriteGrid g{};
+  g.pieces = (uint32_t)w.pieces - 1;
+  g.heads = (uint32_t)w.heads - 1;
+  g.log_p = (uint32_t)log_p;
+  g.rounds = (uint32_t)rounds;
+  g.near = kWave % w.pieces == 0;
+  g.halves = w.layout == kRotHalf;
+  g.mul = SmallDiv((unsigned)w.pieces).mul;
   const dim3 grid(row_blocks(a.n, rb * rounds)), block((unsigned)threads);
-  if (!vec)  // the layout is a branch there
+  if (!w.vec)  // the layout is a branch there
     hipLaunchKernelGGL((cache_write_kernel<IN, FMT, K, false, kRotHalf>), grid, block, 0, s, a, g);
-  else if (a.rot.layout == kRotHalf)
+  else if (w.layout == kRotHalf)
     hipLaunchKernelGGL((cache_write_kernel<IN, FMT, K, true, kRotHalf>), grid, block, 0, s, a, g);
   else
     hipLaunchKernelGGL((cache_write_kernel<IN, FMT, K, true, kRotInterleaved>), grid, block, 0, s, a, g);
@@ -755,27 +771,29 @@ hipError_t cache_write_k(const CacheWriteArgs& a, bool vec, int log_p, hipStream
 }
 
 template <int IN, int FMT>
-hipError_t cache_write_fmt(const CacheWriteArgs& a, bool vec, hipStream_t s) {
-  const int chunks = a.heads * a.d / 8;
-  const bool four = chunks > kRowThreads && kRowThreads % (a.d / 8) == 0;
+hipError_t cache_write_fmt(const CacheWriteArgs& a, const WriteShape& w, hipStream_t s) {
+  const int chunks = w.heads * w.pieces;
+  const bool four = chunks > kRowThreads && kRowThreads % w.pieces == 0;
   int log_p = 2;
   while ((1 << log_p) < chunks && log_p < (FMT == kFP8 && !four ? 10 : 8)) ++log_p;
-  return four ? cache_write_k<IN, FMT, 4>(a, vec, log_p, s) : cache_write_k<IN, FMT, 1>(a, vec, log_p, s);
+  return four ? cache_write_k<IN, FMT, 4>(a, w, log_p, s) : cache_write_k<IN, FMT, 1>(a, w, log_p, s);
 }
 
 template <int IN>
-hipError_t cache_write_in(const CacheWriteArgs& a, int fmt, bool vec, hipStream_t s) {
-  if (fmt == kBF16) return cache_write_fmt<IN, kBF16>(a, vec, s);
-  if (fmt == kFP8) return cache_write_fmt<IN, kFP8>(a, vec, s);
-  if (fmt == kMXFP8) return cache_write_fmt<IN, kMXFP8>(a, vec, s);
-  if (fmt == kMXFP4) return cache_write_fmt<IN, kMXFP4>(a, vec, s);
+hipError_t cache_write_in(const CacheWriteArgs& a, const WriteShape& w, int fmt, hipStream_t s) {
+  if (fmt == kBF16) return cache_write_fmt<IN, kBF16>(a, w, s);
+  if (fmt == kFP8) return cache_write_fmt<IN, kFP8>(a, w, s);
+  if (fmt == kMXFP8) return cache_write_fmt<IN, kMXFP8>(a, w, s);
+  if (fmt == kMXFP4) return cache_write_fmt<IN, kMXFP4>(a, w, s);
   return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-hipError_t launch_cache_write(const CacheWriteArgs& a, int in_dtype, int fmt, hipStream_t s) {
+hipError_t launch_cache_write(const CacheWriteArgs& a, int heads, int d, int layout, int in_dtype, int fmt,
+                              hipStream_t s) {
   if (a.n <= 0) return hipSuccess;
+  if (d % 8 || d <= 0 || heads <= 0 || heads > 256 || d > 8192) return hipErrorInvalidValue;  // WriteGrid's fields
   if (a.slots && a.claim) {
     const dim3 grid(row_blocks(a.n, kRowThreads)), block(kRowThreads);
     for (int clear = 1; clear >= 0; --clear) {
@@ -784,9 +802,10 @@ hipError_t launch_cache_write(const CacheWriteArgs& a, int in_dtype, int fmt, hi
       if (e != hipSuccess) return e;
     }
   }
-  const bool vec = aligned16(a.x, a.ts, a.hs, in_dtype) && (!a.rot.freq || rot_in_eights(a.rot, a.d));
-  return in_dtype == kRowsBF16 ? cache_write_in<kRowsBF16>(a, fmt, vec, s)
-                               : cache_write_in<kRowsFP32>(a, fmt, vec, s);
+  const bool vec = aligned16(a.x, a.ts, a.hs, in_dtype) && (!a.rot.freq || rot_in_eights(a.rot.dim, a.first, layout, d));
+  const WriteShape w{heads, d / 8, layout, vec};
+  return in_dtype == kRowsBF16 ? cache_write_in<kRowsBF16>(a, w, fmt, s)
+                               : cache_write_in<kRowsFP32>(a, w, fmt, s);
 }
 
 // --------------------------------------------------------- cache reading
@@ -863,7 +882,7 @@ constexpr int kReadUnits = 4;
 // a wave stores one contiguous kilobyte of bf16.
 template <int OUT, int FMT, bool PAST>
 __global__ void __launch_bounds__(kRowThreads) cache_read_kernel(CacheReadArgs a, int rows, SmallDiv pieces) {
-  for (int64_t i0 = (int64_t)blockIdx.x * rows; i0 < a.n; i0 += (int64_t)gridDim.x * rows) {
+  for (int64_t i0 = (int64_t)blockIdx.x * rows; i0 < a.n; i0 += kMostBlocks * rows) {
     const unsigned end = (unsigned)min((int64_t)rows, a.n - i0) * pieces.by;
     Stored8<FMT> x[kReadUnits];
     int64_t to[kReadUnits];
@@ -876,7 +895,7 @@ __global__ void __launch_bounds__(kRowThreads) cache_read_kernel(CacheReadArgs a
       to[k] = u < end ? i * a.row + e : -1;
       live[k] = false;
       if (u < end) {
-        const int64_t row = a.slots ? (int64_t)a.slots[i] : a.start + i;
+        const int64_t row = a.slots ? (int64_t)a.slots[i] : (int64_t)a.start + i;
         live[k] = row >= 0 && row < a.L;
         if (live[k]) x[k].load(a, row, (int)e);
       }
