@@ -4,7 +4,7 @@ cache, the attention's mass at the selected entries and the indexer's loss.
 As in the package's own module only tensors are marshalled here; the kernels run on
 the tensors' GPU and its current stream.  A call's host time is most of a small
 operator's, so these functions build no stream, guard or pointer object that a
-call does not need.
+call does not need, and make results like an argument where they can (0.9 us against 1.4).
 """
 from __future__ import annotations
 
@@ -18,19 +18,24 @@ from . import (BF16, FP8_E4M3, MXFP4_E2M1, _FMT, Attention, Cache, RotaryPlan, R
 __all__ = ["Rotary", "rotary", "cache_write", "cache_read", "cache_write_workspace_bytes",
            "quantize", "attention_mass", "attention_mass_workspace_bytes", "index_loss"]
 
+_EWORKSPACE = -3  # HYTOPK_EWORKSPACE
 _bf16, _f32, _i32, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
-_current_device, _raw_stream = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+_empty_like, _contiguous = torch.empty_like, torch.contiguous_format
 
 
-def _launch(device, fn, *args) -> None:
-    """Calls fn(*args, stream) on the device's current stream, with that device
+def _call(device, fn, *args) -> int:
+    """The status of fn(*args, stream) on the device's current stream, with that device
     current."""
     index = device.index
     if index == _current_device():
-        rc = fn(*args, _raw_stream(index))
-    else:
-        with torch.cuda.device(device):
-            rc = fn(*args, _raw_stream(index))
+        return fn(*args, _raw_stream(index))
+    with torch.cuda.device(device):
+        return fn(*args, _raw_stream(index))
+
+
+def _launch(device, fn, *args) -> None:
+    rc = _call(device, fn, *args)
     if rc != 0:
         _check(rc)
 
@@ -118,11 +123,15 @@ def rotary(x, rot: Rotary, *, q_start: int = 0, q_pos=None, backward: bool = Fal
     shape, device = x.shape, x.device
     n, d = shape[0], shape[-1]
     heads = shape[1] if len(shape) == 3 else 1
-    if out is None:
-        out = x.new_empty(shape, dtype=out_dtype)
-    elif out.shape != shape or out.device != device or out_dtype not in (None, out.dtype):
-        raise ValueError(f"out must have x's shape {tuple(shape)} and device, and out_dtype")
-    ya = _rows_array(out, "out")
+    if out is None and (out_dtype is None or out_dtype == x.dtype):
+        out = _empty_like(x, memory_format=_contiguous)
+        ya = RowsArray(out.data_ptr(), heads * d, d, xa.dtype, 0)
+    else:
+        if out is None:
+            out = x.new_empty(shape, dtype=out_dtype)
+        elif out.shape != shape or out.device != device or out_dtype not in (None, out.dtype):
+            raise ValueError(f"out must have x's shape {tuple(shape)} and device, and out_dtype")
+        ya = _rows_array(out, "out")
     if q_pos is not None:
         _need(q_pos, "q_pos", (n,), _i32, device)
     _launch(device, load_library().hytopk_rotary, _plan(rot, device), n, heads, d, xa, ya,
@@ -134,7 +143,7 @@ def _cache(codes, scale, fmt) -> Cache:
     """codes [L][d] or [L][heads][d] (MXFP4: the last axis holds d/2 bytes) and
     scales as ``select`` takes them."""
     _gpu(codes, "codes")
-    code = _dtype_code(codes, fmt)
+    code = _dtype_code(codes) if fmt is None else _FMT[fmt]
     shape, dtype = codes.shape, codes.dtype
     axes = len(shape)
     if axes != 2 and axes != 3:
@@ -186,15 +195,16 @@ def cache_write(x, codes, scale=None, *, fmt=None, start: int = 0, slots=None, r
         _need(q_pos, "q_pos", (n,), _i32, device)
     if slots is not None:
         _need(slots, "slots", (n,), _i32, device)
-        if workspace is None:
-            need = lib.hytopk_cache_write_workspace(c, n, 1)
-            if need:
-                workspace = torch.empty(need, dtype=_u8, device=device)
     if workspace is not None:
         _workspace(workspace, device)
-    _launch(device, lib.hytopk_cache_write, c, n, xa, _address(slots), int(start),
-            _plan(rotary, device), _address(q_pos), int(q_start), _address(workspace),
-            0 if workspace is None else workspace.numel())
+    args = (c, n, xa, _address(slots), int(start), _plan(rotary, device), _address(q_pos), int(q_start))
+    rc = _call(device, lib.hytopk_cache_write, *args, _address(workspace),
+               0 if workspace is None else workspace.numel())
+    if rc == _EWORKSPACE and workspace is None:  # many rows by slot; few need none, so it is not asked before
+        workspace = torch.empty(lib.hytopk_cache_write_workspace(c, n, 1), dtype=_u8, device=device)
+        rc = _call(device, lib.hytopk_cache_write, *args, workspace.data_ptr(), workspace.numel())
+    if rc != 0:
+        _check(rc)
 
 
 def quantize(x, fmt: str, *, rotary=None, q_start: int = 0, q_pos=None):
@@ -284,7 +294,7 @@ def attention_mass(q, k, idx, *, softmax_scale=None, lse=None, workspace=None, o
     if lse is not None:
         _need(lse, "lse", (p.n, p.heads), _f32, device)
     if out is None:
-        out = q.new_empty((p.n, p.k), dtype=_f32)
+        out = _empty_like(idx, dtype=_f32)
     else:
         _need(out, "out", (p.n, p.k), _f32, device)
     if workspace is None and lse is None:
@@ -315,8 +325,11 @@ def index_loss(score, mass, *, weight=None, want=("loss", "d_score"), out=None):
     if weight is not None:
         _need(weight, "weight", (n,), _f32, device)
     if out is None:
-        loss = score.new_empty(n) if "loss" in want else None
-        grad = torch.empty_like(score) if "d_score" in want else None
+        loss = grad = None
+        if "loss" in want:
+            loss = score.new_empty(n) if weight is None else _empty_like(weight)
+        if "d_score" in want:
+            grad = _empty_like(score)
     else:
         loss, grad = out
         if loss is not None:
