@@ -854,13 +854,17 @@ hk::RotArgs rot_args(const hytopk_rotary_plan* p, const int32_t* q_pos, int64_t 
   return r;
 }
 
-// Whether memory lies in the cache's codes or scales.
-bool in_cache(const hytopk_cache* c, Extent m) {
+// The cache's codes and (none for bf16) scales.
+Extent cache_codes(const hytopk_cache* c) {
   const int64_t e = c->L * c->heads * c->d;
-  const int64_t codes = c->dtype == HYTOPK_BF16 ? 2 * e : (c->dtype == HYTOPK_MXFP4_E2M1 ? e / 2 : e);
-  const int64_t scale = c->dtype == HYTOPK_BF16 ? 0 : (c->dtype == HYTOPK_FP8_E4M3 ? 4 * c->L : e / 32);
-  return touches(m, c->codes, codes) || (scale && touches(m, c->scale, scale));
+  return extent(c->codes, c->dtype == HYTOPK_BF16 ? 2 * e : (c->dtype == HYTOPK_MXFP4_E2M1 ? e / 2 : e));
 }
+Extent cache_scale(const hytopk_cache* c) {
+  if (c->dtype == HYTOPK_BF16) return Extent{0, 0};
+  return extent(c->scale, c->dtype == HYTOPK_FP8_E4M3 ? 4 * c->L : c->L * c->heads * c->d / 32);
+}
+// Whether memory lies in the cache's codes or scales.
+bool in_cache(const hytopk_cache* c, Extent m) { return overlap(m, cache_codes(c)) || overlap(m, cache_scale(c)); }
 bool in_cache(const hytopk_cache* c, const void* p, int64_t bytes) { return p && in_cache(c, extent(p, bytes)); }
 
 // The geometry alone (what the workspace query knows).
@@ -1025,6 +1029,7 @@ int hytopk_cache_write(const hytopk_cache* c, int64_t n, const hytopk_rows* x,
     if (in_cache(c, slots, 4 * n) || (claim && in_cache(c, workspace, 4 * c->L)) ||
         (plan && (in_cache(c, q_pos, 4 * n) || in_cache(c, plan->freq, 4 * (int64_t)plan->dim))))
       return fail(HYTOPK_EINVAL, "the slots, the positions, the plan or the workspace overlap the cache");
+    if (overlap(cache_codes(c), cache_scale(c))) return fail(HYTOPK_EINVAL, "the cache's codes and scales overlap");
     hk::CacheWriteArgs a{};
     a.x = x->data;
     a.ts = x->token_stride;
