@@ -1029,6 +1029,12 @@ int hytopk_cache_write(const hytopk_cache* c, int64_t n, const hytopk_rows* x,
     if (in_cache(c, slots, 4 * n) || (claim && in_cache(c, workspace, 4 * c->L)) ||
         (plan && (in_cache(c, q_pos, 4 * n) || in_cache(c, plan->freq, 4 * (int64_t)plan->dim))))
       return fail(HYTOPK_EINVAL, "the slots, the positions, the plan or the workspace overlap the cache");
+    if (claim) {  // cleared and written while the others are read
+      const Extent w = extent(workspace, 4 * c->L);
+      if (touches(w, slots, 4 * n) || overlap(w, extent(x, n, c->heads, c->d)) ||
+          (plan && (touches(w, q_pos, 4 * n) || touches(w, plan->freq, 4 * (int64_t)plan->dim))))
+        return fail(HYTOPK_EINVAL, "the workspace overlaps the rows, the slots, the positions or the plan");
+    }
     if (overlap(cache_codes(c), cache_scale(c))) return fail(HYTOPK_EINVAL, "the cache's codes and scales overlap");
     hk::CacheWriteArgs a{};
     a.x = x->data;

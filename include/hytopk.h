@@ -378,7 +378,7 @@ size_t hytopk_cache_write_workspace(const hytopk_cache* c, int64_t n, int32_t by
  *         code = x * 2^-e rounded, saturating at 448 or 6.
  * x is finite: an infinity or NaN leaves its own row (FP8) or block (MX)
  * unspecified.  Nothing that the call reads, nor its workspace, may overlap the cache,
- * nor its codes its scales. */
+ * nor the workspace what the call reads, nor the codes their scales. */
 int hytopk_cache_write(const hytopk_cache* c, int64_t n, const hytopk_rows* x,
                        const int32_t* slots, int64_t start, const hytopk_rotary_plan* plan,
                        const int32_t* q_pos, int64_t q_start, void* workspace,

@@ -47,3 +47,20 @@ def test_a_write_s_last_check_is_that_codes_and_scales_lie_apart(lib):
     # scales apart: the next fault before it shows
     for scale in (CODES + (128 << 20), CODES - (4 << 20)):
         refused(lib, write(lib, scale=scale, slots=CODES), EINVAL, "overlap the cache")
+
+
+# the claim workspace of more than 1,024 rows by slot: 4 L bytes
+@pytest.mark.parametrize("kw", [
+    dict(slots=WS + (4 << 20) - 4), dict(slots=WS - 4 * 2000 + 4), dict(x=WS + 1024), dict(x=WS - 2 * 128 * 2000 + 2),
+    dict(pos=WS + 64), dict(freq=WS + (4 << 20) - 8), dict(freq=WS - 8 * 32 + 8),
+])
+def test_a_write_s_workspace_lies_apart_from_what_it_reads(lib, kw):
+    refused(lib, write(lib, **kw), EINVAL, "the workspace overlaps")
+
+
+def test_a_workspace_that_is_not_used_may_lie_anywhere(lib):
+    for kw in (dict(n=1024, slots=WS), dict(slots=None, x=WS), dict(n=4, pos=WS)):
+        refused(lib, write(lib, **kw), EINVAL, "codes and scales overlap")
+    # one that only touches what is read is fine
+    for kw in (dict(slots=WS + (4 << 20)), dict(slots=WS - 8000), dict(x=WS + (4 << 20)), dict(freq=WS - 256)):
+        refused(lib, write(lib, **kw), EINVAL, "codes and scales overlap")
