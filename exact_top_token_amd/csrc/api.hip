@@ -816,6 +816,46 @@ Extent extent(const void* p, int64_t bytes) {
 }
 
 bool overlap(Extent a, Extent b) { return a.lo < b.hi && b.lo < a.hi; }
+// The bytes that rows are stored in along one axis: `count` pieces `stride` apart.
+struct Axis {
+  int64_t count, stride;
+};
+
+// Whether pieces of `lx` and `ly` bytes that repeat along the same axes, outermost first, meet, where y's
+// begin `off` bytes behind x's.  Each axis steps over all of what lies inside it, so off modulo its stride leaves
+// two neighbours of an x piece.
+bool pieces_meet(const Axis* axis, int axes, int64_t lx, int64_t ly, int64_t off) {
+  int64_t steps = 0;
+  for (int i = 0; i < axes; ++i) steps += (axis[i].count - 1) * axis[i].stride;
+  if (off >= steps + lx || off + steps + ly <= 0) return false;
+  if (axes == 0) return true;
+  const int64_t s = axis->stride, r = ((off % s) + s) % s;
+  return pieces_meet(axis + 1, axes - 1, lx, ly, r) || pieces_meet(axis + 1, axes - 1, lx, ly, r - s);
+}
+
+// Whether rows x and y share memory.  Rows of one geometry (slices of one buffer) may lie between each other's;
+// others are taken as whole extents.
+bool rows_meet(const hytopk_rows* x, const hytopk_rows* y, int64_t n, int32_t heads, int32_t d) {
+  const Extent ex = extent(x, n, heads, d), ey = extent(y, n, heads, d);
+  if (!overlap(ex, ey)) return false;
+  const int64_t bx = rows_elem(x), by = rows_elem(y);
+  Axis axis[2];
+  int axes = 0;
+  if (n > 1) axis[axes++] = Axis{n, y->token_stride * by};
+  if (heads > 1) axis[axes++] = Axis{heads, y->head_stride * by};
+  if ((n > 1 && x->token_stride * bx != y->token_stride * by) ||
+      (heads > 1 && x->head_stride * bx != y->head_stride * by))
+    return true;
+  if (axes == 2 && axis[0].stride < axis[1].stride) std::swap(axis[0], axis[1]);
+  // an axis steps over what lies inside it
+  int64_t span = std::max(bx, by) * d;
+  for (int i = axes - 1; i >= 0; --i) {
+    if (axis[i].stride < span) return true;
+    span += (axis[i].count - 1) * axis[i].stride;
+  }
+  return pieces_meet(axis, axes, bx * d, by * d, (int64_t)(ey.lo - ex.lo));
+}
+
 // Whether `bytes` bytes at p (NULL: none) lie in m.
 bool touches(Extent m, const void* p, int64_t bytes) { return p && overlap(m, extent(p, bytes)); }
 
@@ -980,8 +1020,7 @@ int hytopk_rotary(const hytopk_rotary_plan* plan, int64_t n, int32_t heads, int3
     const bool same = x->data == y->data && x->dtype == y->dtype &&
                       (n == 1 || x->token_stride == y->token_stride) &&
                       (heads == 1 || x->head_stride == y->head_stride);
-    if (!same && overlap(extent(x, n, heads, d), extent(y, n, heads, d)))
-      return fail(HYTOPK_EINVAL, "x and y overlap (y may be x itself)");
+    if (!same && rows_meet(x, y, n, heads, d)) return fail(HYTOPK_EINVAL, "x and y overlap (y may be x itself)");
     const Extent out = extent(y, n, heads, d);
     if (touches(out, q_pos, 4 * n) || touches(out, plan->freq, 4 * (int64_t)plan->dim))
       return fail(HYTOPK_EINVAL, "y overlaps the positions or the plan");

@@ -340,8 +340,9 @@ int hytopk_rotary_frequencies(int32_t dim, double base, int32_t scaling, double 
  * (gain included): the gradient with respect to x from the gradient with
  * respect to y.  Angles are reduced in 64 bits (exact to 32-bit rounding at any
  * int32 position), products are fp32, rounded once to y's type.  x and y may
- * be the same rows (same data, strides and type); otherwise their memory must
- * not overlap.  heads, d >= 1 and heads * d < 2^31; dim <= 1024. */
+ * be the same rows (same data, strides and type); otherwise they must share no
+ * memory, and lie one behind the other unless their strides in bytes are the same
+ * (disjoint slices of one buffer may lie between each other).  heads, d >= 1 and heads * d < 2^31; dim <= 1024. */
 int hytopk_rotary(const hytopk_rotary_plan* plan, int64_t n, int32_t heads, int32_t d,
                   const hytopk_rows* x, const hytopk_rows* y, const int32_t* q_pos,
                   int64_t q_start, int32_t backward, void* stream);

@@ -64,3 +64,56 @@ def test_a_workspace_that_is_not_used_may_lie_anywhere(lib):
     # one that only touches what is read is fine
     for kw in (dict(slots=WS + (4 << 20)), dict(slots=WS - 8000), dict(x=WS + (4 << 20)), dict(freq=WS - 256)):
         refused(lib, write(lib, **kw), EINVAL, "codes and scales overlap")
+
+
+def rotary(lib, n=4, heads=3, d=64, x=(X, None, None, BF16), y=(OUT, None, None, BF16), dim=32, first=0, layout=0, gain=1.0,
+           freq=None, pos=None, start=0):
+    """x, y: (address, token stride, head stride, type); the plan lies over y's first row (the last check)."""
+    rows = [None if r is None else hk.RowsArray(r[0], heads * d if r[1] is None else r[1], d if r[2] is None else r[2], r[3], 0)
+            for r in (x, y)]
+    p = hk.RotaryPlan((y[0] & ~7) if freq is None else freq, gain, dim, first, layout, 0)
+    return lib.hytopk_rotary(ctypes.byref(p), n, heads, d, *(r if r is None else ctypes.byref(r) for r in rows), pos, start, 0, None)
+
+
+def test_rotary_s_last_check_is_that_y_lies_apart_from_plan_and_positions(lib):
+    for kw in (dict(), dict(x=(OUT, None, None, BF16)), dict(x=(X, None, 0, FP32)), dict(x=(X, 0, 0, BF16)), dict(n=1)):
+        refused(lib, rotary(lib, **kw), EINVAL, "the positions or the plan")
+
+
+SLICES = [  # n, heads, d, x, y of one buffer (offset in elements, token stride, head stride), whether they share memory
+    (9, 3, 64, (0, 600, 200), (64, 600, 200), False), (9, 3, 64, (0, 600, 200), (136, 600, 200), False),
+    (9, 3, 64, (0, 600, 200), (63, 600, 200), True), (9, 3, 64, (0, 600, 200), (137, 600, 200), True),
+    (9, 3, 64, (136, 600, 200), (0, 600, 200), False), (9, 3, 64, (137, 600, 200), (0, 600, 200), True),
+    # neighbouring heads of a projection, one slot apart, in the next token's slice
+    (9, 3, 64, (0, 576, 64), (192, 576, 64), False), (9, 3, 64, (0, 576, 64), (384, 576, 64), False),
+    (9, 3, 64, (0, 576, 64), (191, 576, 64), True), (9, 3, 64, (0, 576, 64), (385, 576, 64), True),
+    (9, 3, 64, (0, 576, 64), (192 + 576, 576, 64), False), (9, 3, 64, (0, 576, 64), (128, 576, 64), True),
+    # heads before tokens
+    (9, 3, 64, (0, 128, 2000), (64, 128, 2000), False), (9, 3, 64, (0, 128, 2000), (65, 128, 2000), True),
+    (9, 3, 64, (0, 64, 2000), (9 * 64, 64, 2000), False), (9, 3, 64, (0, 64, 2000), (8 * 64, 64, 2000), True),
+    # one axis alone
+    (9, 1, 64, (0, 128, 5), (64, 128, 7), False), (1, 3, 64, (0, 5, 128), (64, 7, 128), False),
+    # other strides: taken as whole extents
+    (9, 3, 64, (0, 600, 200), (64, 600, 190), True), (9, 3, 64, (0, 600, 0), (64, 600, 100), True),
+    (9, 3, 64, (0, 600, 200), (8 * 600 + 2 * 200 + 64, 600, 190), False),
+]
+
+
+@pytest.mark.parametrize("elem", [BF16, FP32])
+@pytest.mark.parametrize("case", SLICES)
+def test_rotary_between_slices_of_one_buffer(lib, case, elem):
+    n, heads, d, x, y, shared = case
+    size = 4 if elem == FP32 else 2
+    rows = [(X + size * r[0], r[1], r[2], elem) for r in (x, y)]
+    cells = [{r[0] + i * r[1] + h * r[2] + e for i in range(n) for h in range(heads) for e in range(d)} for r in (x, y)]
+    assert shared or not cells[0] & cells[1]
+    if x[1:] == y[1:]:
+        assert bool(cells[0] & cells[1]) == shared
+    refused(lib, rotary(lib, n, heads, d, *rows), EINVAL, "x and y overlap" if shared else "the positions or the plan")
+
+
+def test_rotary_between_slices_of_two_types(lib):
+    """fp32 rows of 256 bytes and bf16 rows of 128 in cells of 384."""
+    for off, shared in ((0, True), (254, True), (256, False), (258, True), (256 + 384, False), (256 - 384, False)):
+        x, y = (X, 96 * 3, 96, FP32), (X + off, 2 * 96 * 3, 2 * 96, BF16)
+        refused(lib, rotary(lib, x=x, y=y), EINVAL, "x and y overlap" if shared else "the positions or the plan")
