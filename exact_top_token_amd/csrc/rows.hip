@@ -160,7 +160,7 @@ __device__ __forceinline__ void store1(void* base, int64_t at, float v) {
 
 // ------------------------------------------------------------- rotation
 
-// Cosine and sine of t turns, |t| <= 1/2: the nearest quarter turn k is taken
+// Cosine and sine of t turns, |t| up to 1/2 (or what rounds to it): the nearest quarter turn k is taken
 // off exactly, the rest |x| <= pi/4 goes through the Taylor series to x^9 and x^8
 // (truncated below 2e-9 and 3e-8), and k swaps and signs the two.
 __device__ __forceinline__ float2 turn_cos_sin(float t) {
@@ -181,13 +181,24 @@ __device__ __forceinline__ float2 turn_cos_sin(float t) {
                      __uint_as_float(__float_as_uint(ss) ^ (((unsigned)q & 2u) << 30)));
 }
 
-// (gain cos, turn sin) at position pos, f turns a position.  The angle is formed and
-// reduced to [-1/2, 1/2] in 64 bits: at 2^31 positions its error is below
-// 1e-7 turns, at 2^20 below 1e-10, where 32 bits would keep none of it.
-__device__ __forceinline__ float2 rot_entry(const RotArgs& r, double f, int64_t pos) {
-  double t = (double)pos * f;
-  t -= rint(t);
-  const float2 c = turn_cos_sin((float)t);
+// Turns a position as a sum of two doubles.  One double's rounding, times 2^31 positions, would be 2^-24 of a turn.
+struct Turns {
+  double hi, lo;
+  __device__ __forceinline__ explicit Turns(double freq) {  // radians a position
+    constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;  // 1 / (2 pi)
+    hi = freq * kHi;
+    lo = fma(freq, kLo, fma(freq, kHi, -hi));
+  }
+};
+
+// (gain cos, turn sin) at position pos.  The angle is formed and reduced to [-1/2, 1/2] turns in
+// two doubles, so that at any int32 position only its rounding to fp32 is left (2^-26 of a turn;
+// 32 bits throughout would keep nothing at 2^20).
+__device__ __forceinline__ float2 rot_entry(const RotArgs& r, const Turns& f, int64_t pos) {
+#pragma clang fp contract(off)  // t is the rounded product in both its uses
+  const double p = (double)pos, t = p * f.hi;
+  const double rest = fma(p, f.lo, fma(p, f.hi, -t));
+  const float2 c = turn_cos_sin((float)((t - rint(t)) + rest));
   return make_float2(c.x * r.gain, c.y * r.turn);
 }
 
@@ -239,7 +250,7 @@ __device__ __forceinline__ void rot_table(const RotArgs& r, int64_t t0, int nt, 
   const int first = threadIdx.x / cols;
   if (first >= steps) return;
   for (int i = threadIdx.x - first * cols; i < half; i += cols) {
-    const double f = r.freq[i] * 0.15915494309189533577;  // turns a position
+    const Turns f(r.freq[i]);
     float2* to = cs + rot_slot<W>(i, half);
     for (int t = first; t < nt; t += steps) {
       const int64_t pos = r.pos ? (int64_t)r.pos[t0 + t] : (int64_t)r.pos0 + t0 + t;

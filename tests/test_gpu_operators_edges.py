@@ -38,3 +38,25 @@ def test_rotary_between_slices_of_one_buffer(hk, dtype):
         assert torch.equal(fused[y_at], want)
         before[y_at] = want
         assert torch.equal(fused, before)
+
+
+def test_rotary_angles_at_the_ends_of_int32(hk):
+    """Cosines and sines themselves (rows of ones and zeros, fp32) at positions up to 2^31, where one rounding of
+    a product in 64 bits is 3 * 2^-24 of a radian.  In units of 2^-24: the turn's rounding to fp32, 2 pi 2^-26:
+    1.58; 2 pi as fp32 and its product, 1.47 of an angle up to pi/4: 1.16; the cosine's polynomial 0.42 left off,
+    its terms 0.6, its last rounding 0.5 (the sine's less): 1.52.  4.26 together."""
+    far = 2 ** 31 - 1 - np.arange(600) * 977
+    pos = np.concatenate([far, -far - 1, 2 ** 30 + np.arange(300), 2 ** 20 + np.arange(100), np.arange(100)])
+    for plan in (hk.Rotary(64), hk.Rotary(128, base=1000000.0, layout="interleaved"),
+                 hk.Rotary(64, scaling="linear", factor=3.0), hk.Rotary(64, scaling="ntk", factor=7.0)):
+        half = plan.dim // 2
+        x = np.zeros((len(pos), 2, plan.dim), np.float32)  # (1, 0) gives (cos, sin), (0, 1) gives (-sin, cos)
+        a, b = (np.s_[:half], np.s_[half:]) if plan.layout == "half" else (np.s_[0::2], np.s_[1::2])
+        x[:, 0, a] = 1
+        x[:, 1, b] = 1
+        y = hk.rotary(torch.from_numpy(x).cuda(), plan, q_pos=torch.from_numpy(pos.astype(np.int32)).cuda())
+        ref = op.rotary(x.astype(np.float64), pos, plan.freq.cpu().numpy(), layout=plan.layout)
+        err = np.abs(y.double().cpu().numpy() - ref)
+        say(f"rotary angles: largest error {err.max() / U:.2f} * 2^-24")
+        assert err.max() <= 4.26 * U, (np.argwhere(err > 4.26 * U)[0], err.max() / U)
+        assert np.array_equal(y[:, 1, b].cpu().numpy(), y[:, 0, a].cpu().numpy())
