@@ -9,6 +9,7 @@ call does not need, and make results like an argument where they can (0.9 us aga
 from __future__ import annotations
 
 import ctypes
+import math
 
 import torch
 
@@ -83,10 +84,13 @@ class Rotary:
     part (``gain``), made once and kept for every call.  ``layout`` pairs
     elements (i, i + dim/2) ("half") or (2i, 2i + 1) ("interleaved");
     ``scaling`` ("none", "linear", "ntk", "yarn") stretches the positions by
-    ``factor`` for a model whose positions reached ``original`` before."""
+    ``factor`` for a model whose positions reached ``original`` before.  ``gain`` replaces the
+    scaling's own factor (YaRN: 0.1 ln(factor) + 1; else 1), and ``freq``
+    [dim/2] (radians a position) the frequencies, for a model with its own."""
 
     def __init__(self, dim: int, *, first: int = 0, layout: str = "half", base: float = 10000.0,
-                 scaling: str = "none", factor: float = 1.0, original: int = 0, device="cuda"):
+                 scaling: str = "none", factor: float = 1.0, original: int = 0, gain=None, freq=None,
+                 device="cuda"):
         if layout not in _LAYOUTS:
             raise ValueError(f"unknown rotary layout {layout!r}")
         if scaling not in _SCALINGS:
@@ -94,13 +98,21 @@ class Rotary:
         dim, first, original = int(dim), int(first), int(original)
         if not (0 < dim < 1 << 31 and 0 <= first < 1 << 31):
             raise ValueError("dim must be > 0 and first >= 0, both below 2^31")
-        freq = torch.empty(max(min(dim, 1024) // 2, 1), dtype=torch.float64)
-        gain = ctypes.c_double()
+        made = torch.empty(max(min(dim, 1024) // 2, 1), dtype=torch.float64)
+        factor_on = ctypes.c_double()
         _check(load_library().hytopk_rotary_frequencies(dim, float(base), _SCALINGS[scaling],
-                                                        float(factor), original, freq.data_ptr(),
-                                                        ctypes.byref(gain)))
-        self.freq = freq.to(device)
-        self.gain, self.dim, self.first, self.layout = gain.value, dim, first, layout
+                                                        float(factor), original, made.data_ptr(),
+                                                        ctypes.byref(factor_on)))
+        if freq is not None:
+            own = torch.as_tensor(freq).detach().cpu()
+            if scaling != "none" or own.shape != made.shape or not torch.isfinite(own).all():
+                raise ValueError(f"freq must hold {dim // 2} finite values, and takes no scaling")
+            made.copy_(own)
+        gain = factor_on.value if gain is None else float(gain)
+        if not math.isfinite(gain):
+            raise ValueError("gain must be finite")
+        self.freq = made.to(device)
+        self.gain, self.dim, self.first, self.layout = gain, dim, first, layout
         self._plan = RotaryPlan(self.freq.data_ptr(), self.gain, dim, first, _LAYOUTS[layout], 0)
 
 

@@ -60,3 +60,19 @@ def test_rotary_angles_at_the_ends_of_int32(hk):
         say(f"rotary angles: largest error {err.max() / U:.2f} * 2^-24")
         assert err.max() <= 4.26 * U, (np.argwhere(err > 4.26 * U)[0], err.max() / U)
         assert np.array_equal(y[:, 1, b].cpu().numpy(), y[:, 0, a].cpu().numpy())
+
+
+def test_rotary_with_a_gain_and_frequencies_of_its_own(hk):
+    f = np.geomspace(3.0, 1e-6, 16)
+    x, pos = _rand((40, 3, 64), 4, torch.float32), np.arange(5000, 5040)
+    for kw in (dict(gain=1.0, scaling="yarn", factor=40.0, original=4096), dict(freq=f), dict(freq=torch.from_numpy(f).cuda(), gain=-0.75)):
+        plan = hk.Rotary(32, first=8, **kw)
+        y = hk.rotary(x, plan, q_start=5000).double().cpu().numpy()
+        x64 = x.double().cpu().numpy()
+        freq = f if "freq" in kw else plan.freq.cpu().numpy()
+        gain = kw.get("gain", 1.0)
+        ref = op.rotary(x64, pos, freq, first=8, gain=gain)
+        # 2^-21 gain (|a| + |b|), as derived in test_gpu_rotary.py
+        both = 2.0 ** -21 * abs(gain) * (np.abs(x64[..., 8:24]) + np.abs(x64[..., 24:40]))
+        assert np.all(np.abs(y - ref)[..., 8:40] <= np.concatenate([both, both], -1))
+        assert np.array_equal(y[..., :8], x64[..., :8]) and np.array_equal(y[..., 40:], x64[..., 40:])

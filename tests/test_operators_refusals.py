@@ -117,3 +117,31 @@ def test_rotary_between_slices_of_two_types(lib):
     for off, shared in ((0, True), (254, True), (256, False), (258, True), (256 + 384, False), (256 - 384, False)):
         x, y = (X, 96 * 3, 96, FP32), (X + off, 2 * 96 * 3, 2 * 96, BF16)
         refused(lib, rotary(lib, x=x, y=y), EINVAL, "x and y overlap" if shared else "the positions or the plan")
+
+
+def test_a_plan_with_a_gain_or_frequencies_of_its_own():
+    """YaRN of a model that takes the factor elsewhere, and frequencies that no scaling here gives."""
+    import numpy as np
+    import torch
+    kw = dict(scaling="yarn", factor=40.0, original=4096, device="cpu")
+    one, usual = hk.Rotary(64, gain=1.0, **kw), hk.Rotary(64, **kw)
+    assert one.gain == 1.0 and one._plan.gain == 1.0 and torch.equal(one.freq, usual.freq)
+    assert abs(usual.gain - (0.1 * np.log(40.0) + 1)) < 1e-15
+    assert hk.Rotary(64, gain=0, device="cpu").gain == 0.0
+    f = np.geomspace(2.0, 1e-7, 32)
+    for own in (f, list(f), torch.from_numpy(f)):
+        p = hk.Rotary(64, first=64, layout="interleaved", freq=own, gain=0.5, device="cpu")
+        assert p.freq.dtype == torch.float64 and np.array_equal(p.freq.numpy(), f)
+        assert (p.gain, p.dim, p.first, p.layout) == (0.5, 64, 64, "interleaved")
+        assert p._plan.freq == p.freq.data_ptr()
+    mine = torch.from_numpy(f.copy())
+    kept = hk.Rotary(64, freq=mine, device="cpu")
+    mine.zero_()
+    assert kept.gain == 1.0 and np.array_equal(kept.freq.numpy(), f)  # a copy: the plan does not change with it
+    assert np.array_equal(hk.Rotary(64, freq=f.astype(np.float32), device="cpu").freq.numpy(), f.astype(np.float32).astype(np.float64))
+    for bad in (dict(freq=f[:31]), dict(freq=f[None]), dict(freq=f * np.inf), dict(freq=np.append(f[:31], np.nan)),
+                dict(freq=f, scaling="linear", factor=2.0), dict(gain=float("nan")), dict(gain=float("inf"))):
+        with pytest.raises(ValueError):
+            hk.Rotary(64, device="cpu", **bad)
+    with pytest.raises(hk.HytopkError):
+        hk.Rotary(63, freq=f, device="cpu")
