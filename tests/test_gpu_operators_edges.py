@@ -76,3 +76,27 @@ def test_rotary_with_a_gain_and_frequencies_of_its_own(hk):
         both = 2.0 ** -21 * abs(gain) * (np.abs(x64[..., 8:24]) + np.abs(x64[..., 24:40]))
         assert np.all(np.abs(y - ref)[..., 8:40] <= np.concatenate([both, both], -1))
         assert np.array_equal(y[..., :8], x64[..., :8]) and np.array_equal(y[..., 40:], x64[..., 40:])
+
+
+@pytest.mark.parametrize("k", [40, 61, 700, 1999, 2048])
+def test_index_loss_of_live_entries_at_the_lowest_score(hk, k):
+    """A score of the type's lowest value is live: with mass there the loss is t * 3.4e38 an entry, and finite.
+    t: a sum of k terms in k/64 + 6 steps, a reciprocal and a product; a term two more roundings; the terms' sum the
+    same steps again, and the weight's product."""
+    low = torch.finfo(torch.float32).min
+    score, mass = torch.zeros(3, k), torch.ones(3, k)
+    score[:, -5:] = low
+    score[1, :3] = torch.tensor([4.0, -20.0, 30.0])
+    score[2] = -1e30
+    score[2, 7:] = low
+    mass[2, 7:-1] = 0.0
+    weight = torch.tensor([0.125, 1.0, 0.25])
+    loss, grad = hk.index_loss(score.cuda(), mass.cuda(), weight=weight.cuda())
+    rl, rg = op.index_loss(score.numpy(), mass.numpy(), weight.numpy())
+    assert np.isfinite(rl).all() and (rl > 1e34).all()
+    steps = 2 * (k / 64 + 6) + 6
+    assert np.all(np.abs(loss.double().cpu().numpy() - rl) <= steps * U * rl)
+    # p: the exponential of an exact 0, -24, 26 or nothing below 2^-23 of itself, its row's sum, reciprocal, product
+    p = rg / weight[:, None].numpy() + mass.numpy() / mass.sum(1, keepdim=True).numpy()
+    tol = ((k / 64 + 6 + 100) * p + (k / 64 + 10) / 7) * U
+    assert np.all(np.abs(grad.double().cpu().numpy() - rg) <= tol)
