@@ -100,3 +100,27 @@ def test_index_loss_of_live_entries_at_the_lowest_score(hk, k):
     p = rg / weight[:, None].numpy() + mass.numpy() / mass.sum(1, keepdim=True).numpy()
     tol = ((k / 64 + 6 + 100) * p + (k / 64 + 10) / 7) * U
     assert np.all(np.abs(grad.double().cpu().numpy() - rg) <= tol)
+
+
+@pytest.mark.parametrize("k", [5, 64, 700, 2047, 2048])
+def test_index_loss_of_masses_whose_sum_passes_fp32(hk, k):
+    """Finite masses, an infinite sum: the same bits as from the masses times 2^-40 (a power of two moves no
+    rounding).  An infinity itself shows, in its row alone."""
+    g = torch.Generator().manual_seed(k)
+    score = torch.randn((5, k), generator=g)
+    mass = torch.rand((5, k), generator=g) * 1e38 + 2e38
+    mass[1, 2:] = 3.0
+    score[2, k // 2:] = -float("inf")
+    mass[2, k // 2:] = float("inf")  # no part of the row
+    assert torch.isinf(mass.sum(1)[[0, 1, 3]]).all()
+    loss, grad = hk.index_loss(score.cuda(), mass.cuda())
+    small = torch.where(torch.isinf(mass), mass, mass * 2.0 ** -40)
+    l2, g2 = hk.index_loss(score.cuda(), small.cuda())
+    assert torch.isfinite(loss).all() and torch.equal(loss, l2) and torch.equal(grad, g2)
+    rl, rg = op.index_loss(score.numpy(), mass.numpy())
+    # t and p within their row's sum (k/64 + 6 steps) and 100 roundings
+    assert np.all(np.abs(grad.double().cpu().numpy() - rg) <= (k / 64 + 106) * U)
+    mass[3, 1] = float("inf")
+    l3, g3 = hk.index_loss(score.cuda(), mass.cuda())
+    keep = [0, 1, 2, 4]
+    assert torch.isnan(l3[3]) and torch.equal(l3[keep], loss[keep]) and torch.equal(g3[keep], grad[keep])
