@@ -145,3 +145,158 @@ def test_a_plan_with_a_gain_or_frequencies_of_its_own():
             hk.Rotary(64, device="cpu", **bad)
     with pytest.raises(hk.HytopkError):
         hk.Rotary(63, freq=f, device="cpu")
+
+
+ROTARY = [  # arguments, status, a part of the message
+    (dict(dim=63), EINVAL, "must be even"), (dict(dim=0), EINVAL, "must be even"), (dict(dim=66), EINVAL, "outside the head"),
+    (dict(first=-2), EINVAL, "outside the head"), (dict(first=34), EINVAL, "outside the head"),
+    (dict(layout=2), EINVAL, "unknown rotary layout"), (dict(layout=-1), EINVAL, "unknown rotary layout"),
+    (dict(freq=FREQ + 4), EINVAL, "8-byte aligned"), (dict(gain=float("nan")), EINVAL, "gain must be finite"),
+    (dict(gain=float("-inf")), EINVAL, "gain must be finite"), (dict(gain=1e39), EINVAL, "gain must be finite"),
+    (dict(dim=1026, d=2048), EUNSUPPORTED, "rotary dim > 1024"),
+    (dict(n=-1), EINVAL, "n must be >= 0"), (dict(heads=0), EINVAL, "heads, d > 0"), (dict(d=0, dim=2), EINVAL, "heads, d > 0"),
+    (dict(n=1 << 31), EUNSUPPORTED, "n >= 2^31"), (dict(heads=1 << 20, d=1 << 11), EUNSUPPORTED, "heads * d >= 2^31"),
+    (dict(x=None), EINVAL, "rows are NULL"), (dict(x=(0, None, None, BF16)), EINVAL, "rows data is NULL"),
+    (dict(x=(X, None, None, 2)), EINVAL, "unknown rows dtype"), (dict(x=(X, None, None, -1)), EINVAL, "unknown rows dtype"),
+    (dict(x=(X + 1, None, None, BF16)), EINVAL, "aligned to their element"),
+    (dict(x=(X + 2, None, None, FP32)), EINVAL, "aligned to their element"),
+    (dict(x=(X, -1, None, BF16)), EINVAL, "strides must be >= 0"), (dict(x=(X, None, -1, BF16)), EINVAL, "strides must be >= 0"),
+    (dict(x=(X, 1 << 62, None, BF16)), EINVAL, "more memory than exists"),
+    (dict(y=(OUT, 1 << 62, None, BF16)), EINVAL, "more memory than exists"),
+    (dict(y=(OUT, None, None, 7)), EINVAL, "unknown rows dtype"), (dict(y=(OUT + 1, None, None, BF16)), EINVAL, "aligned to their element"),
+    (dict(y=(OUT, None, 0, BF16)), EINVAL, "rows of y overlap"), (dict(y=(OUT, None, 63, BF16)), EINVAL, "rows of y overlap"),
+    (dict(y=(OUT, 191, None, BF16)), EINVAL, "rows of y overlap"), (dict(y=(OUT, 64, 255, BF16)), EINVAL, "rows of y overlap"),
+    (dict(y=(X + 64, None, None, BF16)), EINVAL, "x and y overlap"), (dict(y=(X, None, None, FP32)), EINVAL, "x and y overlap"),
+    (dict(y=(X, 600, None, BF16)), EINVAL, "x and y overlap"),
+    (dict(start=-1), EINVAL, "positions q_start"), (dict(start=(1 << 31) - 3), EINVAL, "positions q_start"),
+    (dict(pos=POS + 2), EINVAL, "q_pos must be 4-byte"), (dict(pos=OUT + 4 * 3 * 64 * 2 - 4, freq=FREQ), EINVAL, "the positions or the plan"),
+    (dict(start=(1 << 31) - 4), EINVAL, "the positions or the plan"), (dict(pos=POS, start=-1), EINVAL, "the positions or the plan"),
+    (dict(y=(OUT, 64, 256, BF16)), EINVAL, "the positions or the plan"), (dict(d=1030, dim=1024), EINVAL, "the positions or the plan"),
+]
+
+
+@pytest.mark.parametrize("kw,status,words", ROTARY)
+def test_rotary_refuses_for_its_reason(lib, kw, status, words):
+    refused(lib, rotary(lib, **kw), status, words)
+
+
+def test_rotary_refuses_a_plan_without_frequencies(lib):
+    p, r = hk.RotaryPlan(None, 1.0, 32, 0, 0, 0), hk.RowsArray(X, 192, 64, BF16, 0)
+    call = lambda plan: lib.hytopk_rotary(plan, 4, 3, 64, ctypes.byref(r), ctypes.byref(r), None, 0, 0, None)  # noqa: E731
+    refused(lib, call(ctypes.byref(p)), EINVAL, "rotary freq is NULL")
+    refused(lib, call(None), EINVAL, "rotary plan is NULL")
+
+
+WRITE = [
+    (dict(codes=None), EINVAL, "cache codes are NULL"), (dict(codes=CODES + 8), EINVAL, "codes must be 16-byte"),
+    (dict(scale=None), EINVAL, "need scales"), (dict(scale=SCALE + 2), EINVAL, "scales must be 4-byte"),
+    (dict(L=0), EINVAL, "L, heads and d"), (dict(heads=0), EINVAL, "L, heads and d"), (dict(d=0), EINVAL, "L, heads and d"),
+    (dict(dtype=4), EINVAL, "unknown dtype"), (dict(dtype=-1), EINVAL, "unknown dtype"), (dict(L=1 << 31), EUNSUPPORTED, "L >= 2^31"),
+    (dict(d=100), EUNSUPPORTED, "multiples of 32"), (dict(d=16), EUNSUPPORTED, "multiples of 32"),
+    (dict(heads=65), EUNSUPPORTED, "heads * d > 8192"), (dict(n=-1), EINVAL, "n must be >= 0"), (dict(n=1 << 31), EUNSUPPORTED, "n >= 2^31"),
+    (dict(slots=SLOTS + 1), EINVAL, "slots must be 4-byte"), (dict(slots=None, start=-1), EINVAL, "outside the cache"),
+    (dict(slots=None, start=(1 << 20) - 1999), EINVAL, "outside the cache"), (dict(slots=None, n=(1 << 20) + 1), EINVAL, "outside the cache"),
+    (dict(x=None), EINVAL, "rows data is NULL"), (dict(x=X + 1), EINVAL, "aligned to their element"), (dict(xtype=2), EINVAL, "unknown rows dtype"),
+    (dict(ts=-1), EINVAL, "strides must be >= 0"), (dict(dim=130), EINVAL, "outside the head"), (dict(dim=0), EINVAL, "must be even"),
+    (dict(pos=POS + 2), EINVAL, "q_pos must be 4-byte"), (dict(freq=FREQ + 4), EINVAL, "8-byte aligned"),
+    (dict(x=CODES + (128 << 20) - 2), EINVAL, "x overlaps the cache"), (dict(x=CODES - 2000 * 256 + 2), EINVAL, "x overlaps the cache"),
+    (dict(x=SCALE, scale=SCALE + 4096), EINVAL, "x overlaps the cache"), (dict(ws=None), EWORKSPACE, "workspace is NULL"),
+    (dict(ws=WS + 128), EWORKSPACE, "256-byte aligned"), (dict(ws_bytes=(4 << 20) - 1), EWORKSPACE, "too small"),
+    (dict(slots=CODES + 4), EINVAL, "overlap the cache"), (dict(pos=CODES + 4), EINVAL, "overlap the cache"),
+    (dict(freq=CODES + 8), EINVAL, "overlap the cache"), (dict(ws=CODES + 256), EINVAL, "overlap the cache"),
+    (dict(slots=None, start=(1 << 20) - 2000), EINVAL, "codes and scales overlap"), (dict(ws_bytes=4 << 20), EINVAL, "codes and scales overlap"),
+    (dict(ts=0, hs=0), EINVAL, "codes and scales overlap"), (dict(freq=None, pos=POS + 2), EINVAL, "codes and scales overlap"),
+]
+
+
+@pytest.mark.parametrize("kw,status,words", WRITE)
+def test_cache_write_refuses_for_its_reason(lib, kw, status, words):
+    refused(lib, write(lib, **kw), status, words)
+
+
+def read(lib, n=100, L=1 << 20, dtype=hk.FP8_E4M3, heads=1, d=128, codes=CODES, scale=SCALE, slots=OUT + 1024, start=0,
+         out=OUT, out_type=BF16):
+    """The slots lie in the result (the last check)."""
+    c = hk.Cache(codes, scale, L, heads, d, dtype, 0)
+    return lib.hytopk_cache_read(ctypes.byref(c), n, slots, start, out, out_type, None)
+
+
+READ = [
+    (dict(), EINVAL, "out overlaps the slots"), (dict(slots=OUT + 100 * 256 - 4), EINVAL, "out overlaps the slots"),
+    (dict(slots=OUT + 100 * 512 - 4, out_type=FP32), EINVAL, "out overlaps the slots"), (dict(slots=OUT - 396), EINVAL, "out overlaps the slots"),
+    (dict(dtype=hk.BF16, scale=None), EINVAL, "out overlaps the slots"),
+    (dict(codes=None), EINVAL, "cache codes are NULL"), (dict(codes=CODES + 8), EINVAL, "codes must be 16-byte"), (dict(scale=None), EINVAL, "need scales"),
+    (dict(scale=SCALE + 1), EINVAL, "scales must be 4-byte"), (dict(L=0), EINVAL, "L, heads and d"), (dict(dtype=9), EINVAL, "unknown dtype"),
+    (dict(d=48), EUNSUPPORTED, "multiples of 32"), (dict(heads=65), EUNSUPPORTED, "heads * d > 8192"), (dict(n=-1), EINVAL, "n must be >= 0"),
+    (dict(n=1 << 31), EUNSUPPORTED, "n >= 2^31"), (dict(slots=OUT + 1026), EINVAL, "slots must be 4-byte"),
+    (dict(slots=None, start=-1), EINVAL, "outside the cache"), (dict(slots=None, start=(1 << 20) - 99), EINVAL, "outside the cache"),
+    (dict(out=None), EINVAL, "out is NULL"), (dict(out=OUT + 8), EINVAL, "out must be 16-byte"), (dict(out_type=2), EINVAL, "unknown rows dtype"),
+    (dict(out=CODES + (128 << 20) - 16), EINVAL, "out overlaps the cache"), (dict(out=SCALE - 100 * 256 + 16), EINVAL, "out overlaps the cache"),
+    (dict(slots=None, start=(1 << 20) - 100, out=CODES), EINVAL, "out overlaps the cache"),
+]
+
+
+@pytest.mark.parametrize("kw,status,words", READ)
+def test_cache_read_refuses_for_its_reason(lib, kw, status, words):
+    refused(lib, read(lib, **kw), status, words)
+
+
+Q, K, IDX, LSE, MASS, MWS = (at(i + 20) for i in range(6))
+OVER = "must not overlap the inputs"
+
+
+def mass(lib, L=1000, n=4, heads=64, key_heads=1, d=128, k=100, scale=0.1, q=Q, keys=K, idx=IDX, lse=LSE, out=IDX + 16, ws=MWS,
+         ws_bytes=1 << 30):
+    """The mass lies over the indices (the last check)."""
+    a = hk.Attention(L, n, heads, key_heads, d, k, scale, 0)
+    return lib.hytopk_attention_mass(ctypes.byref(a), q, keys, idx, lse, out, ws, ws_bytes, None)
+
+
+MASS_CASES = [
+    (dict(), EINVAL, OVER), (dict(lse=None), EINVAL, OVER), (dict(ws=None, ws_bytes=0), EINVAL, OVER), (dict(heads=1024, key_heads=2), EINVAL, OVER),
+    (dict(L=0), EINVAL, "L must be > 0"), (dict(n=-1), EINVAL, "n >= 0"), (dict(heads=0), EINVAL, "key_heads must divide"),
+    (dict(key_heads=0), EINVAL, "key_heads must divide"), (dict(key_heads=3), EINVAL, "key_heads must divide"), (dict(key_heads=-1), EINVAL, "key_heads must divide"),
+    (dict(k=0), EINVAL, "k must be > 0"), (dict(k=2049), EUNSUPPORTED, "k > 2048"), (dict(d=100), EUNSUPPORTED, "d must be 64"), (dict(d=0), EUNSUPPORTED, "d must be 64"),
+    (dict(scale=float("nan")), EINVAL, "softmax_scale must be finite"), (dict(scale=3e38), EINVAL, "softmax_scale must be finite"),
+    (dict(L=1 << 31), EUNSUPPORTED, "L >= 2^31"), (dict(n=1 << 24), EUNSUPPORTED, "n >= 2^24"), (dict(n=1 << 23, d=512), EUNSUPPORTED, "n >= 2^24, or 2^23"),
+    (dict(heads=1025), EUNSUPPORTED, "heads > 1024"),
+    (dict(q=None), EINVAL, "must be non-NULL"), (dict(keys=None), EINVAL, "must be non-NULL"), (dict(idx=None), EINVAL, "must be non-NULL"),
+    (dict(out=None), EINVAL, "must be non-NULL"), (dict(q=Q + 8), EINVAL, "q and k must be 16-byte"), (dict(keys=K + 2), EINVAL, "q and k must be 16-byte"),
+    (dict(idx=IDX + 2), EINVAL, "4-byte aligned"), (dict(lse=LSE + 2), EINVAL, "4-byte aligned"), (dict(out=IDX + 18), EINVAL, "4-byte aligned"),
+    (dict(lse=None, ws=None), EWORKSPACE, "workspace is NULL"), (dict(lse=None, ws=MWS + 4), EWORKSPACE, "256-byte aligned"),
+    (dict(lse=None, n=1, ws_bytes=1), EWORKSPACE, "too small"),
+    (dict(out=Q + 2 * 4 * 64 * 128 - 4), EINVAL, OVER), (dict(out=K - 1596), EINVAL, OVER), (dict(out=LSE + 4), EINVAL, OVER),
+    (dict(out=MASS, lse=None, ws=MASS - 256, n=1, k=2000), EINVAL, OVER), (dict(out=MASS, lse=None, ws=Q, n=1, k=2000), EINVAL, OVER),
+    (dict(out=MASS, lse=None, ws=K, n=1, k=2000), EINVAL, OVER), (dict(out=MASS, lse=None, ws=IDX, n=1, k=2000), EINVAL, OVER),
+]
+
+
+@pytest.mark.parametrize("kw,status,words", MASS_CASES)
+def test_attention_mass_refuses_for_its_reason(lib, kw, status, words):
+    refused(lib, mass(lib, **kw), status, words)
+
+
+SCORE, TARGET, WEIGHT, LOSS, GRAD = (at(i + 30) for i in range(5))
+
+
+def index_loss(lib, n=4, k=100, score=SCORE, target=TARGET, weight=WEIGHT, loss=TARGET + 1584, grad=GRAD):
+    """The loss lies over the target (the last check)."""
+    return lib.hytopk_index_loss(n, k, score, target, weight, loss, grad, None)
+
+
+LOSS_CASES = [
+    (dict(), EINVAL, "loss overlaps"), (dict(grad=None), EINVAL, "loss overlaps"), (dict(weight=None), EINVAL, "loss overlaps"),
+    (dict(grad=SCORE), EINVAL, "loss overlaps"), (dict(grad=TARGET), EINVAL, "loss overlaps"), (dict(loss=SCORE - 12), EINVAL, "loss overlaps"),
+    (dict(loss=WEIGHT + 12), EINVAL, "loss overlaps"), (dict(loss=GRAD + 1596), EINVAL, "loss overlaps"),
+    (dict(n=-1), EINVAL, "n must be >= 0"), (dict(k=0), EINVAL, "k > 0"), (dict(k=2049), EUNSUPPORTED, "k > 2048"), (dict(n=1 << 31), EUNSUPPORTED, "n >= 2^31"),
+    (dict(score=None), EINVAL, "score and mass must be non-NULL"), (dict(target=None), EINVAL, "score and mass must be non-NULL"),
+    (dict(loss=None, grad=None), EINVAL, "both NULL"), (dict(score=SCORE + 2), EINVAL, "4-byte aligned"), (dict(target=TARGET + 2), EINVAL, "4-byte aligned"),
+    (dict(weight=WEIGHT + 1), EINVAL, "4-byte aligned"), (dict(loss=LOSS + 3), EINVAL, "4-byte aligned"), (dict(grad=GRAD + 2), EINVAL, "4-byte aligned"),
+    (dict(grad=SCORE + 16), EINVAL, "d_score overlaps an input"), (dict(grad=TARGET - 16), EINVAL, "d_score overlaps an input"),
+    (dict(grad=WEIGHT - 1596), EINVAL, "d_score overlaps an input"),
+]
+
+
+@pytest.mark.parametrize("kw,status,words", LOSS_CASES)
+def test_index_loss_refuses_for_its_reason(lib, kw, status, words):
+    refused(lib, index_loss(lib, **kw), status, words)
