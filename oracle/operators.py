@@ -8,12 +8,36 @@ from __future__ import annotations
 
 import numpy as np
 
-__all__ = ["rotary_frequencies", "rotary", "attention_probabilities", "attention_mass", "index_loss"]
+__all__ = ["rotary_frequencies", "rotary_plan", "rotary", "attention_probabilities", "attention_mass", "index_loss"]
 
 
 def rotary_frequencies(dim: int, base: float = 10000.0) -> np.ndarray:
     """base^(-2i/dim) for i = 0 .. dim/2 - 1."""
     return float(base) ** (-2.0 * np.arange(dim // 2) / dim)
+
+
+def rotary_plan(dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, original: int = 0):
+    """(frequencies, factor on the rotated part).  NTK: the base at which the slowest pair comes out divided by
+    the factor.  YaRN: per pair a share of f / factor that rises along the pairs' numbers, from the last whole
+    number at which a pair still makes 32 turns in the original context to the first at which it makes one or less
+    (within 0 .. dim - 1); where every pair makes one or less, all are divided."""
+    if scaling == "none":
+        return rotary_frequencies(dim, base), 1.0
+    if scaling == "linear":
+        return rotary_frequencies(dim, base) / factor, 1.0
+    if scaling == "ntk":
+        return rotary_frequencies(dim, base * factor ** (dim / max(dim - 2, 1))), 1.0
+    f = rotary_frequencies(dim, base)
+    # original base^(-2 x / dim) = 2 pi turns, solved for x
+    many, one = (0.5 * dim * np.log(original / (2 * np.pi * turns)) / np.log(base) for turns in (32, 1))
+    a, b = max(np.floor(many), 0.0), min(np.ceil(one), dim - 1.0)
+    share = np.empty(dim // 2)
+    for i in range(dim // 2):
+        if one <= 0 or i >= max(b, a + 1e-3):
+            share[i] = 1.0
+        else:
+            share[i] = 0.0 if i <= a else (i - a) / (b - a)
+    return f * ((1 - share) + share / factor), 1 + np.log(factor) / 10
 
 
 def rotary(x: np.ndarray, pos: np.ndarray, freq: np.ndarray, *, first: int = 0,

@@ -124,3 +124,21 @@ def test_index_loss_of_masses_whose_sum_passes_fp32(hk, k):
     l3, g3 = hk.index_loss(score.cuda(), mass.cuda())
     keep = [0, 1, 2, 4]
     assert torch.isnan(l3[3]) and torch.equal(l3[keep], loss[keep]) and torch.equal(g3[keep], grad[keep])
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("scaling", ["none", "linear", "ntk", "yarn"])
+def test_rotary_of_every_scaling_by_the_oracle_s_own_plan(hk, scaling, layout):
+    dim, base, factor, original, first = 64, 500000.0, 8.0, 8192, 32
+    plan = hk.Rotary(dim, first=first, layout=layout, base=base, scaling=scaling, factor=factor, original=original)
+    freq, gain = op.rotary_plan(dim, base, scaling, factor, original)
+    x = _rand((200, 3, 128), 11, torch.float32)
+    pos = np.random.default_rng(4).integers(0, 1 << 17, 200)
+    y = hk.rotary(x, plan, q_pos=torch.from_numpy(pos.astype(np.int32)).cuda()).double().cpu().numpy()
+    x64 = x.double().cpu().numpy()
+    ref = op.rotary(x64, pos, freq, first=first, layout=layout, gain=gain)
+    # 2^-21 gain (|a| + |b|), as derived in test_gpu_rotary.py, which leaves room for the plans' 1e-13 of 2^17 radians
+    part = np.abs(x64[..., first:first + dim])
+    both = part + (np.roll(part, dim // 2, -1) if layout == "half" else part.reshape(200, 3, -1, 2)[..., ::-1].reshape(part.shape))
+    assert np.all(np.abs(y - ref)[..., first:first + dim] <= 2.0 ** -21 * gain * both)
+    assert np.array_equal(y[..., :first], x64[..., :first]) and np.array_equal(y[..., first + dim:], x64[..., first + dim:])
