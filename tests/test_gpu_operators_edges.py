@@ -142,3 +142,46 @@ def test_rotary_of_every_scaling_by_the_oracle_s_own_plan(hk, scaling, layout):
     both = part + (np.roll(part, dim // 2, -1) if layout == "half" else part.reshape(200, 3, -1, 2)[..., ::-1].reshape(part.shape))
     assert np.all(np.abs(y - ref)[..., first:first + dim] <= 2.0 ** -21 * gain * both)
     assert np.array_equal(y[..., :first], x64[..., :first]) and np.array_equal(y[..., first + dim:], x64[..., first + dim:])
+
+
+def test_the_training_step_s_gradient_is_its_loss_s_slope(hk):
+    """rotary -> select -> replay -> attention mass -> loss -> backward -> transposed rotation: the loss in
+    64 bits (the selection and the mass fixed) rises along the gradients of the rows before the rotation
+    and of the weights as steeply as those gradients are long."""
+    L, n, H, d, k, A = 500, 24, 16, 128, 80, 8
+    plan = hk.Rotary(64, first=32, layout="interleaved", scaling="yarn", factor=4.0, original=256)
+    rand = lambda shape, seed, f=1.0: (f * torch.randn(shape, generator=torch.Generator().manual_seed(seed))).to(torch.bfloat16).cuda()  # noqa: E731
+    xq, xk = rand((n, H, d), 1, 0.3), rand((L, d), 2, 0.3)
+    w = torch.rand((n, H), generator=torch.Generator().manual_seed(3)).cuda()
+    q, key = hk.rotary(xq, plan, q_start=L - n), hk.rotary(xk, plan)
+    idx, score = hk.select(q, key, w, k)
+    mass = hk.attention_mass(rand((n, A, 64), 4, 2.0), rand((L, 2, 64), 5), idx)
+    _, d_score = hk.index_loss(hk.replay(q, key, w, idx), mass)
+    g = hk.backward(q, key, w, idx, d_score)
+    dxq = hk.rotary(g["dq"], plan, q_start=L - n, backward=True)
+    dxk = hk.rotary(g["dk"], plan, backward=True)
+    host = lambda t: t.double().cpu().numpy()  # noqa: E731
+    q0, k0, w0, m0, at = host(q), host(key), host(w), host(mass), idx.cpu().numpy()
+    live = at >= 0
+
+    def loss(q, key, w):
+        dots = np.maximum(np.matmul(key[at], q.transpose(0, 2, 1)), 0.0)  # [n][k][H]
+        s = np.where(live, (dots * w[:, None]).sum(-1), -np.inf)
+        return op.index_loss(s, m0)[0].sum()
+
+    freq = plan.freq.cpu().numpy()
+    turn = lambda v, pos: op.rotary(v, pos, freq, first=32, layout="interleaved", gain=plan.gain)  # noqa: E731
+    zero = (0 * q0, 0 * k0, 0 * w0)
+    for name, grad, move, raw in (("dq", host(dxq), lambda v: (turn(v, np.arange(L - n, L)), zero[1], zero[2]), host(g["dq"])),
+                                  ("dk", host(dxk), lambda v: (zero[0], turn(v[:, None], np.arange(L))[:, 0], zero[2]), host(g["dk"])),
+                                  ("dw", host(g["dw"]), lambda v: (zero[0], zero[1], v), host(g["dw"]))):
+        length = np.sqrt((grad ** 2).sum())
+        u = move(grad / length)
+        h = 1e-5
+        up, down = (loss(q0 + t * u[0], k0 + t * u[1], w0 + t * u[2]) for t in (h, -h))
+        slope = (up - down) / (2 * h)
+        say(f"slope along {name}: {slope:.6f}, length {length:.6f}")
+        # the backward's results lie within 1e-3 of their largest (test_gpu_operators_chain.py), here summed over the unit direction;
+        # the difference itself 1e-9 of the loss over 2 h, and ReLU's corners h of the slope
+        tol = 1e-3 * np.abs(raw).max() * plan.gain * np.abs(grad).sum() / length + 1e-9 * abs(up) / h + 10 * h * length
+        assert slope > 0 and abs(slope - length) <= tol
