@@ -455,8 +455,7 @@ __global__ void __launch_bounds__(kMassThreads, PT > 4 ? 2 : 3) mass_staged_kern
   float* rs = ms + gw * PT * 16;                                      // [gw][PT * 16]
   float2* red = reinterpret_cast<float2*>(rs + gw * PT * 16);         // [waves][PT * 16]
   uint64_t* live64 = reinterpret_cast<uint64_t*>(red + W * PT * 16);  // [split_len / 64] live entries
-  // [split_len] where an entry's key row begins, in 16-byte pieces (padding: row 0, which no live
-  // entry uses)
+  // [split_len] where an entry's key row begins, in 16-byte pieces (padding fetches row 0, and live64 leaves it out)
   uint32_t* rows_at = reinterpret_cast<uint32_t*>(live64 + a.split_len / 64);
   // [gw][split_len] fp32 bits; with one pass each sum takes the place of its row, which is through by then
   uint32_t* sums = rows_at + (T > PT ? a.split_len : 0);

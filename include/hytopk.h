@@ -386,7 +386,8 @@ int hytopk_cache_write(const hytopk_cache* c, int64_t n, const hytopk_rows* x,
                        size_t workspace_bytes, void* stream);
 
 /* Reads cache rows back: out [n][heads][d] (contiguous, 16-byte aligned, type out_dtype) =
- * code * scale of row slots[i], or start + i with slots NULL, rounded once.
+ * code * scale of row slots[i], or start + i with slots NULL, in fp32 and from there rounded to out_dtype
+ * (MX scales are powers of two, so only FP8 rows are rounded in both).
  * Slots outside [0, L) (the padding of a selection among them) give rows of zeros.  An E4M3 NaN
  * code or a scale byte of 255 reads as NaN. */
 int hytopk_cache_read(const hytopk_cache* c, int64_t n, const int32_t* slots, int64_t start,
@@ -415,8 +416,8 @@ size_t hytopk_attention_mass_workspace(const hytopk_attention* p);
  * lse [n][heads] fp32 is the attention's log-sum-exp (its own normaliser, over
  * whatever keys it attended to); with lse NULL it is taken over the row's
  * entries, so that each row sums to 1, and the workspace is required.
- * An index outside [0, L) is padding: mass 0, no part in the sum; its key row is
- * never read.  An index that stands twice counts twice.  Products are bf16 MFMA with fp32
+ * An index outside [0, L) is padding: mass 0, no part in the sum (whatever key 0
+ * holds, which may be fetched in its place).  An index that stands twice counts twice.  Products are bf16 MFMA with fp32
  * accumulation; maxima, sums and exponentials are fp32.
  * n < 2^24 (2^23 for d of 512 or 576) and heads <= 1024, or HYTOPK_EUNSUPPORTED.  mass and the
  * workspace must not overlap the inputs or each other. */
