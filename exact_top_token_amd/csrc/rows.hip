@@ -191,14 +191,13 @@ struct Turns {
   }
 };
 
-// (gain cos, turn sin) at position pos.  The angle is formed and reduced to [-1/2, 1/2] turns in
-// two doubles, so that at any int32 position only its rounding to fp32 is left (2^-26 of a turn;
-// 32 bits throughout would keep nothing at 2^20).
-__device__ __forceinline__ float2 rot_entry(const RotArgs& r, const Turns& f, int64_t pos) {
-#pragma clang fp contract(off)  // t is the rounded product in both its uses
-  const double p = (double)pos, t = p * f.hi;
-  const double rest = fma(p, f.lo, fma(p, f.hi, -t));
-  const float2 c = turn_cos_sin((float)((t - rint(t)) + rest));
+// (gain cos, turn sin) at position pos.  The angle is formed and reduced to [-1/2, 1/2] turns in 64 bits with
+// one rounding of what the whole turns leave, so that at any int32 position only the rounding to fp32 is
+// left (2^-26 of a turn; 32 bits throughout would keep nothing at 2^20).
+__device__ __forceinline__ float2 rot_entry(const RotArgs& r, const Turns& f, int pos) {
+  const double p = (double)pos;
+  const double t = fma(p, f.lo, fma(p, f.hi, -rint(p * f.hi)));
+  const float2 c = turn_cos_sin((float)t);
   return make_float2(c.x * r.gain, c.y * r.turn);
 }
 
@@ -253,7 +252,7 @@ __device__ __forceinline__ void rot_table(const RotArgs& r, int64_t t0, int nt, 
     const Turns f(r.freq[i]);
     float2* to = cs + rot_slot<W>(i, half);
     for (int t = first; t < nt; t += steps) {
-      const int64_t pos = r.pos ? (int64_t)r.pos[t0 + t] : (int64_t)r.pos0 + t0 + t;
+      const int pos = r.pos ? r.pos[t0 + t] : r.pos0 + (int)t0 + t;  // below 2^31
       to[t * half] = rot_entry(r, f, pos);
     }
   }
