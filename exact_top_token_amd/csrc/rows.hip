@@ -160,44 +160,45 @@ __device__ __forceinline__ void store1(void* base, int64_t at, float v) {
 
 // ------------------------------------------------------------- rotation
 
-// Cosine and sine of t turns, |t| up to 1/2 (or what rounds to it): the nearest quarter turn k is taken
-// off exactly, the rest |x| <= pi/4 goes through the Taylor series to x^9 and x^8
-// (truncated below 2e-9 and 3e-8), and k swaps and signs the two.
-__device__ __forceinline__ float2 turn_cos_sin(float t) {
-  const float k = rintf(4.0f * t);
-  const float x = fmaf(k, -0.25f, t) * 6.28318530717958648f;
-  const float z = x * x;
-  float s = fmaf(z, 1.0f / 362880.0f, -1.0f / 5040.0f);
-  s = fmaf(z, s, 1.0f / 120.0f);
-  s = fmaf(z, s, -1.0f / 6.0f);
-  s = fmaf(z * s, x, x);
-  float c = fmaf(z, 1.0f / 40320.0f, -1.0f / 720.0f);
-  c = fmaf(z, c, 1.0f / 24.0f);
-  c = fmaf(z, c, -0.5f);
+// Quarter turns a position, less whole turns (positions are whole numbers), as a sum of two doubles: one double's
+// rounding, times 2^31 positions, would be 2^-24 of a turn.
+struct Turns {
+  double hi, lo;
+  __device__ __forceinline__ explicit Turns(double freq) {  // radians a position
+#pragma clang fp contract(off)  // t is the rounded product wherever it stands
+    constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;  // 1 / (2 pi)
+    const double t = freq * kHi;
+    lo = 4.0 * fma(freq, kLo, fma(freq, kHi, -t));
+    hi = 4.0 * (t - rint(t));
+  }
+};
+
+// Cosine and sine of q + r quarter turns, |r| <= 1/2 (or what rounds to it).  sin(pi/2 r) = r (pi/2 + P(r^2)) and
+// cos(pi/2 r) = 1 + r^2 Q(r^2), P and Q interpolated at the Chebyshev nodes of [0, 1/4] (off by 2.4e-9 and 2e-10;
+// pi/2 is rounded to fp32 and P holds the rest); q swaps and signs the two.
+__device__ __forceinline__ float2 turn_cos_sin(int q, float r) {
+  const float z = r * r;
+  float s = fmaf(z, -0.004602149128913879f, 0.07968021929264069f);
+  s = fmaf(z, s, -0.6459634900093079f);
+  s = fmaf(z, s, -4.8553051357203e-08f);
+  s = fmaf(r, 1.5707963705062866f, r * s);
+  float c = fmaf(z, 0.0009067399078048766f, -0.02086152881383896f);
+  c = fmaf(z, c, 0.253669410943985f);
+  c = fmaf(z, c, -1.2337005138397217f);
   c = fmaf(z, c, 1.0f);
-  const int q = (int)k;  // -2 .. 2
   const float cc = q & 1 ? s : c, ss = q & 1 ? c : s;
   return make_float2(__uint_as_float(__float_as_uint(cc) ^ (((unsigned)(q + 1) & 2u) << 30)),
                      __uint_as_float(__float_as_uint(ss) ^ (((unsigned)q & 2u) << 30)));
 }
 
-// Turns a position as a sum of two doubles.  One double's rounding, times 2^31 positions, would be 2^-24 of a turn.
-struct Turns {
-  double hi, lo;
-  __device__ __forceinline__ explicit Turns(double freq) {  // radians a position
-    constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;  // 1 / (2 pi)
-    hi = freq * kHi;
-    lo = fma(freq, kLo, fma(freq, kHi, -hi));
-  }
-};
-
-// (gain cos, turn sin) at position pos.  The angle is formed and reduced to [-1/2, 1/2] turns in 64 bits with
-// one rounding of what the whole turns leave, so that at any int32 position only the rounding to fp32 is
-// left (2^-26 of a turn; 32 bits throughout would keep nothing at 2^20).
+// (gain cos, turn sin) at position pos.  The angle is formed in 64 bits and reduced to the nearest quarter turn
+// there, so that at any int32 position its rounding to fp32 is 2^-28 of a turn.  1.5 * 2^52 more leaves
+// a number of quarter turns below 2^33 rounded to a whole one, its last 32 bits the sum's.
 __device__ __forceinline__ float2 rot_entry(const RotArgs& r, const Turns& f, int pos) {
-  const double p = (double)pos;
-  const double t = fma(p, f.lo, fma(p, f.hi, -rint(p * f.hi)));
-  const float2 c = turn_cos_sin((float)t);
+  constexpr double kWhole = 6755399441055744.0;
+  const double p = (double)pos, n = fma(p, f.hi, kWhole);
+  const double rest = fma(p, f.lo, fma(p, f.hi, kWhole - n));
+  const float2 c = turn_cos_sin((int)__double_as_longlong(n), (float)rest);
   return make_float2(c.x * r.gain, c.y * r.turn);
 }
 

@@ -185,3 +185,23 @@ def test_the_training_step_s_gradient_is_its_loss_s_slope(hk):
         # the difference itself 1e-9 of the loss over 2 h, and ReLU's corners h of the slope
         tol = 1e-3 * np.abs(raw).max() * plan.gain * np.abs(grad).sum() / length + 1e-9 * abs(up) / h + 10 * h * length
         assert slope > 0 and abs(slope - length) <= tol
+
+
+def test_rotary_cosines_and_sines_are_rounded_little_more_than_once(hk):
+    """In units of 2^-24, at any position: the rest of the nearest quarter turn as fp32, pi/2 2^-26, moves a cosine below
+    0.71 by 0.28; its polynomial r^2 Q, up to 0.29, three roundings relative to it, 0.88; the last rounding 0.5.  The
+    sine: 0.37, r P up to 0.08 four roundings, 0.31, the last 0.5, what the polynomial leaves off 0.04.  1.67 at most.
+    Frequencies above a turn a position, and negative ones, among them."""
+    rng = np.random.default_rng(9)
+    pos = np.concatenate([rng.integers(-2 ** 31, 2 ** 31, 1500), np.arange(500), [2 ** 31 - 1, -2 ** 31]])
+    odd = np.concatenate([rng.uniform(-9, 9, 40), np.pi / 2 * np.arange(1, 9), np.geomspace(1e-12, 10, 16)])
+    for plan in (hk.Rotary(64), hk.Rotary(64, base=1000000.0, scaling="yarn", factor=32.0, original=32768, gain=1.0), hk.Rotary(128, freq=odd)):
+        half = plan.dim // 2
+        x = np.zeros((len(pos), 1, plan.dim), np.float32)
+        x[..., :half] = 1  # gives (cos, sin)
+        y = hk.rotary(torch.from_numpy(x).cuda(), plan, q_pos=torch.from_numpy(pos.astype(np.int32)).cuda())
+        # the reference's own mantissa of 64 bits: three roundings of 4.3e9 turns, 0.08
+        ref = op.rotary(x.astype(np.float64), pos, plan.freq.cpu().numpy())
+        err = np.abs(y.double().cpu().numpy() - ref)
+        say(f"rotary cosines and sines: largest error {err.max() / U:.2f} * 2^-24")
+        assert err.max() <= 1.75 * U, (np.argwhere(err > 1.75 * U)[0], err.max() / U)
