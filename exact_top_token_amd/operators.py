@@ -62,7 +62,7 @@ def _rows_array(t, name: str) -> RowsArray:
     axes = len(stride)
     if axes != 2 and axes != 3:
         raise ValueError(f"{name} must be [n][d] or [n][heads][d], got {tuple(t.shape)}")
-    if stride[-1] != 1 and t.shape[-1] > 1:
+    if stride[-1] != 1 and t.shape[-1] > 1 and t.numel():
         raise ValueError(f"the last axis of {name} must be contiguous")
     return RowsArray(t.data_ptr(), stride[0], stride[1] if axes == 3 else 0,
                      0 if dtype == _bf16 else 1, 0)

@@ -300,3 +300,14 @@ LOSS_CASES = [
 @pytest.mark.parametrize("kw,status,words", LOSS_CASES)
 def test_index_loss_refuses_for_its_reason(lib, kw, status, words):
     refused(lib, index_loss(lib, **kw), status, words)
+
+
+def test_empty_rows_have_no_strides_to_refuse():
+    """A tensor without elements is contiguous whatever its strides say (those from numpy are all 0)."""
+    import numpy as np
+    import torch
+    empty = torch.from_numpy(np.zeros((0, 3, 64), np.float32))
+    assert empty.stride() == (0, 0, 0)
+    hk.operators._rows_array(empty, "x")
+    with pytest.raises(ValueError):
+        hk.operators._rows_array(torch.zeros(64, 3, 2).transpose(0, 2), "x")
