@@ -339,7 +339,7 @@ int hytopk_rotary_frequencies(int32_t dim, double base, int32_t scaling, double 
  * or, with q_pos NULL, q_start + i (below 2^31).  backward = 1 applies the transposed rotation
  * (gain included): the gradient with respect to x from the gradient with
  * respect to y.  Angles are formed and reduced in 64 bits and their rounding errors (exact to
- * their rounding to 32 bits, 2^-26 of a turn, at any int32 position), products are fp32, rounded once to y's type.  x and y may
+ * their rounding to 32 bits, 2^-28 of a turn, at any int32 position), products are fp32, rounded once to y's type.  x and y may
  * be the same rows (same data, strides and type); otherwise they must share no
  * memory, and lie one behind the other unless their strides in bytes are the same
  * (disjoint slices of one buffer may lie between each other).  heads, d >= 1 and heads * d < 2^31; dim <= 1024. */
