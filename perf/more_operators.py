@@ -154,7 +154,7 @@ def prepare(case, seed):
         if op != "norm":
             s["dy"] = (normal(n, h, d) / math.sqrt(d)).to(DTYPES[case["dy"]]).view(_shape(case))
         if op == "grad":  # kept by the forward pass
-            s["mean"], s["rstd"] = (t[..., 0].float().contiguous() for t in _statistics(s["x"].double()))
+            s["stats"] = torch.cat(_statistics(s["x"].double()), -1).float()  # [..][2]: mean, reciprocal deviation
     else:
         grad = op == "axes" and case["grad"]
         s["x"] = (normal(n, h, d) * torch.exp(0.5 * normal(n, 1, 1))).to(torch.float32 if grad else torch.bfloat16)
@@ -181,7 +181,7 @@ def _plan(s):
     import exact_top_token_amd as hk
     c = s["case"]
     if c["op"] == "grad":
-        s["saved"] = hk.NormSaved(s["x"], None, s["mean"], s["rstd"], None)
+        s["saved"] = hk.NormSaved(s["x"], None, s["stats"], None)
     if c["op"] in ("axes", "axes_write"):
         s["plan"] = hk.Rotary(c["rot"], first=c["first"], layout=c["layout"], device=DEV, sections=_sections(c),
                               cycle=c["cycle"], restart=c["restart"], base=10000.0 if c["d"] == 64 else 1000000.0)
@@ -266,7 +266,7 @@ def _plain(s):
         return _stored(y, c["fmt"], 2).to(torch.bfloat16).view(s["x"].shape)
     x = s["x"].float()
     if op == "grad":
-        dx, dw, db = _norm_back(s["dy"].float(), x, s["mean"][..., None], s["rstd"][..., None], s["weight"])
+        dx, dw, db = _norm_back(s["dy"].float(), x, s["stats"][..., :1], s["stats"][..., 1:], s["weight"])
         return {"dx": dx.to(DTYPES[c["dx"]]), "dweight": dw, "dbias": db}
     mean, rstd = _statistics(x)
     y = (x - mean) * rstd * s["weight"] + s["bias"]
