@@ -20,7 +20,7 @@ __all__ = [
     "backward", "backward_workspace_bytes", "select_noalloc", "NOALLOC_SCRATCH_BYTES",
     "select_async", "ASYNC_STATUS_WORDS", "Rotary", "rotary", "cache_write", "cache_read",
     "cache_write_workspace_bytes", "quantize", "attention_mass", "attention_mass_workspace_bytes",
-    "index_loss",
+    "index_loss", "NormSaved", "layer_norm", "layer_norm_backward", "layer_norm_backward_workspace_bytes",
 ]
 
 BF16, FP8_E4M3, MXFP8_E4M3, MXFP4_E2M1 = 0, 1, 2, 3
@@ -33,6 +33,7 @@ EXPORTS = (
     "hytopk_select_noalloc", "hytopk_select_async", "hytopk_rotary_frequencies", "hytopk_rotary",
     "hytopk_cache_write_workspace", "hytopk_cache_write", "hytopk_cache_read",
     "hytopk_attention_mass_workspace", "hytopk_attention_mass", "hytopk_index_loss",
+    "hytopk_layer_norm", "hytopk_layer_norm_backward_workspace", "hytopk_layer_norm_backward",
 )
 NOALLOC_SCRATCH_BYTES = 64 << 20  # HYTOPK_NOALLOC_SCRATCH_BYTES
 
@@ -75,7 +76,7 @@ class RowsArray(ctypes.Structure):
 class RotaryPlan(ctypes.Structure):
     _fields_ = [("freq", ctypes.c_void_p), ("gain", ctypes.c_double), ("dim", ctypes.c_int32),
                 ("first", ctypes.c_int32), ("layout", ctypes.c_int32),
-                ("reserved", ctypes.c_int32)]
+                ("axes", ctypes.c_int32)]
 
 
 class Cache(ctypes.Structure):
@@ -88,6 +89,11 @@ class Attention(ctypes.Structure):
     _fields_ = [("L", ctypes.c_int64), ("n", ctypes.c_int64), ("heads", ctypes.c_int32),
                 ("key_heads", ctypes.c_int32), ("d", ctypes.c_int32), ("k", ctypes.c_int32),
                 ("softmax_scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class Norm(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
 
 
 class HytopkError(RuntimeError):
@@ -156,6 +162,13 @@ def load_library():
     lib.hytopk_cache_write.restype = ctypes.c_int
     lib.hytopk_cache_read.argtypes = [P(Cache), i64, vp, i64, vp, i32, vp]
     lib.hytopk_cache_read.restype = ctypes.c_int
+    lib.hytopk_layer_norm.argtypes = [P(Norm), i64, i32, i32, P(RowsArray), P(RowsArray), vp, P(Cache), vp]
+    lib.hytopk_layer_norm.restype = ctypes.c_int
+    lib.hytopk_layer_norm_backward_workspace.argtypes = [i64, i32, i32]
+    lib.hytopk_layer_norm_backward_workspace.restype = sz
+    lib.hytopk_layer_norm_backward.argtypes = [P(Norm), i64, i32, i32, P(RowsArray), P(RowsArray), P(Cache), vp,
+                                               P(RowsArray), vp, vp, vp, sz, vp]
+    lib.hytopk_layer_norm_backward.restype = ctypes.c_int
     lib.hytopk_attention_mass_workspace.argtypes = [P(Attention)]
     lib.hytopk_attention_mass_workspace.restype = sz
     lib.hytopk_attention_mass.argtypes = [P(Attention), vp, vp, vp, vp, vp, vp, sz, vp]
@@ -483,7 +496,8 @@ def backward(q, k, w, idx, d_score, *, q_scale=None, k_scale=None, q_start=None,
 # The operators around the selection live in a module of their own, loaded on first use (it
 # imports torch, which the build does not need).
 _OPERATORS = ("Rotary", "rotary", "cache_write", "cache_read", "cache_write_workspace_bytes",
-              "quantize", "attention_mass", "attention_mass_workspace_bytes", "index_loss")
+              "quantize", "NormSaved", "layer_norm", "layer_norm_backward",
+              "layer_norm_backward_workspace_bytes", "attention_mass", "attention_mass_workspace_bytes", "index_loss")
 
 
 def __getattr__(name: str):

@@ -19,10 +19,11 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libhytopk.so")
-SOURCES = ["api.hip", "score.hip", "gather.hip", "radix.hip", "backward.hip", "rows.hip", "loss.hip"]
+SOURCES = ["api.hip", "score.hip", "gather.hip", "radix.hip", "backward.hip", "rows.hip", "norm.hip",
+           "loss.hip"]
 # These keep NaN semantics: padding may hold anything, and what is not finite in a
 # live entry has to show in the result.
-NAN_SOURCES = ("rows.hip", "loss.hip")
+NAN_SOURCES = ("rows.hip", "norm.hip", "loss.hip")
 ARCH = os.environ.get("HYTOPK_ARCH", "gfx950")
 
 FLAGS = [

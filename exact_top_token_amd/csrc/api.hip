@@ -765,6 +765,7 @@ int guarded(F body) noexcept {
 constexpr int64_t kMaxRows = int64_t(1) << 31;
 constexpr int kMaxRotary = 1024;
 constexpr int kMaxRowElems = 8192;
+constexpr int kMaxAxes = 16;
 
 bool misaligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
 
@@ -870,6 +871,8 @@ int check_plan(const hytopk_rotary_plan* p, int32_t d) {
   if (!p->freq) return fail(HYTOPK_EINVAL, "rotary freq is NULL");
   if (misaligned(p->freq, 8)) return fail(HYTOPK_EINVAL, "rotary freq must be 8-byte aligned");
   if (!std::isfinite((float)p->gain)) return fail(HYTOPK_EINVAL, "the rotary gain must be finite in fp32");
+  if (p->axes < 0) return fail(HYTOPK_EINVAL, "the rotary axes must be >= 0");
+  if (p->axes > kMaxAxes) return fail(HYTOPK_EUNSUPPORTED, "rotary axes > 16");
   return HYTOPK_OK;
 }
 
@@ -882,6 +885,10 @@ int check_positions(int64_t n, const int32_t* q_pos, int64_t q_start) {
   return HYTOPK_OK;
 }
 
+// Bytes of a plan's frequencies (and the axes behind them), and of the positions of n tokens.
+int64_t plan_bytes(const hytopk_rotary_plan* p) { return (p->axes > 1 ? 6 : 4) * (int64_t)p->dim; }
+int64_t position_bytes(const hytopk_rotary_plan* p, int64_t n) { return 4 * n * std::max(p->axes, 1); }
+
 hk::RotArgs rot_args(const hytopk_rotary_plan* p, const int32_t* q_pos, int64_t q_start, bool backward) {
   hk::RotArgs r{};
   if (!p) return r;
@@ -890,7 +897,8 @@ hk::RotArgs rot_args(const hytopk_rotary_plan* p, const int32_t* q_pos, int64_t 
   r.pos0 = (int)q_start;  // below 2^31
   r.gain = (float)p->gain;
   r.turn = backward ? -r.gain : r.gain;
-  r.dim = p->dim;
+  r.dim = (uint16_t)p->dim;
+  r.axes = (uint16_t)std::max(p->axes, 1);
   return r;
 }
 
@@ -938,6 +946,67 @@ int check_cache(const hytopk_cache* c, int64_t n, const int32_t* slots, int64_t 
 }
 
 bool wants_claim(int64_t n, bool by_slot) { return by_slot && n > hk::kClaimRows; }
+
+int check_norm(const hytopk_norm* p) {
+  if (!p) return fail(HYTOPK_EINVAL, "norm is NULL");
+  if (p->dtype != HYTOPK_ROWS_BF16 && p->dtype != HYTOPK_ROWS_FP32)
+    return fail(HYTOPK_EINVAL, "unknown dtype of the norm's parameters");
+  const uintptr_t e = p->dtype == HYTOPK_ROWS_BF16 ? 2 : 4;
+  if (misaligned(p->weight, e) || misaligned(p->bias, e))
+    return fail(HYTOPK_EINVAL, "weight and bias must be aligned to their element");
+  return HYTOPK_OK;
+}
+
+int check_norm_rows(int64_t n, int32_t heads, int32_t d) {
+  const int rc = check_tokens(n, heads, d);
+  if (rc) return rc;
+  if (d > hk::kMaxNorm) return fail(HYTOPK_EUNSUPPORTED, "rows of a norm have d <= 8192");
+  if (n * heads >= kMaxRows) return fail(HYTOPK_EUNSUPPORTED, "n * heads >= 2^31");
+  return HYTOPK_OK;
+}
+
+int check_stats(const float* stats) {
+  if (misaligned(stats, 8)) return fail(HYTOPK_EINVAL, "stats must be 8-byte aligned");
+  return HYTOPK_OK;
+}
+
+// A norm's checkpoint: one cache row for each of its rows.
+int check_checkpoint(const hytopk_cache* c, int64_t rows, int32_t d) {
+  const int rc = check_cache(c, rows, nullptr, 0);
+  if (rc) return rc;
+  if (c->dtype != HYTOPK_FP8_E4M3 && c->dtype != HYTOPK_MXFP8_E4M3)
+    return fail(HYTOPK_EUNSUPPORTED, "checkpoints are FP8 or MXFP8");
+  if (c->heads != 1 || c->d != d) return fail(HYTOPK_EINVAL, "a checkpoint's rows are the norm's: heads 1, the same d");
+  return HYTOPK_OK;
+}
+
+// The bytes of a norm's parameters.
+Extent parameter(const hytopk_norm* p, const void* v, int32_t d) {
+  return v ? extent(v, (int64_t)d * (p->dtype == HYTOPK_ROWS_BF16 ? 2 : 4)) : Extent{0, 0};
+}
+
+// Memory that a call reads or writes, empty where it does not exist.
+Extent memory(const void* p, int64_t bytes) { return p ? extent(p, bytes) : Extent{0, 0}; }
+Extent memory(const hytopk_rows* r, int64_t n, int32_t heads, int32_t d) { return r ? extent(r, n, heads, d) : Extent{0, 0}; }
+bool empty(Extent e) { return e.lo == e.hi; }
+
+// Whether any of `written` overlaps another of them or any of `read`.
+template <size_t W, size_t R>
+bool written_meets(const Extent (&written)[W], const Extent (&read)[R]) {
+  for (size_t i = 0; i < W; ++i) {
+    if (empty(written[i])) continue;
+    for (size_t j = 0; j < W; ++j)
+      if (j != i && !empty(written[j]) && overlap(written[i], written[j])) return true;
+    for (size_t j = 0; j < R; ++j)
+      if (!empty(read[j]) && overlap(written[i], read[j])) return true;
+  }
+  return false;
+}
+
+bool same_rows(const hytopk_rows* x, const hytopk_rows* y, int64_t n, int32_t heads) {
+  return x->data == y->data && x->dtype == y->dtype && (n == 1 || x->token_stride == y->token_stride) &&
+         (heads == 1 || x->head_stride == y->head_stride);
+}
 
 // The softmax's scale in base 2.
 float log2_scale(const hytopk_attention* p) { return (float)((double)p->softmax_scale * 1.4426950408889634074); }
@@ -1017,12 +1086,10 @@ int hytopk_rotary(const hytopk_rotary_plan* plan, int64_t n, int32_t heads, int3
     if ((rc = check_positions(n, q_pos, q_start))) return rc;
     if (n == 0) return HYTOPK_OK;
     if (!rows_apart(y, n, heads, d)) return fail(HYTOPK_EINVAL, "rows of y overlap each other");
-    const bool same = x->data == y->data && x->dtype == y->dtype &&
-                      (n == 1 || x->token_stride == y->token_stride) &&
-                      (heads == 1 || x->head_stride == y->head_stride);
-    if (!same && rows_meet(x, y, n, heads, d)) return fail(HYTOPK_EINVAL, "x and y overlap (y may be x itself)");
+    if (!same_rows(x, y, n, heads) && rows_meet(x, y, n, heads, d))
+      return fail(HYTOPK_EINVAL, "x and y overlap (y may be x itself)");
     const Extent out = extent(y, n, heads, d);
-    if (touches(out, q_pos, 4 * n) || touches(out, plan->freq, 4 * (int64_t)plan->dim))
+    if (touches(out, q_pos, position_bytes(plan, n)) || touches(out, plan->freq, plan_bytes(plan)))
       return fail(HYTOPK_EINVAL, "y overlaps the positions or the plan");
     hk::RotaryArgs a{};
     a.x = x->data;
@@ -1066,12 +1133,12 @@ int hytopk_cache_write(const hytopk_cache* c, int64_t n, const hytopk_rows* x,
     const bool claim = wants_claim(n, slots != nullptr);
     if (claim && (rc = check_ws(workspace, workspace_bytes, hytopk_cache_write_workspace(c, n, 1)))) return rc;
     if (in_cache(c, slots, 4 * n) || (claim && in_cache(c, workspace, 4 * c->L)) ||
-        (plan && (in_cache(c, q_pos, 4 * n) || in_cache(c, plan->freq, 4 * (int64_t)plan->dim))))
+        (plan && (in_cache(c, q_pos, position_bytes(plan, n)) || in_cache(c, plan->freq, plan_bytes(plan)))))
       return fail(HYTOPK_EINVAL, "the slots, the positions, the plan or the workspace overlap the cache");
     if (claim) {  // cleared and written while the others are read
       const Extent w = extent(workspace, 4 * c->L);
       if (touches(w, slots, 4 * n) || overlap(w, extent(x, n, c->heads, c->d)) ||
-          (plan && (touches(w, q_pos, 4 * n) || touches(w, plan->freq, 4 * (int64_t)plan->dim))))
+          (plan && (touches(w, q_pos, position_bytes(plan, n)) || touches(w, plan->freq, plan_bytes(plan)))))
         return fail(HYTOPK_EINVAL, "the workspace overlaps the rows, the slots, the positions or the plan");
     }
     if (overlap(cache_codes(c), cache_scale(c))) return fail(HYTOPK_EINVAL, "the cache's codes and scales overlap");
@@ -1121,6 +1188,121 @@ int hytopk_cache_read(const hytopk_cache* c, int64_t n, const int32_t* slots, in
     hipStream_t s = static_cast<hipStream_t>(stream);
     Span sp("cache_read", s);
     HK_HIP(hk::launch_cache_read(a, out_dtype, c->dtype, s), "cache read launch");
+    return HYTOPK_OK;
+  });
+}
+
+int hytopk_layer_norm(const hytopk_norm* norm, int64_t n, int32_t heads, int32_t d, const hytopk_rows* x,
+                      const hytopk_rows* y, float* stats, const hytopk_cache* save, void* stream) {
+  return guarded([&]() -> int {
+    int rc = check_norm_rows(n, heads, d);
+    if (rc) return rc;
+    if ((rc = check_norm(norm))) return rc;
+    if (!(norm->eps >= 0.0f) || !std::isfinite(norm->eps)) return fail(HYTOPK_EINVAL, "eps must be finite and >= 0");
+    if ((rc = check_rows(x, n, heads, d)) || (rc = check_rows(y, n, heads, d))) return rc;
+    if ((rc = check_stats(stats))) return rc;
+    const int64_t rows = n * heads;
+    if (save && n > 0) {
+      if ((rc = check_checkpoint(save, rows, d))) return rc;
+      if (!stats) return fail(HYTOPK_EINVAL, "a checkpoint needs stats");
+    }
+    if (n == 0) return HYTOPK_OK;
+    if (!rows_apart(y, n, heads, d)) return fail(HYTOPK_EINVAL, "rows of y overlap each other");
+    if (!same_rows(x, y, n, heads) && rows_meet(x, y, n, heads, d))
+      return fail(HYTOPK_EINVAL, "x and y overlap (y may be x itself)");
+    const Extent w = parameter(norm, norm->weight, d), b = parameter(norm, norm->bias, d);
+    const Extent codes = save ? cache_codes(save) : Extent{0, 0}, scale = save ? cache_scale(save) : Extent{0, 0};
+    const Extent st = memory(stats, 8 * rows), ex = extent(x, n, heads, d), ey = extent(y, n, heads, d);
+    if (written_meets({ey, st, codes, scale}, {w, b}) || written_meets({st, codes, scale}, {ex}))
+      return fail(HYTOPK_EINVAL, "y, the statistics or the checkpoint overlap each other, x or the parameters");
+    hk::NormArgs a{};
+    a.x = x->data;
+    a.y = y->data;
+    a.xts = x->token_stride; a.xhs = x->head_stride;
+    a.yts = y->token_stride; a.yhs = y->head_stride;
+    a.weight = norm->weight;
+    a.bias = norm->bias;
+    a.stats = reinterpret_cast<float2*>(stats);
+    a.codes = save ? static_cast<uint8_t*>(save->codes) : nullptr;
+    a.scale = save ? save->scale : nullptr;
+    a.rows = (int)rows;
+    a.heads = heads;
+    a.eps = norm->eps;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    Span sp("layer_norm", s);
+    HK_HIP(hk::launch_layer_norm(a, d, norm->dtype == HYTOPK_ROWS_FP32, x->dtype, y->dtype,
+                                 save ? save->dtype : HYTOPK_BF16, s), "layer norm launch");
+    return HYTOPK_OK;
+  });
+}
+
+size_t hytopk_layer_norm_backward_workspace(int64_t n, int32_t heads, int32_t d) {
+  size_t need = 0;
+  guarded([&]() -> int {
+    const int rc = check_norm_rows(n, heads, d);
+    if (rc == HYTOPK_OK) need = align_up((size_t)hk::norm_backward_blocks(n * heads, d) * 2 * d * sizeof(float));
+    return rc;
+  });
+  return need;
+}
+
+int hytopk_layer_norm_backward(const hytopk_norm* norm, int64_t n, int32_t heads, int32_t d, const hytopk_rows* dy,
+                               const hytopk_rows* x, const hytopk_cache* saved, const float* stats,
+                               const hytopk_rows* dx, float* dweight, float* dbias, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  return guarded([&]() -> int {
+    int rc = check_norm_rows(n, heads, d);
+    if (rc) return rc;
+    if ((rc = check_norm(norm))) return rc;
+    if ((rc = check_rows(dy, n, heads, d))) return rc;
+    if ((x != nullptr) == (saved != nullptr)) return fail(HYTOPK_EINVAL, "give the norm's input or its checkpoint");
+    const int64_t rows = n * heads;
+    if (x ? (rc = check_rows(x, n, heads, d)) : n > 0 && (rc = check_checkpoint(saved, rows, d))) return rc;
+    if (dx && (rc = check_rows(dx, n, heads, d))) return rc;
+    if ((rc = check_stats(stats))) return rc;
+    if (!stats && n > 0) return fail(HYTOPK_EINVAL, "the backward needs the forward's stats");
+    if (misaligned(dweight, 4) || misaligned(dbias, 4)) return fail(HYTOPK_EINVAL, "dweight and dbias must be 4-byte aligned");
+    const bool sums = dweight || dbias;
+    const int64_t need = sums ? (int64_t)hytopk_layer_norm_backward_workspace(n, heads, d) : 0;
+    if (need && (rc = check_ws(workspace, workspace_bytes, (size_t)need))) return rc;
+    if (n > 0 && dx) {
+      if (!rows_apart(dx, n, heads, d)) return fail(HYTOPK_EINVAL, "rows of dx overlap each other");
+      if (!same_rows(dy, dx, n, heads) && rows_meet(dy, dx, n, heads, d))
+        return fail(HYTOPK_EINVAL, "dy and dx overlap (dx may be dy itself)");
+      if (x && !same_rows(x, dx, n, heads) && rows_meet(x, dx, n, heads, d))
+        return fail(HYTOPK_EINVAL, "x and dx overlap (dx may be x itself)");
+    }
+    const Extent none{0, 0}, w = parameter(norm, norm->weight, d), st = memory(stats, 8 * rows);
+    const Extent ws = need ? extent(workspace, need) : none, gw = memory(dweight, 4 * (int64_t)d), gb = memory(dbias, 4 * (int64_t)d);
+    const Extent ex = n > 0 ? memory(x, n, heads, d) : none, ey = n > 0 ? extent(dy, n, heads, d) : none;
+    const Extent edx = n > 0 ? memory(dx, n, heads, d) : none;
+    const Extent codes = saved && n > 0 ? cache_codes(saved) : none, scale = saved && n > 0 ? cache_scale(saved) : none;
+    if (written_meets({edx, gw, gb, ws}, {w, st, codes, scale}) || written_meets({gw, gb, ws}, {ex, ey}))
+      return fail(HYTOPK_EINVAL, "the gradients or the workspace overlap each other or what is read");
+    hk::NormBackArgs a{};
+    a.dy = dy->data;
+    a.dyts = dy->token_stride; a.dyhs = dy->head_stride;
+    if (x) {
+      a.x = x->data;
+      a.xts = x->token_stride; a.xhs = x->head_stride;
+    } else {
+      a.x = saved->codes;
+      a.scale = saved->scale;
+    }
+    if (dx) {
+      a.dx = dx->data;
+      a.dxts = dx->token_stride; a.dxhs = dx->head_stride;
+    }
+    a.weight = norm->weight;
+    a.stats = reinterpret_cast<const float2*>(stats);
+    a.part = need ? static_cast<float*>(workspace) : nullptr;
+    a.rows = (int)rows;
+    a.heads = heads;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    Span sp("layer_norm_backward", s);
+    HK_HIP(hk::launch_layer_norm_backward(a, d, norm->dtype == HYTOPK_ROWS_FP32, x ? x->dtype : 0,
+                                          saved ? saved->dtype : HYTOPK_BF16, dy->dtype, dx ? dx->dtype : dy->dtype,
+                                          dweight, dbias, s), "layer norm backward launch");
     return HYTOPK_OK;
   });
 }

@@ -257,17 +257,18 @@ constexpr int kRowsBF16 = 0, kRowsFP32 = 1;            // hytopk_rows_dtype
 constexpr int kRotHalf = 0, kRotInterleaved = 1;       // hytopk_rotary_layout
 
 // What a launch takes on the host grows from 2.8 to 3.6 us where a kernel's arguments pass 112 bytes,
-// the grid's and block's sizes (gridDim, blockDim: about 70 bytes) among them.  The kernels of rows.hip
-// and loss.hip are often shorter than that, so their arguments stay within it and they read neither.
+// the grid's and block's sizes (gridDim, blockDim: about 70 bytes) among them.  The kernels of rows.hip,
+// norm.hip and loss.hip are often shorter than that, so their arguments stay within it and they read neither.
 
 // A rotation (freq == null: none) and the tokens' positions.
 struct RotArgs {
-  const double* freq;  // [dim/2] radians a position
-  const int* pos;      // [n] positions, or null (pos0 + i)
+  const double* freq;  // [dim/2] radians a position; with several axes, behind them int [dim/2]: each pair's
+  const int* pos;      // [n][axes] positions, or null (pos0 + i on every axis)
   int pos0;
   float gain;          // factor on the cosines
   float turn;          // factor on the sines: gain, or -gain for the transposed rotation
-  int dim;
+  uint16_t dim;        // at most 1,024
+  uint16_t axes;       // at least 1
 };
 
 struct RotaryArgs {
@@ -308,6 +309,47 @@ struct CacheReadArgs {
 };
 
 hipError_t launch_cache_read(const CacheReadArgs& a, int out_dtype, int fmt, hipStream_t s);
+
+// ---- layer norm and its 8-bit checkpoints (norm.hip)
+
+constexpr int kMaxNorm = 8192;  // elements of a row
+
+struct NormArgs {
+  const void* x;
+  void* y;
+  int64_t xts, xhs, yts, yhs;  // token and head strides in elements
+  const void* weight;  // [d], or null (1)
+  const void* bias;    // [d], or null (0)
+  float2* stats;       // [rows] mean and reciprocal deviation, or null
+  uint8_t* codes;      // the checkpoint's [rows][d] and its scales
+  void* scale;
+  int rows, heads;     // rows = tokens * heads
+  float eps;
+};
+
+// save: kFP8, kMXFP8, or kBF16 for no checkpoint.
+hipError_t launch_layer_norm(const NormArgs& a, int d, bool weight32, int in_dtype, int out_dtype, int save,
+                             hipStream_t s);
+
+struct NormBackArgs {
+  const void* x;       // rows, or a checkpoint's codes
+  const void* dy;
+  void* dx;            // or null
+  union {
+    struct { int64_t xts, xhs; };
+    const void* scale;  // of a checkpoint
+  };
+  int64_t dyts, dyhs, dxts, dxhs;
+  const void* weight;  // [d], or null (1)
+  const float2* stats;  // [rows]
+  float* part;         // [norm_backward_blocks][2][d], or null: no sums
+  int rows, heads;
+};
+
+// codes: kFP8 or kMXFP8 for a checkpoint, kBF16 for rows of x_dtype.
+hipError_t launch_layer_norm_backward(const NormBackArgs& a, int d, bool weight32, int x_dtype, int codes, int dy_dtype,
+                                      int dx_dtype, float* dweight, float* dbias, hipStream_t s);
+int norm_backward_blocks(int64_t rows, int d);
 
 // ---- attention mass at the selected entries, index loss (loss.hip)
 

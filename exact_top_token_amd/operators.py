@@ -1,5 +1,5 @@
-"""Bindings of the operators around the selection: rotary positions, the quantised
-cache, the attention's mass at the selected entries and the indexer's loss.
+"""Bindings of the operators around the selection: layer norm and its 8-bit checkpoints, rotary
+positions, the quantised cache, the attention's mass at the selected entries and the indexer's loss.
 
 As in the package's own module only tensors are marshalled here; the kernels run on
 the tensors' GPU and its current stream.  A call's host time is most of a small
@@ -10,14 +10,16 @@ from __future__ import annotations
 
 import ctypes
 import math
+from typing import NamedTuple
 
 import torch
 
-from . import (BF16, FP8_E4M3, MXFP4_E2M1, _FMT, Attention, Cache, RotaryPlan, RowsArray, _check,
+from . import (BF16, FP8_E4M3, MXFP4_E2M1, MXFP8_E4M3, _FMT, Attention, Cache, Norm, RotaryPlan, RowsArray, _check,
                _dtype_code, _workspace, load_library)
 
 __all__ = ["Rotary", "rotary", "cache_write", "cache_read", "cache_write_workspace_bytes",
-           "quantize", "attention_mass", "attention_mass_workspace_bytes", "index_loss"]
+           "quantize", "NormSaved", "layer_norm", "layer_norm_backward", "layer_norm_backward_workspace_bytes",
+           "attention_mass", "attention_mass_workspace_bytes", "index_loss"]
 
 _EWORKSPACE = -3  # HYTOPK_EWORKSPACE
 _bf16, _f32, _i32, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
@@ -86,11 +88,17 @@ class Rotary:
     ``scaling`` ("none", "linear", "ntk", "yarn") stretches the positions by
     ``factor`` for a model whose positions reached ``original`` before.  ``gain`` replaces the
     scaling's own factor (YaRN: 0.1 ln(factor) + 1; else 1), and ``freq``
-    [dim/2] (radians a position) the frequencies, for a model with its own."""
+    [dim/2] (radians a position) the frequencies, for a model with its own.
+
+    ``sections`` (pairs of each axis, dim/2 in all) is for tokens with a position on
+    each of several axes, such as time, height and width; ``q_pos`` is then int32 [n][axes].  The axes'
+    pairs lie one behind the other or, with ``cycle``, in turn: axis a > 0 takes pairs a, a + A, a + 2A, ... of A axes,
+    as many as it has, and axis 0 the others.  ``restart`` begins the frequencies anew on each axis, as those of a
+    rotation of its pairs alone."""
 
     def __init__(self, dim: int, *, first: int = 0, layout: str = "half", base: float = 10000.0,
                  scaling: str = "none", factor: float = 1.0, original: int = 0, gain=None, freq=None,
-                 device="cuda"):
+                 sections=None, cycle: bool = False, restart: bool = False, device="cuda"):
         if layout not in _LAYOUTS:
             raise ValueError(f"unknown rotary layout {layout!r}")
         if scaling not in _SCALINGS:
@@ -98,22 +106,64 @@ class Rotary:
         dim, first, original = int(dim), int(first), int(original)
         if not (0 < dim < 1 << 31 and 0 <= first < 1 << 31):
             raise ValueError("dim must be > 0 and first >= 0, both below 2^31")
-        made = torch.empty(max(min(dim, 1024) // 2, 1), dtype=torch.float64)
         factor_on = ctypes.c_double()
-        _check(load_library().hytopk_rotary_frequencies(dim, float(base), _SCALINGS[scaling],
-                                                        float(factor), original, made.data_ptr(),
-                                                        ctypes.byref(factor_on)))
+
+        def frequencies(dim):
+            made = torch.empty(max(min(dim, 1024) // 2, 1), dtype=torch.float64)
+            _check(load_library().hytopk_rotary_frequencies(dim, float(base), _SCALINGS[scaling], float(factor),
+                                                            original, made.data_ptr(), ctypes.byref(factor_on)))
+            return made
+
+        made = frequencies(dim)
+        sections = None if sections is None else tuple(sections)
+        axis, axes = _axis_of_pairs(dim // 2, sections, cycle), 1 if sections is None else len(sections)
         if freq is not None:
             own = torch.as_tensor(freq).detach().cpu()
-            if scaling != "none" or own.shape != made.shape or not torch.isfinite(own).all():
-                raise ValueError(f"freq must hold {dim // 2} finite values, and takes no scaling")
+            if scaling != "none" or restart or own.shape != made.shape or not torch.isfinite(own).all():
+                raise ValueError(f"freq must hold {dim // 2} finite values, and takes no scaling or restart")
             made.copy_(own)
+        elif restart:
+            if sections is None:
+                raise ValueError("restart needs sections")
+            for a in range(axes):
+                made[axis == a] = frequencies(2 * int(sections[a]))
         gain = factor_on.value if gain is None else float(gain)
         if not math.isfinite(gain):
             raise ValueError("gain must be finite")
-        self.freq = made.to(device)
-        self.gain, self.dim, self.first, self.layout = gain, dim, first, layout
-        self._plan = RotaryPlan(self.freq.data_ptr(), self.gain, dim, first, _LAYOUTS[layout], 0)
+        half = made.numel()
+        if axes > 1:  # the pairs' axes lie behind the frequencies
+            table = torch.zeros(half + (half + 1) // 2, dtype=torch.float64)
+            table[:half] = made
+            table[half:].view(_i32)[:half] = axis
+            made = table
+        made = made.to(device)
+        self.freq = made[:half]
+        self.axis = made[half:].view(_i32)[:half] if axes > 1 else None
+        self.gain, self.dim, self.first, self.layout, self.axes = gain, dim, first, layout, axes
+        self._plan = RotaryPlan(self.freq.data_ptr(), self.gain, dim, first, _LAYOUTS[layout], axes if axes > 1 else 0)
+
+
+def _axis_of_pairs(pairs: int, sections, cycle: bool):
+    """The axis of each of a rotation's pairs (int32 [pairs])."""
+    axis = torch.zeros(pairs, dtype=_i32)
+    if sections is None:
+        if cycle:
+            raise ValueError("cycle needs sections")
+        return axis
+    counts = [int(s) for s in sections]
+    A = len(counts)
+    if not 1 <= A <= 16 or min(counts) < 1 or sum(counts) != pairs:
+        raise ValueError(f"sections must give 1 to 16 axes one pair or more each, {pairs} in all, got {counts}")
+    at = 0
+    for a, s in enumerate(counts):
+        if not cycle:
+            axis[at:at + s] = a
+            at += s
+        elif a:
+            if a + (s - 1) * A >= pairs:
+                raise ValueError(f"axis {a} has {s} pairs, more than its turns among {pairs} pairs")
+            axis[a:a + s * A:A] = a
+    return axis
 
 
 def _plan(rot, device):
@@ -129,7 +179,8 @@ def rotary(x, rot: Rotary, *, q_start: int = 0, q_pos=None, backward: bool = Fal
     """Rotary positions of rows x [n][d] or [n][heads][d] (bf16 or fp32, any
     strides but the last).  Token i sits at ``q_pos[i]`` (int32 [n] on the GPU) or
     ``q_start + i``.  ``backward`` applies the transposed rotation, which
-    takes a gradient of the result to one of x.  ``out`` may be x itself."""
+    takes a gradient of the result to one of x.  A plan of several axes takes ``q_pos``
+    [n][axes].  ``out`` may be x itself."""
     _gpu(x, "x")
     xa = _rows_array(x, "x")
     shape, device = x.shape, x.device
@@ -145,7 +196,7 @@ def rotary(x, rot: Rotary, *, q_start: int = 0, q_pos=None, backward: bool = Fal
             raise ValueError(f"out must have x's shape {tuple(shape)} and device, and out_dtype")
         ya = _rows_array(out, "out")
     if q_pos is not None:
-        _need(q_pos, "q_pos", (n,), _i32, device)
+        _need(q_pos, "q_pos", (n,) if rot.axes == 1 else (n, rot.axes), _i32, device)
     _launch(device, load_library().hytopk_rotary, _plan(rot, device), n, heads, d, xa, ya,
             _address(q_pos), int(q_start), 1 if backward else 0)
     return out
@@ -204,7 +255,7 @@ def cache_write(x, codes, scale=None, *, fmt=None, start: int = 0, slots=None, r
     if shape[-1] != c.d or (shape[1] if len(shape) == 3 else 1) != c.heads:
         raise ValueError(f"x {tuple(shape)} does not fit cache rows of {c.heads} x {c.d}")
     if q_pos is not None:
-        _need(q_pos, "q_pos", (n,), _i32, device)
+        _need(q_pos, "q_pos", (n,) if rotary is None or rotary.axes == 1 else (n, rotary.axes), _i32, device)
     if slots is not None:
         _need(slots, "slots", (n,), _i32, device)
     if workspace is not None:
@@ -268,6 +319,163 @@ def cache_read(codes, scale=None, *, fmt=None, slots=None, start: int = 0, count
     _launch(device, load_library().hytopk_cache_read, c, n, _address(slots), int(start),
             out.data_ptr(), 0 if dtype == _bf16 else 1)
     return out
+
+
+# ------------------------------------------ layer norm and its checkpoints
+
+_CHECKPOINTS = {"fp8": FP8_E4M3, "mxfp8": MXFP8_E4M3}
+
+
+class NormSaved(NamedTuple):
+    """What a layer norm keeps for its backward: its input (``fmt`` None, ``scale`` None) or the
+    input's codes and scales in 8 bits (``fmt`` "fp8": uint8 of x's shape, fp32 a row; "mxfp8":
+    one uint8 per 32 elements), and each row's mean and reciprocal deviation (``stats``, fp32 [..., 2])."""
+    rows: torch.Tensor
+    scale: torch.Tensor | None
+    stats: torch.Tensor
+    fmt: str | None
+
+
+def _norm_shape(t, name: str):
+    """n, heads and d of rows [n][d] or [n][heads][d]."""
+    shape = t.shape
+    if len(shape) == 2:
+        return shape[0], 1, shape[1]
+    if len(shape) == 3:
+        return shape
+    raise ValueError(f"{name} must be [n][d] or [n][heads][d], got {tuple(shape)}")
+
+
+def _norm(weight, bias, d, eps, device) -> Norm:
+    dtype = _f32
+    if weight is not None:
+        dtype = weight.dtype
+    elif bias is not None:
+        dtype = bias.dtype
+    if dtype != _f32 and dtype != _bf16:
+        raise TypeError(f"weight and bias must be bfloat16 or float32, got {dtype}")
+    if weight is not None:
+        _need(weight, "weight", (d,), dtype, device)
+    if bias is not None:
+        _need(bias, "bias", (d,), dtype, device)
+    return Norm(_address(weight), _address(bias), 0 if dtype == _bf16 else 1, eps)
+
+
+def _saved(s: NormSaved, shape, device):
+    """The rows or the cache that a NormSaved stands for."""
+    lead = shape[:-1]
+    _need(s.stats, "stats", (*lead, 2), _f32, device)
+    if s.fmt is None:
+        if s.scale is not None:
+            raise ValueError("rows that are kept as they are take no scale")
+        if s.rows.shape != shape or s.rows.device != device:
+            raise ValueError(f"saved rows must have the shape {tuple(shape)} and be on {device}")
+        return _rows_array(s.rows, "saved rows"), None
+    if s.fmt not in _CHECKPOINTS:
+        raise ValueError(f"unknown checkpoint format {s.fmt!r}: fp8 or mxfp8")
+    if s.scale is None:
+        raise ValueError("fp8 and mxfp8 checkpoints need scale")
+    d, n = shape[-1], math.prod(lead)
+    _need(s.rows, "saved codes", shape, _u8, device)
+    if s.fmt == "fp8":
+        _need(s.scale, "scale", lead, _f32, device)
+    else:
+        _need(s.scale, "scale", (*lead, d // 32), _u8, device)
+    return None, Cache(s.rows.data_ptr(), s.scale.data_ptr(), n, 1, d, _CHECKPOINTS[s.fmt], 0)
+
+
+def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None, out_dtype=None, save=None):
+    """Layer norm of rows x [n][d] or [n][heads][d] (bf16 or fp32, any strides but the last), each
+    over its d elements: (x - mean) / sqrt(var + eps) * weight + bias, with weight and bias [d]
+    (fp32 or bf16, one type; None: ones and zeros).  ``out`` may be x itself.  With ``save`` the result is
+    (y, saved) and ``layer_norm_backward`` takes ``saved``: "x" keeps x itself (not a copy), "fp8" or "mxfp8"
+    a checkpoint of it in 8 bits (d a multiple of 32), made in the same pass, and a NormSaved names the buffers to fill."""
+    _gpu(x, "x")
+    n, heads, d = _norm_shape(x, "x")
+    xa = _rows_array(x, "x")
+    shape, device = x.shape, x.device
+    if out is None and (out_dtype is None or out_dtype == x.dtype):
+        out = _empty_like(x, memory_format=_contiguous)
+        ya = RowsArray(out.data_ptr(), heads * d, d, xa.dtype, 0)
+    else:
+        if out is None:
+            out = x.new_empty(shape, dtype=out_dtype)
+        elif out.shape != shape or out.device != device or out_dtype not in (None, out.dtype):
+            raise ValueError(f"out must have x's shape {tuple(shape)} and device, and out_dtype")
+        ya = _rows_array(out, "out")
+    p = _norm(weight, bias, d, eps, device)
+    if save is None:
+        _launch(device, load_library().hytopk_layer_norm, p, n, heads, d, xa, ya, None, None)
+        return out
+    if not isinstance(save, NormSaved):
+        stats = x.new_empty((*shape[:-1], 2), dtype=_f32)
+        if save == "x":
+            save = NormSaved(x, None, stats, None)
+        elif save in _CHECKPOINTS:
+            if d % 32:
+                raise ValueError("checkpoints in 8 bits need d in multiples of 32")
+            scale = (x.new_empty(shape[:-1], dtype=_f32) if save == "fp8"
+                     else x.new_empty((*shape[:-1], d // 32), dtype=_u8))
+            save = NormSaved(x.new_empty(shape, dtype=_u8), scale, stats, save)
+        else:
+            raise ValueError(f"save must be 'x', 'fp8', 'mxfp8' or a NormSaved, got {save!r}")
+    rows, cache = _saved(save, shape, device)
+    if cache is None and (rows.data != xa.data or save.rows.dtype != x.dtype or save.rows.stride() != x.stride()):
+        raise ValueError("a NormSaved without a format keeps x itself")
+    if cache is None and rows.data == ya.data and rows.data:
+        raise ValueError("x is kept for the backward: out must not be x")
+    _launch(device, load_library().hytopk_layer_norm, p, n, heads, d, xa, ya, save.stats.data_ptr(), cache)
+    return out, save
+
+
+def layer_norm_backward_workspace_bytes(dy) -> int:
+    """Workspace bytes of layer_norm_backward for dweight or dbias."""
+    return int(load_library().hytopk_layer_norm_backward_workspace(*_norm_shape(dy, "dy")))
+
+
+def layer_norm_backward(dy, saved: NormSaved, weight=None, *, want=("dx", "dweight", "dbias"), dx_dtype=None,
+                        workspace=None, out=None):
+    """Gradients of ``layer_norm`` from dy (the result's shape; bf16 or fp32, any strides but the last)
+    and what it saved: a dict with dx (dy's shape, dy's type or ``dx_dtype``), dweight and dbias (fp32 [d], summed
+    over all rows in a fixed order), those of ``want``.  ``weight`` is the forward's.  ``out`` gives tensors for some
+    of them; dx may be dy or the saved rows themselves."""
+    _gpu(dy, "dy")
+    lib = load_library()
+    n, heads, d = _norm_shape(dy, "dy")
+    ga = _rows_array(dy, "dy")
+    shape, device = dy.shape, dy.device
+    p = _norm(weight, None, d, 0.0, device)
+    rows, cache = _saved(saved, shape, device)
+    res = {} if out is None else dict(out)
+    for name in res:
+        if name not in ("dx", "dweight", "dbias"):
+            raise ValueError(f"unknown gradient name in out: {name!r}")
+    for name in want:
+        if name in res:
+            continue
+        if name == "dx":
+            res[name] = (_empty_like(dy, memory_format=_contiguous) if dx_dtype is None
+                         else dy.new_empty(shape, dtype=dx_dtype))
+        elif name in ("dweight", "dbias"):
+            res[name] = dy.new_empty(d, dtype=_f32)
+        else:
+            raise ValueError(f"unknown gradient name in want: {name!r}")
+    dx, dweight, dbias = res.get("dx"), res.get("dweight"), res.get("dbias")
+    xa = None
+    if dx is not None:
+        if dx.shape != shape or dx.device != device or dx_dtype not in (None, dx.dtype):
+            raise ValueError(f"dx must have dy's shape {tuple(shape)} and device, and dx_dtype")
+        xa = _rows_array(dx, "dx")
+    for t, name in ((dweight, "dweight"), (dbias, "dbias")):
+        if t is not None:
+            _need(t, name, (d,), _f32, device)
+    if workspace is not None:
+        _workspace(workspace, device)
+    elif dweight is not None or dbias is not None:
+        workspace = dy.new_empty(lib.hytopk_layer_norm_backward_workspace(n, heads, d), dtype=_u8)
+    _launch(device, lib.hytopk_layer_norm_backward, p, n, heads, d, ga, rows, cache, saved.stats.data_ptr(), xa,
+            _address(dweight), _address(dbias), _address(workspace), 0 if workspace is None else workspace.numel())
+    return res
 
 
 # ------------------------------------------- the indexer's target and loss

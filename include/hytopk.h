@@ -272,14 +272,16 @@ int hytopk_backward(const hytopk_problem* p, const void* q, const void* q_scale,
  * Around the selection: what makes the indexer's queries and keys, and what
  * turns the replayed scores into the backward's upstream gradient.
  *
- *   rotary positions -> quantised rows in the storage formats above
+ *   layer norm (its input kept, or a checkpoint of it in 8 bits)
+ *     -> rotary positions -> quantised rows in the storage formats above
  *     -> hytopk_select -> hytopk_replay
  *     -> attention mass (the target) -> index loss and d_score
- *     -> hytopk_backward -> transposed rotation of dq and dk
+ *     -> hytopk_backward -> transposed rotation of dq and dk -> the norm's backward
  *
  * All of them are asynchronous on `stream`, launch kernels only (no copy, memset or
  * synchronisation: they can be recorded in a HIP graph after one eager call
- * with the same shapes) and hold no state between calls.  n = 0 is a valid call that does nothing.
+ * with the same shapes) and hold no state between calls.  n = 0 is a valid call that does nothing
+ * (the norm's backward sets its sums to 0).
  * ------------------------------------------------------------------------- */
 
 /* Element types of the rows that the rotation and the cache calls read and write. */
@@ -317,14 +319,18 @@ typedef enum {
 
 /* A rotation of elements first .. first + dim - 1 of every head: at position
  * p, pair i = (a, b) becomes gain * (a cos(p f_i) - b sin(p f_i),
- * b cos(p f_i) + a sin(p f_i)); the other elements stay as they are. */
+ * b cos(p f_i) + a sin(p f_i)); the other elements stay as they are.
+ * With axes >= 2 (time, height and width of video; height and width of an image) a
+ * token has a position on each, q_pos is [n][axes], and pair i turns by the position on its own axis:
+ * behind the dim/2 frequencies freq then holds int32 [dim/2], the pairs' axes (a value outside
+ * 0 .. axes - 1 counts as axes - 1).  Tokens without q_pos sit at q_start + i on every axis. */
 typedef struct {
   const double* freq;  /* device [dim/2]: f_i in radians a position, 8-byte aligned */
   double gain;         /* factor on the rotated part */
   int32_t dim;         /* rotated elements of a head, even, first + dim <= d */
   int32_t first;
   int32_t layout;      /* hytopk_rotary_layout */
-  int32_t reserved;
+  int32_t axes;        /* 0 or 1: one position a token; up to 16 */
 } hytopk_rotary_plan;
 
 /* The frequencies and gain of a plan, computed on the host in 64 bits:
@@ -335,7 +341,7 @@ typedef struct {
 int hytopk_rotary_frequencies(int32_t dim, double base, int32_t scaling, double factor,
                               int64_t original, double* freq, double* gain);
 
-/* y = the rotation of x.  Token i sits at position q_pos[i] (device int32 [n])
+/* y = the rotation of x.  Token i sits at position q_pos[i] (device int32 [n], or [n][axes])
  * or, with q_pos NULL, q_start + i (below 2^31).  backward = 1 applies the transposed rotation
  * (gain included): the gradient with respect to x from the gradient with
  * respect to y.  Angles are formed and reduced in 64 bits and their rounding errors (exact to
@@ -392,6 +398,49 @@ int hytopk_cache_write(const hytopk_cache* c, int64_t n, const hytopk_rows* x,
  * code or a scale byte of 255 reads as NaN. */
 int hytopk_cache_read(const hytopk_cache* c, int64_t n, const int32_t* slots, int64_t start,
                       void* out, int32_t out_dtype, void* stream);
+
+/* A layer norm's parameters. */
+typedef struct {
+  const void* weight;  /* device [d], aligned to its element; NULL: ones */
+  const void* bias;    /* device [d]; NULL: zeros */
+  int32_t dtype;       /* hytopk_rows_dtype of both */
+  float eps;           /* added to the variance: finite, >= 0 */
+} hytopk_norm;
+
+/* Layer norm of rows x [n][heads][d], each (token, head) by itself over its d
+ * elements:
+ *   mean = sum x / d,  rstd = (sum (x - mean)^2 / d + eps)^(-1/2),
+ *   y = (x - mean) rstd weight + bias
+ * in fp32, rounded once to y's type.  The squares of a row's deviations must sum below 2^128; a
+ * constant row gives bias, or NaN with eps = 0.  A row that is not finite gives NaN in its own
+ * row alone.
+ * stats (fp32 [n][heads][2], 8-byte aligned, or NULL): mean and rstd, for the backward.
+ * save (or NULL): a checkpoint of x in 8 bits for the backward, taken from the same read: cache rows
+ * 0 .. n * heads - 1 of a FP8 or MXFP8 cache (heads 1, d as here, L >= n * heads), row i * heads + h
+ * quantised as hytopk_cache_write does; needs stats and finite x.
+ * y may be x itself (same data, strides and type); otherwise nothing that is written may overlap
+ * anything else (slices of one buffer with the same strides in bytes may lie between each other).
+ * d <= 8192 and n * heads < 2^31, or HYTOPK_EUNSUPPORTED. */
+int hytopk_layer_norm(const hytopk_norm* norm, int64_t n, int32_t heads, int32_t d, const hytopk_rows* x,
+                      const hytopk_rows* y, float* stats, const hytopk_cache* save, void* stream);
+
+/* Workspace bytes of hytopk_layer_norm_backward when dweight or dbias is asked for (0 on invalid input). */
+size_t hytopk_layer_norm_backward_workspace(int64_t n, int32_t heads, int32_t d);
+
+/* The gradients of hytopk_layer_norm from dy [n][heads][d], with stats as it gave them and
+ * h = (x - mean) rstd, g = dy weight:
+ *   dx = rstd (g - mean(g) - h mean(g h))   (means over the row)
+ *   dweight [d] = sum over rows of dy h,   dbias [d] = sum over rows of dy   (fp32)
+ * x is the forward's input (`x`, `saved` NULL) or its checkpoint (`saved`, `x` NULL), whose decoded rows
+ * then stand for x in h; mean and rstd are those of x itself.  Sums are fp32 in
+ * an order that depends on the sizes alone: results are bitwise reproducible.  dx, dweight and dbias may be
+ * NULL to skip them; dweight and dbias are fully written, the workspace (256-byte aligned) is required for
+ * either.  norm gives the weight (its bias and eps are not read).  dx may be dy or x itself; otherwise
+ * nothing that is written, the workspace included, may overlap anything else. */
+int hytopk_layer_norm_backward(const hytopk_norm* norm, int64_t n, int32_t heads, int32_t d, const hytopk_rows* dy,
+                               const hytopk_rows* x, const hytopk_cache* saved, const float* stats,
+                               const hytopk_rows* dx, float* dweight, float* dbias, void* workspace,
+                               size_t workspace_bytes, void* stream);
 
 /* Attention over selected entries: query i's `heads` heads attend to the keys
  * idx[i][0..k) of key head h / (heads / key_heads). */
@@ -452,7 +501,7 @@ const char* hytopk_last_error(void);  /* thread-local; "" when none */
  * by a pair of hipEvents recorded on the caller's stream, and the elapsed time
  * is accumulated per phase name ("sample_tau", "score_compact", "check",
  * "cand_select", "score_rows", "row_topk", "replay", "bwd_query", "bwd_dk", "rotary",
- * "cache_write", "cache_read", "attention_mass", "index_loss").  Process-wide; not for
+ * "cache_write", "cache_read", "layer_norm", "layer_norm_backward", "attention_mass", "index_loss").  Process-wide; not for
  * use with concurrent calls on different streams. */
 typedef struct {
   char name[32];

@@ -1,4 +1,4 @@
-"""CPU fp64 definitions of the operators around the selection: rotary
+"""CPU fp64 definitions of the operators around the selection: layer norm, rotary
 positions, the attention's mass at the selected entries, the indexer's loss.
 
 TEST INFRASTRUCTURE ONLY (see ``oracle.oracle``).  The storage formats'
@@ -8,7 +8,8 @@ from __future__ import annotations
 
 import numpy as np
 
-__all__ = ["rotary_frequencies", "rotary_plan", "rotary", "attention_probabilities", "attention_mass", "index_loss"]
+__all__ = ["rotary_frequencies", "rotary_plan", "rotary", "layer_norm", "layer_norm_backward",
+           "attention_probabilities", "attention_mass", "index_loss"]
 
 
 def rotary_frequencies(dim: int, base: float = 10000.0) -> np.ndarray:
@@ -41,13 +42,14 @@ def rotary_plan(dim: int, base: float = 10000.0, scaling: str = "none", factor: 
 
 
 def rotary(x: np.ndarray, pos: np.ndarray, freq: np.ndarray, *, first: int = 0,
-           layout: str = "half", gain: float = 1.0, backward: bool = False) -> np.ndarray:
+           layout: str = "half", gain: float = 1.0, backward: bool = False, axis=None) -> np.ndarray:
     """x [n][heads][d]: pair i = (a, b) of elements first .. first + dim - 1
     becomes gain * (a cos - b sin, b cos + a sin) at angle pos * freq[i];
-    backward applies the transpose."""
+    backward applies the transpose.  With ``axis`` [dim/2] pos is [n][axes] and pair i turns by its own axis' position."""
     half = len(freq)
+    pos = pos[:, axis] if axis is not None else pos[:, None]
     # the angle as turns in extended precision, so that far positions keep theirs
-    turns = pos.astype(np.longdouble)[:, None] * freq.astype(np.longdouble) / (2 * np.longdouble(np.pi)
+    turns = pos.astype(np.longdouble) * freq.astype(np.longdouble) / (2 * np.longdouble(np.pi)
                                                                                + np.longdouble(2.4492935982947064e-16))
     ang = ((turns - np.rint(turns)) * 2 * np.longdouble(np.pi)).astype(np.float64)
     c, s = gain * np.cos(ang)[:, None], gain * np.sin(ang)[:, None]
@@ -60,6 +62,23 @@ def rotary(x: np.ndarray, pos: np.ndarray, freq: np.ndarray, *, first: int = 0,
     y[..., ia] = a * c - b * s
     y[..., ib] = b * c + a * s
     return y
+
+
+def layer_norm(x, weight, bias, eps: float):
+    """Rows x [..., d] in fp64: (y, mean [...], rstd [...])."""
+    mean = x.mean(-1, keepdims=True)
+    rstd = 1.0 / np.sqrt(((x - mean) ** 2).mean(-1, keepdims=True) + eps)
+    return (x - mean) * rstd * weight + bias, mean[..., 0], rstd[..., 0]
+
+
+def layer_norm_backward(dy, x, mean, rstd, weight):
+    """(dx, dweight, dbias) of rows in fp64 with the statistics given: the derivative of sum(dy * y) where mean and rstd are
+    x's own."""
+    h = (x - mean[..., None]) * rstd[..., None]
+    g = dy * weight
+    dx = rstd[..., None] * (g - g.mean(-1, keepdims=True) - h * (g * h).mean(-1, keepdims=True))
+    rows = tuple(range(x.ndim - 1))
+    return dx, (dy * h).sum(rows), dy.sum(rows)
 
 
 def attention_probabilities(q, k, idx, scale: float, lse=None):
