@@ -1240,7 +1240,7 @@ size_t hytopk_layer_norm_backward_workspace(int64_t n, int32_t heads, int32_t d)
   size_t need = 0;
   guarded([&]() -> int {
     const int rc = check_norm_rows(n, heads, d);
-    if (rc == HYTOPK_OK) need = align_up((size_t)hk::norm_backward_blocks(n * heads, d) * 2 * d * sizeof(float));
+    if (rc == HYTOPK_OK) need = align_up((size_t)hk::norm_backward_blocks(n * heads, d) * 2 * hk::norm_columns(d) * sizeof(float));
     return rc;
   });
   return need;

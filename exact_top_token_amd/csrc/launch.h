@@ -342,7 +342,7 @@ struct NormBackArgs {
   int64_t dyts, dyhs, dxts, dxhs;
   const void* weight;  // [d], or null (1)
   const float2* stats;  // [rows]
-  float* part;         // [norm_backward_blocks][2][d], or null: no sums
+  float* part;         // [norm_backward_blocks][2][norm_columns(d)], or null: no sums
   int rows, heads;
 };
 
@@ -350,6 +350,8 @@ struct NormBackArgs {
 hipError_t launch_layer_norm_backward(const NormBackArgs& a, int d, bool weight32, int x_dtype, int codes, int dy_dtype,
                                       int dx_dtype, float* dweight, float* dbias, hipStream_t s);
 int norm_backward_blocks(int64_t rows, int d);
+// Columns of a workgroup's sums: d rounded up to whole 16 bytes.
+__host__ __device__ constexpr int norm_columns(int d) { return (d + 3) / 4 * 4; }
 
 // ---- attention mass at the selected entries, index loss (loss.hip)
 

@@ -9,8 +9,8 @@ namespace hk {
 
 namespace {
 
-constexpr int kNormThreads = 256;      // threads of a forward workgroup
-constexpr int kMaxBackThreads = 512;   // and at most of a backward one
+constexpr int kNormThreads = 256;  // threads of a forward workgroup
+constexpr int kBackThreads = 512;  // and of a backward one
 
 // Elements whose type is read from the arguments and which are accessed one by one: rows off
 // 16 bytes and widths that are no multiple of eight.
@@ -83,26 +83,29 @@ template <int CTRL>
 __device__ __forceinline__ float add_dpp(float x) {
   return x + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xf, 0xf, true));
 }
+// The sum with the lane 16 or 32 lanes away.
+__device__ __forceinline__ float add_16(float x) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+__device__ __forceinline__ float add_32(float x) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
 __device__ __forceinline__ float lanes_add(float x, int P) {
   if (P > 1) x = add_dpp<0xb1>(x);
   if (P > 2) x = add_dpp<0x4e>(x);
   if (P > 4) x = add_dpp<0x141>(x);
   if (P > 8) x = add_dpp<0x140>(x);
-  if (P > 16) {
-    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-  }
-  if (P > 32) {
-    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    x = __uint_as_float(b[0]) + __uint_as_float(b[1]);
-  }
+  if (P > 16) x = add_16(x);
+  if (P > 32) x = add_32(x);
   return x;
 }
 
 // Joins what the waves of a row hold (P > 64 threads a row; `flip` alternates between two
 // halves, so that one barrier a step is enough: the other half is read by waves still in the last step).
 template <typename Join>
-__device__ __forceinline__ float2 join_waves(float2 (*red)[kMaxBackThreads / kWave], int& flip, int P, float2 v, Join join) {
+__device__ __forceinline__ float2 join_waves(float2 (*red)[kBackThreads / kWave], int& flip, int P, float2 v, Join join) {
   float2* part = red[flip];
   flip ^= 1;
   if (lane_id() == 0) part[threadIdx.x >> 6] = v;
@@ -143,7 +146,7 @@ namespace {
 template <int IN, int OUT, int SAVE, int K>
 __global__ void __launch_bounds__(kNormThreads) layer_norm_kernel(NormArgs a, NormGrid g) {
 #pragma clang fp contract(off)  // every path (alignment, types, checkpoint) gives the same bits
-  __shared__ float2 red[2][kMaxBackThreads / kWave];
+  __shared__ float2 red[2][kBackThreads / kWave];
   const int d = g.d, P = 1 << g.log_p, RB = kNormThreads >> g.log_p;
   const int lr = threadIdx.x & (P - 1), rl = threadIdx.x >> g.log_p;
   const float inv_d = 1.0f / (float)d;
@@ -257,19 +260,18 @@ __global__ void __launch_bounds__(kNormThreads) layer_norm_kernel(NormArgs a, No
 
 // Threads and pieces a row of d elements: the fewest slots that hold it, on 16 threads or more (rows shorter
 // than that: one piece a thread), so that neighbouring threads read neighbouring pieces and the four
-// pieces of an MX block lie on neighbouring lanes; of equals the most threads of one wave, which need no barrier, else
-// the fewest.
+// pieces of an MX block lie on neighbouring lanes; of equals the most threads up to 1 << best_log_p, else the fewest.
 struct RowShape {
   int log_p, k;
 };
-RowShape row_shape(int d, int most_log_p, int most_k) {
+RowShape row_shape(int d, int most_log_p, int most_k, int best_log_p) {
   const int pieces = (d + 7) / 8;
   RowShape best{0, 0};
   for (int log_p = 0; log_p <= most_log_p; ++log_p)
     for (int k = 1; k <= most_k; ++k) {
       const int slots = k << log_p, had = best.k << best.log_p;
       if (slots < pieces || (log_p < 4 && k > 1)) continue;
-      if (best.k == 0 || slots < had || (slots == had && log_p <= 6)) best = RowShape{log_p, k};
+      if (best.k == 0 || slots < had || (slots == had && log_p <= best_log_p)) best = RowShape{log_p, k};
     }
   return best;
 }
@@ -313,7 +315,7 @@ hipError_t launch_layer_norm(const NormArgs& args, int d, bool weight32, int in_
     a.xts = a.xhs;
     a.yts = a.yhs;
   }
-  const RowShape shape = row_shape(d, 8, 4);
+  const RowShape shape = row_shape(d, 8, 4, 6);  // one wave where it fits: no barrier
   NormGrid g{};
   g.d = (uint32_t)d;
   g.log_p = (uint32_t)shape.log_p;
@@ -377,11 +379,11 @@ struct XPiece<kCodesMXFP8> : CodePiece<kMXFP8> {};
 // forward's, so both of a row's sums are formed at once; each row is read once and stays in registers, and a thread keeps the sums
 // of its columns over all its rows.
 template <int X, int DY, int DX, int K>
-__global__ void __launch_bounds__(kMaxBackThreads) layer_norm_backward_kernel(NormBackArgs a, NormBackGrid g) {
+__global__ void __launch_bounds__(kBackThreads) layer_norm_backward_kernel(NormBackArgs a, NormBackGrid g) {
 #pragma clang fp contract(off)  // as forward
-  __shared__ float2 red[2][kMaxBackThreads / kWave];
-  __shared__ float cols[kMaxBackThreads / kWave][kWave * 8];
-  const int d = g.d, P = 1 << g.log_p, threads = max(kNormThreads, P), RB = threads >> g.log_p;
+  __shared__ float2 red[2][kBackThreads / kWave];
+  __shared__ float cols[kBackThreads / kWave][kWave * 8];
+  const int d = g.d, P = 1 << g.log_p, RB = kBackThreads >> g.log_p;
   const int lr = threadIdx.x & (P - 1), rl = threadIdx.x >> g.log_p;
   const float inv_d = 1.0f / (float)d;
   auto count = [&](int k) { return min(max(d - 8 * (lr + k * P), 0), 8); };
@@ -463,7 +465,8 @@ __global__ void __launch_bounds__(kMaxBackThreads) layer_norm_backward_kernel(No
   }
   if (!a.part) return;
   // The columns' sums over the workgroup's row groups: over the wave's lanes, then over the waves.
-  float* to = a.part + (int64_t)blockIdx.x * 2 * d;
+  const int dp = norm_columns(d);
+  float* to = a.part + (int64_t)blockIdx.x * 2 * dp;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
 #pragma unroll
@@ -473,10 +476,13 @@ __global__ void __launch_bounds__(kMaxBackThreads) layer_norm_backward_kernel(No
 #pragma unroll
         for (int i = 0; i < 8; ++i) c[i] += __shfl_xor(c[i], off);
       const int e0 = 8 * (lr + k * P);
-      if (P >= threads) {  // one row at a time: nothing to join
+      auto store = [&] {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (e0 + i < d) to[side * d + e0 + i] = c[i];
+        for (int i = 0; i < 8; i += 4)
+          if (e0 + i < dp) *reinterpret_cast<f32x4*>(to + side * dp + e0 + i) = f32x4{c[i], c[i + 1], c[i + 2], c[i + 3]};
+      };
+      if (P == kBackThreads) {  // one row at a time: nothing to join
+        store();
         continue;
       }
       __syncthreads();  // the last piece's sums are read
@@ -485,34 +491,61 @@ __global__ void __launch_bounds__(kMaxBackThreads) layer_norm_backward_kernel(No
       __syncthreads();
       if (rl != 0) continue;
       const int step = max(P / kWave, 1);  // waves of a row group
-      for (int wv = (threadIdx.x >> 6) + step; wv < threads / kWave; wv += step)
+      for (int wv = (threadIdx.x >> 6) + step; wv < kBackThreads / kWave; wv += step)
 #pragma unroll
         for (int i = 0; i < 8; ++i) c[i] += cols[wv][i * kWave + lane_id()];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (e0 + i < d) to[side * d + e0 + i] = c[i];
+      store();
     }
   }
 }
 
-// The sums of the workgroups' columns, [blocks][2 d], in a fixed order: 16 columns a workgroup, 16 threads a column.
-__global__ void __launch_bounds__(256) norm_columns_kernel(const float* part, float* dw, float* db, int d, int blocks) {
-  __shared__ float sums[16][17];
-  const int c = threadIdx.x & 15, r = threadIdx.x >> 4, col = blockIdx.x * 16 + c;
-  float s = 0.0f;
-  if (col < 2 * d)
-    for (int b = r; b < blocks; b += 16) s += part[(int64_t)b * 2 * d + col];
-  sums[r][c] = s;
+// The sums of the workgroups' columns, [blocks][2][dp], in a fixed order: Q threads of a workgroup take four columns each,
+// its other threads further rows, so that all loads of a thread are under way together.
+constexpr int kColumnThreads = 1024;
+template <int Q>
+__global__ void __launch_bounds__(kColumnThreads) norm_columns_kernel(const float* part, float* dw, float* db, int d, int blocks) {
+  constexpr int kRows = kColumnThreads / Q, kWaves = kColumnThreads / kWave;
+  __shared__ f32x4 sums[kWaves][Q];
+  const int dp = norm_columns(d);
+  const int c = threadIdx.x % Q, r = threadIdx.x / Q, col = (blockIdx.x * Q + c) * 4;
+  f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (col < 2 * dp) {
+    constexpr int kFlight = 512 / kRows;
+    const float* p = part + col;
+    for (int b0 = r; b0 < blocks; b0 += kFlight * kRows) {
+      f32x4 v[kFlight];
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i) {
+        v[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (b0 + i * kRows < blocks) v[i] = *reinterpret_cast<const f32x4*>(p + (int64_t)(b0 + i * kRows) * 2 * dp);
+      }
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i) s += v[i];
+    }
+  }
+  // over the rows of a wave, then over the waves
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (Q < 8) s[i] += __shfl_xor(s[i], 4);
+    if (Q < 16) s[i] += __shfl_xor(s[i], 8);
+    s[i] = add_32(add_16(s[i]));
+  }
+  if (lane_id() < Q) sums[threadIdx.x / kWave][c] = s;
   __syncthreads();
-  if (r != 0 || col >= 2 * d) return;
-  for (int i = 1; i < 16; ++i) s += sums[i][c];
-  float* to = col < d ? dw : db;
-  if (to) to[col < d ? col : col - d] = s;
+  if (r != 0 || col >= 2 * dp) return;
+  s = sums[0][c];
+  for (int i = 1; i < kWaves; ++i) s += sums[i][c];
+  float* to = col < dp ? dw : db;
+  const int e0 = col < dp ? col : col - dp;
+  if (!to) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (e0 + i < d) to[e0 + i] = s[i];
 }
 
 template <int X, int DY, int DX>
 hipError_t backward_k(const NormBackArgs& a, const NormBackGrid& g, int k, hipStream_t s) {
-  const dim3 grid(g.blocks), block((unsigned)std::max(kNormThreads, 1 << g.log_p));
+  const dim3 grid(g.blocks), block(kBackThreads);
   switch (k) {
     case 1: hipLaunchKernelGGL((layer_norm_backward_kernel<X, DY, DX, 1>), grid, block, 0, s, a, g); break;
     case 2: hipLaunchKernelGGL((layer_norm_backward_kernel<X, DY, DX, 2>), grid, block, 0, s, a, g); break;
@@ -532,13 +565,13 @@ hipError_t backward_io(const NormBackArgs& a, const NormBackGrid& g, int k, int 
                          : backward_k<X, kRowsFP32, kRowsFP32>(a, g, k, s);
 }
 
-RowShape back_shape(int d) { return row_shape(d, 9, 3); }
+RowShape back_shape(int d) { return row_shape(d, 9, 3, 9); }
 
 }  // namespace
 
 int norm_backward_blocks(int64_t rows, int d) {
-  const int64_t rb = std::max(kNormThreads, 1 << back_shape(d).log_p) >> back_shape(d).log_p;
-  return (int)std::min<int64_t>((rows + rb - 1) / rb, 1024);
+  const int64_t rb = kBackThreads >> back_shape(d).log_p;
+  return (int)std::min<int64_t>((rows + rb - 1) / rb, back_shape(d).k == 1 ? 512 : 256);
 }
 
 hipError_t launch_layer_norm_backward(const NormBackArgs& args, int d, bool weight32, int x_dtype, int codes, int dy_dtype,
@@ -587,8 +620,12 @@ hipError_t launch_layer_norm_backward(const NormBackArgs& args, int d, bool weig
     if (e != hipSuccess) return e;
   }
   if (!dweight && !dbias) return hipSuccess;
-  hipLaunchKernelGGL(norm_columns_kernel, dim3((unsigned)(2 * d + 15) / 16), dim3(256), 0, s, a.part, dweight, dbias, d,
-                     blocks);
+  // 256 contiguous bytes a row where that leaves 32 workgroups or more, else 64
+  const int quads = norm_columns(d) / 2;
+  if (quads >= 512)
+    hipLaunchKernelGGL((norm_columns_kernel<16>), dim3((quads + 15) / 16), dim3(kColumnThreads), 0, s, a.part, dweight, dbias, d, blocks);
+  else
+    hipLaunchKernelGGL((norm_columns_kernel<4>), dim3((quads + 3) / 4), dim3(kColumnThreads), 0, s, a.part, dweight, dbias, d, blocks);
   return hipGetLastError();
 }
 
