@@ -47,7 +47,8 @@ struct Piece<kAny> {
   }
 };
 
-template <int T>
+// PAST: not kept in the caches.
+template <int T, bool PAST>
 __device__ __forceinline__ void put(void* base, int64_t at, int e, bool fp32, const float* v) {
   if constexpr (T == kAny) {
 #pragma unroll
@@ -57,33 +58,54 @@ __device__ __forceinline__ void put(void* base, int64_t at, int e, bool fp32, co
       else store1<kRowsBF16>(base, at + i, v[i]);
     }
   } else {
-    store8<T>(base, at, v);
+    store8<T, PAST>(base, at, v);
   }
 }
 
-// `e` elements of a weight or bias from element `at`, or `other` without one; `whole`: all eight, 16-byte aligned.
-__device__ __forceinline__ void parameters(const void* p, bool fp32, bool whole, int at, int e, float other, float* v) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = other;
-  if (!p || e == 0) return;
-  if (whole) {
-    if (fp32) load8<kRowsFP32, true>(p, at, v);
-    else load8<kRowsBF16, true>(p, at, v);
-    return;
-  }
-  for (int i = 0; i < e; ++i) {
-    const float x = fp32 ? load1<kRowsFP32>(p, at + i) : load1<kRowsBF16>(p, at + i);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j == i ? x : v[j];
-  }
+template <bool PAST>
+__device__ __forceinline__ void put_codes(uint8_t* to, const u32x2& c) {
+  if constexpr (PAST) __builtin_nontemporal_store(c, reinterpret_cast<u32x2*>(to));
+  else *reinterpret_cast<u32x2*>(to) = c;
 }
 
-// The sum over groups of P neighbouring lanes (a power of two up to 64), in each of them.
+// Eight elements of a weight or bias from element `at`, of which `e` exist, or `other` without one.  WHOLE: pieces of
+// eight, 16-byte aligned; loaded first and read later, so that loads of several are under way together.
+template <bool WHOLE>
+struct Parameters {
+  u32x4 w[2];
+  __device__ __forceinline__ void load(const void* p, bool fp32, int at, int e) {
+    w[0] = w[1] = u32x4{0u, 0u, 0u, 0u};
+    if (!p || e == 0) return;
+    if constexpr (WHOLE) {
+      const char* c = static_cast<const char*>(p) + (int64_t)at * (fp32 ? 4 : 2);
+      w[0] = *reinterpret_cast<const u32x4*>(c);
+      if (fp32) w[1] = *reinterpret_cast<const u32x4*>(c + 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < e) w[i >> 2][i & 3] = __float_as_uint(fp32 ? load1<kRowsFP32>(p, at + i) : load1<kRowsBF16>(p, at + i));
+    }
+  }
+  __device__ __forceinline__ void floats(const void* p, bool fp32, float other, float* v) const {
+    if (!p) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = other;
+    } else if (WHOLE && !fp32) {
+      unpack_bf16(w[0], v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i >> 2][i & 3]);
+    }
+  }
+};
+
+// The sum over groups of 1 << log_p neighbouring lanes (at most 64), in each of them: halves, then rows of 16, halves of
+// rows (mirrored) and quads by lane permutations inside the vector instruction.
 template <int CTRL>
 __device__ __forceinline__ float add_dpp(float x) {
   return x + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xf, 0xf, true));
 }
-// The sum with the lane 16 or 32 lanes away.
+// With the lane 16 or 32 lanes away.
 __device__ __forceinline__ float add_16(float x) {
   const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return __uint_as_float(a[0]) + __uint_as_float(a[1]);
@@ -92,14 +114,21 @@ __device__ __forceinline__ float add_32(float x) {
   const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
-__device__ __forceinline__ float lanes_add(float x, int P) {
-  if (P > 1) x = add_dpp<0xb1>(x);
-  if (P > 2) x = add_dpp<0x4e>(x);
-  if (P > 4) x = add_dpp<0x141>(x);
-  if (P > 8) x = add_dpp<0x140>(x);
-  if (P > 16) x = add_16(x);
-  if (P > 32) x = add_32(x);
-  return x;
+template <int N>
+__device__ __forceinline__ void lanes_add(float (&x)[N], int log_p) {
+  auto each = [&](auto step) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = step(x[i]);
+  };
+  switch (log_p) {
+    default: each(add_32); [[fallthrough]];
+    case 5: each(add_16); [[fallthrough]];
+    case 4: each(add_dpp<0x140>); [[fallthrough]];
+    case 3: each(add_dpp<0x141>); [[fallthrough]];
+    case 2: each(add_dpp<0x4e>); [[fallthrough]];
+    case 1: each(add_dpp<0xb1>); [[fallthrough]];
+    case 0: break;
+  }
 }
 
 // Joins what the waves of a row hold (P > 64 threads a row; `flip` alternates between two
@@ -116,11 +145,32 @@ __device__ __forceinline__ float2 join_waves(float2 (*red)[kBackThreads / kWave]
   return v;
 }
 
+// Waits for the loads under way.  Stores count like loads, and the compiler would wait for a row's at the end of its
+// round, where the next row's elements change registers; called before them, it waits only for the last round's.
+__device__ __forceinline__ void loads_done() { __builtin_amdgcn_s_waitcnt(0x0f70); }  // vmcnt(0)
+
 // 1 / sqrt(v) within 2^-23; the instruction takes subnormal arguments as 0.
 __device__ __forceinline__ float inverse_root(float v) {
   const bool low = v < 0x1p-96f;
   return __builtin_amdgcn_rsqf(low ? v * 0x1p96f : v) * (low ? 0x1p48f : 1.0f);
 }
+
+// A thread's place in rows `ts` and `hs` apart: of the row's elements from `e` on, `step` further each round where
+// rows are one axis (one head).
+struct Walk {
+  int64_t at, step;
+  __device__ __forceinline__ Walk(unsigned row, int heads, int64_t ts, int64_t hs, int rows, int e) : step(rows * ts) {
+    at = place(row, heads, ts, hs) + e;
+  }
+  __device__ __forceinline__ void next(unsigned row, int heads, int64_t ts, int64_t hs, int e) {
+    at = heads == 1 ? at + step : place(row, heads, ts, hs) + e;
+  }
+  static __device__ __forceinline__ int64_t place(unsigned row, int heads, int64_t ts, int64_t hs) {
+    if (heads == 1) return row * ts;
+    const unsigned t = row / (unsigned)heads;
+    return t * ts + (row - t * (unsigned)heads) * hs;
+  }
+};
 
 }  // namespace
 
@@ -130,8 +180,7 @@ struct NormGrid {
   uint32_t d : 14;      // at most 8,192
   uint32_t log_p : 4;
   uint32_t rounds : 11;  // times threads / P rows of a workgroup
-  uint32_t fp32 : 1;     // weight and bias; whether both can be read 16 bytes at a time
-  uint32_t whole : 1;
+  uint32_t fp32 : 1;     // weight and bias
   uint32_t x32 : 1;      // x, y (rows accessed one element at a time)
   uint32_t y32 : 1;
 };
@@ -143,71 +192,83 @@ namespace {
 // first sum gives m0, the mean but for that sum's rounding; the sums of x - m0 and its square then give the rest of
 // the mean and the variance about m0, less that rest's square, so neither an offset of the row nor its sum's
 // rounding reaches the deviations.  SAVE: the row is also quantised as a cache row of its own.
-template <int IN, int OUT, int SAVE, int K>
+template <int IN, int OUT, int SAVE, int K, bool PAST>
 __global__ void __launch_bounds__(kNormThreads) layer_norm_kernel(NormArgs a, NormGrid g) {
 #pragma clang fp contract(off)  // every path (alignment, types, checkpoint) gives the same bits
   __shared__ float2 red[2][kBackThreads / kWave];
   const int d = g.d, P = 1 << g.log_p, RB = kNormThreads >> g.log_p;
   const int lr = threadIdx.x & (P - 1), rl = threadIdx.x >> g.log_p;
   const float inv_d = 1.0f / (float)d;
-  auto count = [&](int k) { return min(max(d - 8 * (lr + k * P), 0), 8); };  // elements of the thread's k-th piece
-  float w[K][8], b[K][8];
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    parameters(a.weight, g.fp32, g.whole, 8 * (lr + k * P), count(k), 1.0f, w[k]);
-    parameters(a.bias, g.fp32, g.whole, 8 * (lr + k * P), count(k), 0.0f, b[k]);
-  }
-  const int64_t row0 = (int64_t)blockIdx.x * RB * g.rounds + rl;
-  // The token and head of a row (one head: rows `ts` apart).
-  auto place = [&](int64_t row, int64_t ts, int64_t hs) {
-    if (a.heads == 1) return row * ts;
-    const unsigned t = (unsigned)row / (unsigned)a.heads;
-    return (int64_t)t * ts + (int64_t)((unsigned)row - t * (unsigned)a.heads) * hs;
-  };
+  // elements of the thread's k-th piece: all but the last pieces are whole
+  const int last = min(max(d - 8 * (lr + (K - 1) * P), 0), 8);
+  auto count = [&](int k) { return k < K - 1 ? 8 : last; };
+  const unsigned rows = a.rows;
+  unsigned row = blockIdx.x * (RB * g.rounds) + rl;
+  Walk from(row, a.heads, a.xts, a.xhs, RB, 8 * lr), to(row, a.heads, a.yts, a.yhs, RB, 8 * lr);
   Piece<IN> raw[K];  // the next row's elements, under way while this one is worked on
-  auto fetch = [&](int64_t row) {
-    const int64_t at = row < a.rows ? place(row, a.xts, a.xhs) : 0;
+  auto fetch = [&](unsigned at_row) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       raw[k].zero();
-      if (row < a.rows && count(k) > 0) raw[k].load(a.x, at + 8 * (lr + k * P), count(k), g.x32);
+      if (at_row < rows && count(k) > 0) raw[k].load(a.x, from.at + 8 * k * P, count(k), g.x32);
     }
   };
-  fetch(row0);
+  fetch(row);
+  float w[K][8], b[K][8];
+  {
+    Parameters<IN != kAny> pw[K], pb[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      pw[k].load(a.weight, g.fp32, 8 * (lr + k * P), count(k));
+      pb[k].load(a.bias, g.fp32, 8 * (lr + k * P), count(k));
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      pw[k].floats(a.weight, g.fp32, 1.0f, w[k]);
+      pb[k].floats(a.bias, g.fp32, 0.0f, b[k]);
+    }
+  }
   int flip = 0;
-  for (int r = 0; r < (int)g.rounds; ++r) {
-    const int64_t row = row0 + (int64_t)r * RB;
-    if (row - rl >= a.rows) break;  // the whole workgroup
+  // `left` rows of this round's first row on, the same in the whole workgroup
+  int left = (int)(rows - (row - rl));
+  for (int r = 0; r < (int)g.rounds && left > 0; ++r, left -= RB) {
     float v[K][8];
 #pragma unroll
     for (int k = 0; k < K; ++k) raw[k].floats(v[k]);
-    if (r + 1 < (int)g.rounds) fetch(row + RB);
+    const unsigned now = row;
+    row += RB;
+    if (r + 1 < (int)g.rounds) {
+      from.next(row, a.heads, a.xts, a.xhs, 8 * lr);
+      fetch(row);
+    }
 
-    float sum = 0.0f, top = 0.0f;
+    float sum[1] = {0.0f}, top = 0.0f;
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int k = 0; k < K; ++k) {
+      sum[0] += ((v[k][0] + v[k][1]) + (v[k][2] + v[k][3])) + ((v[k][4] + v[k][5]) + (v[k][6] + v[k][7]));
+      if constexpr (SAVE == kFP8) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        sum += v[k][i];
-        if constexpr (SAVE == kFP8) top = fmaxf(top, fabsf(v[k][i]));
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[k][i]));
       }
-    sum = lanes_add(sum, P);
+    }
+    lanes_add(sum, g.log_p);
     if constexpr (SAVE == kFP8) top = lanes_max(top, P);
     if (P > kWave) {
-      const float2 s = join_waves(red, flip, P, make_float2(sum, top),
+      const float2 s = join_waves(red, flip, P, make_float2(sum[0], top),
                                   [](float2 x, float2 y) { return make_float2(x.x + y.x, fmaxf(x.y, y.y)); });
-      sum = s.x;
+      sum[0] = s.x;
       top = s.y;
     }
-    const float m0 = sum * inv_d;
+    const float m0 = sum[0] * inv_d;
+    const int64_t code0 = (int64_t)now * d + 8 * lr;
     if constexpr (SAVE == kFP8) {
-      const float scale = top > 0.0f ? fmaxf(top / 448.0f, 0x1p-126f) : 1.0f, inv = 1.0f / scale;
-      if (row < a.rows && lr == 0) static_cast<float*>(a.scale)[row] = scale;
+      const Reciprocal by(e4m3_scale(top));
+      if (now < rows && lr == 0) static_cast<float*>(a.scale)[now] = by.scale;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (row >= a.rows || count(k) == 0) continue;
-        const u32x2 c = {e4m3x4_quotient(v[k], scale, inv), e4m3x4_quotient(v[k] + 4, scale, inv)};
-        *reinterpret_cast<u32x2*>(a.codes + row * d + 8 * (lr + k * P)) = c;
+        if (now >= rows || count(k) == 0) continue;
+        const u32x2 c = {e4m3x4_quotient(v[k], by), e4m3x4_quotient(v[k] + 4, by)};
+        put_codes<PAST>(a.codes + code0 + 8 * k * P, c);
       }
     } else if constexpr (SAVE == kMXFP8) {
 #pragma unroll
@@ -216,45 +277,46 @@ __global__ void __launch_bounds__(kNormThreads) layer_norm_kernel(NormArgs a, No
 #pragma unroll
         for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[k][i]));
         const int e = mx_exponent<kMXFP8>(quad_max(m));  // the four lanes of a block
-        if (row >= a.rows || count(k) == 0) continue;
-        const int64_t at = row * d + 8 * (lr + k * P);
+        if (now >= rows || count(k) == 0) continue;
+        const int64_t at = code0 + 8 * k * P;
         if ((lr & 3) == 0) static_cast<uint8_t*>(a.scale)[at >> 5] = (uint8_t)(e + 127);
-        *reinterpret_cast<u32x2*>(a.codes + at) = mx_e4m3x8(v[k], e);
+        put_codes<PAST>(a.codes + at, mx_e4m3x8(v[k], e));
       }
     }
 
-    float s1 = 0.0f, s2 = 0.0f;
+    float s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int n = count(k);
+      // elements that do not exist were read as 0 and keep it
+      const float m = count(k) > 0 ? m0 : 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float c = i < (IN == kAny ? n : 8 * min(n, 1)) ? v[k][i] - m0 : 0.0f;
-        v[k][i] = c;
-        s1 += c;
-        s2 = fmaf(c, c, s2);
+        v[k][i] -= IN == kAny && i >= count(k) ? 0.0f : m;
+        s[0] += v[k][i];
+        s[1] = fmaf(v[k][i], v[k][i], s[1]);
       }
     }
-    s1 = lanes_add(s1, P);
-    s2 = lanes_add(s2, P);
+    lanes_add(s, g.log_p);
     if (P > kWave) {
-      const float2 s = join_waves(red, flip, P, make_float2(s1, s2),
+      const float2 j = join_waves(red, flip, P, make_float2(s[0], s[1]),
                                   [](float2 x, float2 y) { return make_float2(x.x + y.x, x.y + y.y); });
-      s1 = s.x;
-      s2 = s.y;
+      s[0] = j.x;
+      s[1] = j.y;
     }
-    const float rest = s1 * inv_d, var = fmaf(-rest, rest, s2 * inv_d);
-    const float rstd = inverse_root(fmaxf(var, 0.0f) + a.eps);
-    if (row >= a.rows) continue;
-    if (a.stats && lr == 0) a.stats[row] = make_float2(m0 + rest, rstd);
-    const int64_t at = place(row, a.yts, a.yhs);
+    const float rest = s[0] * inv_d, var = fmaf(-rest, rest, s[1] * inv_d);
+    const float rstd = inverse_root(fmaxf(var, 0.0f) + a.eps), off = -rest * rstd;
+    loads_done();
+    if (now < rows) {
+      if (a.stats && lr == 0) a.stats[now] = make_float2(m0 + rest, rstd);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if (count(k) == 0) continue;
+      for (int k = 0; k < K; ++k) {
+        if (count(k) == 0) continue;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[k][i] = fmaf((v[k][i] - rest) * rstd, w[k][i], b[k][i]);
-      put<OUT>(a.y, at + 8 * (lr + k * P), count(k), g.y32, v[k]);
+        for (int i = 0; i < 8; ++i) v[k][i] = fmaf(fmaf(v[k][i], rstd, off), w[k][i], b[k][i]);
+        put<OUT, PAST>(a.y, to.at + 8 * k * P, count(k), g.y32, v[k]);
+      }
     }
+    if (r + 1 < (int)g.rounds) to.next(row, a.heads, a.yts, a.yhs, 8 * lr);
   }
 }
 
@@ -276,22 +338,32 @@ RowShape row_shape(int d, int most_log_p, int most_k, int best_log_p) {
   return best;
 }
 
-template <int IN, int OUT, int SAVE>
-hipError_t layer_norm_k(const NormArgs& a, NormGrid g, int k, hipStream_t s) {
-  const int64_t rb = kNormThreads >> g.log_p;
-  int64_t rounds = 1;
-  while (rounds < 4 && a.rows / (rb * 2 * rounds) >= 2048) rounds *= 2;
-  rounds = std::max(rounds, (a.rows / rb + kMostBlocks) / kMostBlocks);
+// Results larger than the chip's L2 caches (32 MiB) go past them: the forward of 8,192 x 4,096 23.0 us against 28.8, the
+// backward of 131,072 x 128 21.9 against 25.5.  Rows off 16 bytes do not.
+bool past_caches(int64_t rows, int d, int dtype) { return rows * d * rows_bytes(dtype) >= int64_t(32) << 20; }
+
+template <int IN, int OUT, int SAVE, bool PAST>
+hipError_t layer_norm_past(const NormArgs& a, NormGrid g, int k, hipStream_t s) {
+  const int64_t rb = kNormThreads >> g.log_p, sets = (a.rows + rb - 1) / rb;
+  const int64_t rounds = std::max(std::min<int64_t>((sets + 2047) / 2048, 8), (sets + kMostBlocks - 1) / kMostBlocks);
   g.rounds = (uint32_t)rounds;
-  const dim3 grid((unsigned)((a.rows + rb * rounds - 1) / (rb * rounds))), block(kNormThreads);
+  const dim3 grid((unsigned)((sets + rounds - 1) / rounds)), block(kNormThreads);
   switch (k) {
-    case 1: hipLaunchKernelGGL((layer_norm_kernel<IN, OUT, SAVE, 1>), grid, block, 0, s, a, g); break;
-    case 2: hipLaunchKernelGGL((layer_norm_kernel<IN, OUT, SAVE, 2>), grid, block, 0, s, a, g); break;
-    case 3: hipLaunchKernelGGL((layer_norm_kernel<IN, OUT, SAVE, 3>), grid, block, 0, s, a, g); break;
-    case 4: hipLaunchKernelGGL((layer_norm_kernel<IN, OUT, SAVE, 4>), grid, block, 0, s, a, g); break;
+    case 1: hipLaunchKernelGGL((layer_norm_kernel<IN, OUT, SAVE, 1, PAST>), grid, block, 0, s, a, g); break;
+    case 2: hipLaunchKernelGGL((layer_norm_kernel<IN, OUT, SAVE, 2, PAST>), grid, block, 0, s, a, g); break;
+    case 3: hipLaunchKernelGGL((layer_norm_kernel<IN, OUT, SAVE, 3, PAST>), grid, block, 0, s, a, g); break;
+    case 4: hipLaunchKernelGGL((layer_norm_kernel<IN, OUT, SAVE, 4, PAST>), grid, block, 0, s, a, g); break;
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();
+}
+
+template <int IN, int OUT, int SAVE>
+hipError_t layer_norm_k(const NormArgs& a, const NormGrid& g, int k, hipStream_t s) {
+  if constexpr (OUT != kAny) {
+    if (past_caches(a.rows, (int)g.d, OUT)) return layer_norm_past<IN, OUT, SAVE, true>(a, g, k, s);
+  }
+  return layer_norm_past<IN, OUT, SAVE, false>(a, g, k, s);
 }
 
 template <int IN, int OUT>
@@ -315,17 +387,19 @@ hipError_t launch_layer_norm(const NormArgs& args, int d, bool weight32, int in_
     a.xts = a.xhs;
     a.yts = a.yhs;
   }
-  const RowShape shape = row_shape(d, 8, 4, 6);  // one wave where it fits: no barrier
+  // of equals two pieces a thread for rows of several waves (with one and two 13.2 and 12.2 us of 8,192 x 2,048, with four and
+  // two 25.2 and 23.0 of 8,192 x 4,096)
+  const RowShape shape = row_shape(d, 8, 4, d > 2048 ? 8 : d > 1024 ? 7 : 6);
   NormGrid g{};
   g.d = (uint32_t)d;
   g.log_p = (uint32_t)shape.log_p;
   g.fp32 = weight32;
-  g.whole = d % 8 == 0 && aligned16(a.weight, 0, 0, kRowsBF16) && aligned16(a.bias, 0, 0, kRowsBF16);
   g.x32 = in_dtype == kRowsFP32;
   g.y32 = out_dtype == kRowsFP32;
   const int64_t xhs = a.heads == 1 ? 0 : a.xhs, yhs = a.heads == 1 ? 0 : a.yhs;
   const int64_t xts = a.rows == a.heads ? 0 : a.xts, yts = a.rows == a.heads ? 0 : a.yts;  // one token: no stride
-  if (d % 8 || !aligned16(a.x, xts, xhs, in_dtype) || !aligned16(a.y, yts, yhs, out_dtype))
+  auto whole = [](const void* p) { return aligned16(p, 0, 0, kRowsBF16); };
+  if (d % 8 || !aligned16(a.x, xts, xhs, in_dtype) || !aligned16(a.y, yts, yhs, out_dtype) || !whole(a.weight) || !whole(a.bias))
     return layer_norm_save<kAny, kAny>(a, g, shape.k, save, s);
   if (in_dtype == kRowsBF16) {
     return out_dtype == kRowsBF16 ? layer_norm_save<kRowsBF16, kRowsBF16>(a, g, shape.k, save, s)
@@ -340,8 +414,7 @@ hipError_t launch_layer_norm(const NormArgs& args, int d, bool weight32, int in_
 struct NormBackGrid {
   uint32_t d : 14;
   uint32_t log_p : 4;
-  uint32_t fp32 : 1;  // weight; whether it can be read 16 bytes at a time
-  uint32_t whole : 1;
+  uint32_t fp32 : 1;  // weight
   uint32_t x32 : 1;   // rows accessed one element at a time
   uint32_t dy32 : 1;
   uint32_t dx32 : 1;
@@ -355,8 +428,8 @@ template <int X>
 struct XPiece {
   Piece<X> raw;
   __device__ __forceinline__ void zero() { raw.zero(); }
-  __device__ __forceinline__ void load(const NormBackArgs& a, int64_t, int64_t at, int, int e0, int e, bool fp32) {
-    raw.load(a.x, at + e0, e, fp32);
+  __device__ __forceinline__ void load(const NormBackArgs& a, int64_t, int64_t at, int e, bool fp32) {
+    raw.load(a.x, at, e, fp32);
   }
   __device__ __forceinline__ void floats(float* v) const { raw.floats(v); }
 };
@@ -364,8 +437,8 @@ template <int FMT>
 struct CodePiece {
   Stored8<FMT> raw;
   __device__ __forceinline__ void zero() { raw = Stored8<FMT>{}; }
-  __device__ __forceinline__ void load(const NormBackArgs& a, int64_t row, int64_t, int d, int e0, int, bool) {
-    raw.load(static_cast<const uint8_t*>(a.x), a.scale, row, row * d + e0);
+  __device__ __forceinline__ void load(const NormBackArgs& a, int64_t row, int64_t at, int, bool) {
+    raw.load(static_cast<const uint8_t*>(a.x), a.scale, row, at);
   }
   __device__ __forceinline__ void floats(float* v) const { raw.decode(v); }
 };
@@ -378,7 +451,7 @@ struct XPiece<kCodesMXFP8> : CodePiece<kMXFP8> {};
 // workgroup's sums over its rows of dy h and dy, [2][d] behind those of the ones before it.  Statistics are the
 // forward's, so both of a row's sums are formed at once; each row is read once and stays in registers, and a thread keeps the sums
 // of its columns over all its rows.
-template <int X, int DY, int DX, int K>
+template <int X, int DY, int DX, int K, bool PAST>
 __global__ void __launch_bounds__(kBackThreads) layer_norm_backward_kernel(NormBackArgs a, NormBackGrid g) {
 #pragma clang fp contract(off)  // as forward
   __shared__ float2 red[2][kBackThreads / kWave];
@@ -386,42 +459,49 @@ __global__ void __launch_bounds__(kBackThreads) layer_norm_backward_kernel(NormB
   const int d = g.d, P = 1 << g.log_p, RB = kBackThreads >> g.log_p;
   const int lr = threadIdx.x & (P - 1), rl = threadIdx.x >> g.log_p;
   const float inv_d = 1.0f / (float)d;
-  auto count = [&](int k) { return min(max(d - 8 * (lr + k * P), 0), 8); };
+  const int last = min(max(d - 8 * (lr + (K - 1) * P), 0), 8);
+  auto count = [&](int k) { return k < K - 1 ? 8 : last; };
   float w[K][8], dw[K][8], db[K][8];
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    parameters(a.weight, g.fp32, g.whole, 8 * (lr + k * P), count(k), 1.0f, w[k]);
+  for (int k = 0; k < K; ++k)
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[k][i] = db[k][i] = 0.0f;
-  }
-  auto place = [&](int64_t row, int64_t ts, int64_t hs) {
-    if (a.heads == 1) return row * ts;
-    const unsigned t = (unsigned)row / (unsigned)a.heads;
-    return (int64_t)t * ts + (int64_t)((unsigned)row - t * (unsigned)a.heads) * hs;
-  };
+  const unsigned rows = a.rows;
+  const int step = (int)g.blocks * RB;
+  unsigned row = blockIdx.x * RB + rl;
+  const bool coded = X >= kCodesFP8;
+  // a checkpoint's rows are one axis
+  const int xheads = coded ? 1 : a.heads;
+  const int64_t xts = coded ? d : a.xts, xhs = coded ? 0 : a.xhs;
+  Walk from(row, xheads, xts, xhs, step, 8 * lr), up(row, a.heads, a.dyts, a.dyhs, step, 8 * lr);
+  Walk to(row, a.heads, a.dxts, a.dxhs, step, 8 * lr);
   XPiece<X> xr[K];  // the next row's elements and statistics, under way while this one is worked on
   Piece<DY> yr[K];
   float2 stats;
-  auto fetch = [&](int64_t row) {
-    const bool have = row < a.rows;
-    const int64_t ya = have ? place(row, a.dyts, a.dyhs) : 0;
-    const int64_t xa = have && X < kCodesFP8 ? place(row, a.xts, a.xhs) : 0;
+  auto fetch = [&](unsigned at_row) {
+    const bool have = at_row < rows;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       xr[k].zero();
       yr[k].zero();
-      const int e0 = 8 * (lr + k * P);
       if (have && count(k) > 0) {
-        yr[k].load(a.dy, ya + e0, count(k), g.dy32);
-        xr[k].load(a, row, xa, d, e0, count(k), g.x32);
+        yr[k].load(a.dy, up.at + 8 * k * P, count(k), g.dy32);
+        xr[k].load(a, at_row, from.at + 8 * k * P, count(k), g.x32);
       }
     }
-    stats = have ? a.stats[row] : make_float2(0.0f, 0.0f);
+    stats = have ? a.stats[at_row] : make_float2(0.0f, 0.0f);
   };
-  int64_t row = (int64_t)blockIdx.x * RB + rl;
   fetch(row);
+  {
+    Parameters<DY != kAny> pw[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) pw[k].load(a.weight, g.fp32, 8 * (lr + k * P), count(k));
+#pragma unroll
+    for (int k = 0; k < K; ++k) pw[k].floats(a.weight, g.fp32, 1.0f, w[k]);
+  }
   int flip = 0;
-  for (; row - rl < a.rows; row += (int64_t)g.blocks * RB) {
+  // rows from this round's first one on, the same in the whole workgroup
+  for (int64_t left = (int64_t)rows - (row - rl); left > 0; left -= step) {
     float h[K][8], dy[K][8];
     const float mean = stats.x, rstd = stats.y;
 #pragma unroll
@@ -429,8 +509,12 @@ __global__ void __launch_bounds__(kBackThreads) layer_norm_backward_kernel(NormB
       xr[k].floats(h[k]);
       yr[k].floats(dy[k]);
     }
-    fetch(row + (int64_t)g.blocks * RB);
-    float s1 = 0.0f, s2 = 0.0f;
+    const unsigned now = row;
+    row += step;  // below 2^31 + 2^18
+    from.next(row, xheads, xts, xhs, 8 * lr);
+    up.next(row, a.heads, a.dyts, a.dyhs, 8 * lr);
+    fetch(row);
+    float s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -439,34 +523,33 @@ __global__ void __launch_bounds__(kBackThreads) layer_norm_backward_kernel(NormB
         dw[k][i] = fmaf(dy[k][i], h[k][i], dw[k][i]);
         db[k][i] += dy[k][i];
         dy[k][i] *= w[k][i];
-        s1 += dy[k][i];
-        s2 = fmaf(dy[k][i], h[k][i], s2);
+        s[0] += dy[k][i];
+        s[1] = fmaf(dy[k][i], h[k][i], s[1]);
       }
     if (!a.dx) continue;
-    s1 = lanes_add(s1, P);
-    s2 = lanes_add(s2, P);
+    lanes_add(s, g.log_p);
     if (P > kWave) {
-      const float2 s = join_waves(red, flip, P, make_float2(s1, s2),
+      const float2 j = join_waves(red, flip, P, make_float2(s[0], s[1]),
                                   [](float2 x, float2 y) { return make_float2(x.x + y.x, x.y + y.y); });
-      s1 = s.x;
-      s2 = s.y;
+      s[0] = j.x;
+      s[1] = j.y;
     }
-    s1 *= inv_d;
-    s2 *= inv_d;
-    if (row >= a.rows) continue;
-    const int64_t at = place(row, a.dxts, a.dxhs);
+    const float c1 = -(s[0] * inv_d) * rstd, c2 = -(s[1] * inv_d) * rstd;
+    if (now < rows) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if (count(k) == 0) continue;
+      for (int k = 0; k < K; ++k) {
+        if (count(k) == 0) continue;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dy[k][i] = rstd * fmaf(-h[k][i], s2, dy[k][i] - s1);
-      put<DX>(a.dx, at + 8 * (lr + k * P), count(k), g.dx32, dy[k]);
+        for (int i = 0; i < 8; ++i) dy[k][i] = fmaf(dy[k][i], rstd, fmaf(h[k][i], c2, c1));
+        put<DX, PAST>(a.dx, to.at + 8 * k * P, count(k), g.dx32, dy[k]);
+      }
     }
+    to.next(row, a.heads, a.dxts, a.dxhs, 8 * lr);
   }
   if (!a.part) return;
   // The columns' sums over the workgroup's row groups: over the wave's lanes, then over the waves.
   const int dp = norm_columns(d);
-  float* to = a.part + (int64_t)blockIdx.x * 2 * dp;
+  float* sums = a.part + (int64_t)blockIdx.x * 2 * dp;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
 #pragma unroll
@@ -479,7 +562,7 @@ __global__ void __launch_bounds__(kBackThreads) layer_norm_backward_kernel(NormB
       auto store = [&] {
 #pragma unroll
         for (int i = 0; i < 8; i += 4)
-          if (e0 + i < dp) *reinterpret_cast<f32x4*>(to + side * dp + e0 + i) = f32x4{c[i], c[i + 1], c[i + 2], c[i + 3]};
+          if (e0 + i < dp) *reinterpret_cast<f32x4*>(sums + side * dp + e0 + i) = f32x4{c[i], c[i + 1], c[i + 2], c[i + 3]};
       };
       if (P == kBackThreads) {  // one row at a time: nothing to join
         store();
@@ -543,16 +626,24 @@ __global__ void __launch_bounds__(kColumnThreads) norm_columns_kernel(const floa
     if (e0 + i < d) to[e0 + i] = s[i];
 }
 
-template <int X, int DY, int DX>
-hipError_t backward_k(const NormBackArgs& a, const NormBackGrid& g, int k, hipStream_t s) {
+template <int X, int DY, int DX, bool PAST>
+hipError_t backward_past(const NormBackArgs& a, const NormBackGrid& g, int k, hipStream_t s) {
   const dim3 grid(g.blocks), block(kBackThreads);
   switch (k) {
-    case 1: hipLaunchKernelGGL((layer_norm_backward_kernel<X, DY, DX, 1>), grid, block, 0, s, a, g); break;
-    case 2: hipLaunchKernelGGL((layer_norm_backward_kernel<X, DY, DX, 2>), grid, block, 0, s, a, g); break;
-    case 3: hipLaunchKernelGGL((layer_norm_backward_kernel<X, DY, DX, 3>), grid, block, 0, s, a, g); break;
+    case 1: hipLaunchKernelGGL((layer_norm_backward_kernel<X, DY, DX, 1, PAST>), grid, block, 0, s, a, g); break;
+    case 2: hipLaunchKernelGGL((layer_norm_backward_kernel<X, DY, DX, 2, PAST>), grid, block, 0, s, a, g); break;
+    case 3: hipLaunchKernelGGL((layer_norm_backward_kernel<X, DY, DX, 3, PAST>), grid, block, 0, s, a, g); break;
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();
+}
+
+template <int X, int DY, int DX>
+hipError_t backward_k(const NormBackArgs& a, const NormBackGrid& g, int k, hipStream_t s) {
+  if constexpr (DX != kAny) {
+    if (past_caches(a.rows, (int)g.d, DX)) return backward_past<X, DY, DX, true>(a, g, k, s);
+  }
+  return backward_past<X, DY, DX, false>(a, g, k, s);
 }
 
 template <int X>
@@ -594,7 +685,6 @@ hipError_t launch_layer_norm_backward(const NormBackArgs& args, int d, bool weig
     g.d = (uint32_t)d;
     g.log_p = (uint32_t)shape.log_p;
     g.fp32 = weight32;
-    g.whole = d % 8 == 0 && aligned16(a.weight, 0, 0, kRowsBF16);
     g.x32 = x_dtype == kRowsFP32;
     g.dy32 = dy_dtype == kRowsFP32;
     g.dx32 = dx_dtype == kRowsFP32;
@@ -602,7 +692,7 @@ hipError_t launch_layer_norm_backward(const NormBackArgs& args, int d, bool weig
     auto ok = [&](const void* p, int64_t ts, int64_t hs, int dtype) {
       return aligned16(p, a.rows == a.heads ? 0 : ts, a.heads == 1 ? 0 : hs, dtype);
     };
-    const bool vec = d % 8 == 0 && ok(a.dy, a.dyts, a.dyhs, dy_dtype) && (!rows || ok(a.x, a.xts, a.xhs, x_dtype)) &&
+    const bool vec = d % 8 == 0 && aligned16(a.weight, 0, 0, kRowsBF16) && ok(a.dy, a.dyts, a.dyhs, dy_dtype) && (!rows || ok(a.x, a.xts, a.xhs, x_dtype)) &&
                      (!a.dx || ok(a.dx, a.dxts, a.dxhs, dx_dtype));
     hipError_t e;
     if (!vec) {

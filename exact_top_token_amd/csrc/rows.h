@@ -172,33 +172,49 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
 }
 
-// x / scale with an inexact result's last bit set: rounding that to a short
-// format equals rounding the exact quotient (the 64-bit quotient of two 24-bit
-// numbers cannot round onto a tie of fewer bits unless it is one).
-__device__ __forceinline__ float quotient_odd(float x, float scale) {
-  const double q = (double)x / (double)scale;
-  const float f = (float)q;
-  const double df = (double)f;
-  if (df == q || !isfinite(f)) return f;
-  uint32_t u = __float_as_uint(f);
-  if (fabs(df) > fabs(q)) --u;  // toward zero
-  return __uint_as_float(u | 1u);
+// The scale of an FP8 row whose largest magnitude is m: max(m / 448, 2^-126), 1 for a row of zeros.  The quotient is rounded
+// as a division's: a product with the rounded 1 / 448 and one correction by the exact remainder (all 2^23
+// significands compared with the division's).
+__device__ __forceinline__ float e4m3_scale(float m) {
+  constexpr float kInv = 1.0f / 448.0f;
+  const float q = m * kInv;
+  return m > 0.0f ? fmaxf(fmaf(fmaf(-448.0f, q, m), kInv, q), 0x1p-126f) : 1.0f;
 }
 
-// The E4M3 bytes of four exact quotients x / scale.  x * inv is within 2^-22
-// of the quotient; only where the codes of its two ends differ, near a tie, is the
-// quotient formed in 64 bits.
-__device__ __forceinline__ uint32_t e4m3x4_quotient(const float* x, float scale, float inv) {
-  constexpr float kLo = 1.0f - 0x1p-22f, kHi = 1.0f + 0x1p-22f;
-  float q[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) q[i] = x[i] * inv;
-  const uint32_t lo = e4m3x4(q[0] * kLo, q[1] * kLo, q[2] * kLo, q[3] * kLo);
-  const uint32_t hi = e4m3x4(q[0] * kHi, q[1] * kHi, q[2] * kHi, q[3] * kHi);
+// The E4M3 bytes of four exact quotients x / scale.  `below` and `above` are 1 / scale less and plus 2^-21 of it, so x
+// times them lies on either side of the quotient, and its code is one of the two's.  Where they differ, the quotient
+// lies near the tie between them, half of a + b: x - (a + b) / 2 scale, one fused operation, has the exact difference's sign
+// (rows far below 1 are raised by 2^64 first, so that none is lost below the smallest number).  Rows of bf16 meet ties often:
+// where the largest's significand is a multiple of 7, one element in some thirty.
+struct Reciprocal {
+  float scale, below, above;
+  __device__ __forceinline__ explicit Reciprocal(float s) : scale(s) {
+    const float inv = __builtin_amdgcn_rcpf(s);  // within 2^-23 of it, each of the two products within 2^-24
+    below = inv * (1.0f - 0x1p-21f);
+    above = inv * (1.0f + 0x1p-21f);
+  }
+};
+__device__ __forceinline__ uint32_t e4m3x4_quotient(const float* x, const Reciprocal& r) {
+  const uint32_t lo = e4m3x4(x[0] * r.below, x[1] * r.below, x[2] * r.below, x[3] * r.below);
+  const uint32_t hi = e4m3x4(x[0] * r.above, x[1] * r.above, x[2] * r.above, x[3] * r.above);
   if (lo == hi) return lo;
+  const float raise = r.scale < 1.0f ? 0x1p64f : 1.0f, half = r.scale * raise * 0.5f;
+  auto pair = [](uint32_t codes, int i) {
+    return i == 0 ? __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, false) : __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, true);
+  };
+  uint32_t take = 0;  // the bytes of `hi` that are taken
 #pragma unroll
-  for (int i = 0; i < 4; ++i) q[i] = quotient_odd(x[i], scale);
-  return e4m3x4(q[0], q[1], q[2], q[3]);
+  for (int i = 0; i < 4; i += 2) {
+    const auto a = pair(lo, i), b = pair(hi, i);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float over = fmaf(-(a[j] + b[j]), half, x[i + j] * raise);
+      // beyond the tie, or on it with an odd code below
+      const bool up = over == 0.0f ? (lo >> (8 * (i + j))) & 1u : (__float_as_uint(over) ^ __float_as_uint(x[i + j])) >> 31 == 0;
+      take |= up ? 0xffu << (8 * (i + j)) : 0u;
+    }
+  }
+  return lo ^ ((lo ^ hi) & take);
 }
 
 // The exponent that a block of an MX format shares, where m is its largest magnitude: floor(log2(m)) less the

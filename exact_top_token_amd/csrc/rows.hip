@@ -451,7 +451,7 @@ cache_write_kernel(CacheWriteArgs a, WriteGrid g) {
       };
 
       float v[KV][8];
-      float scale = 1.0f, inv = 1.0f;
+      float scale = 1.0f;
       if constexpr (FMT == kFP8) {
         float m = 0.0f;
 #pragma unroll
@@ -469,11 +469,11 @@ cache_write_kernel(CacheWriteArgs a, WriteGrid g) {
           const int w0 = rl * (P / kWave);
           for (int w = 0; w < P / kWave; ++w) m = fmaxf(m, sums[w0 + w]);
         }
-        scale = m > 0.0f ? fmaxf(m / 448.0f, 0x1p-126f) : 1.0f;
-        inv = 1.0f / scale;
+        scale = e4m3_scale(m);
         if (row >= 0 && my.lr == 0) static_cast<float*>(a.scale)[row] = scale;
       }
 
+      const Reciprocal by(scale);
       const int64_t chunk0 = (int64_t)((uint64_t)(unsigned)row * (unsigned)chunks) + my.lr;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
@@ -492,7 +492,7 @@ cache_write_kernel(CacheWriteArgs a, WriteGrid g) {
         } else if constexpr (FMT == kBF16) {
           store8<kRowsBF16>(a.codes, chunk * 8, y);
         } else if constexpr (FMT == kFP8) {
-          const u32x2 w = {e4m3x4_quotient(y, scale, inv), e4m3x4_quotient(y + 4, scale, inv)};
+          const u32x2 w = {e4m3x4_quotient(y, by), e4m3x4_quotient(y + 4, by)};
           *reinterpret_cast<u32x2*>(a.codes + chunk * 8) = w;
         } else {
           if ((my.lr & 3) == 0)
