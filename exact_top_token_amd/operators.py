@@ -174,6 +174,11 @@ def _plan(rot, device):
     return rot._plan
 
 
+def _positions(n, rot):
+    """The shape of n tokens' positions."""
+    return (n,) if rot is None or rot.axes == 1 else (n, rot.axes)
+
+
 def rotary(x, rot: Rotary, *, q_start: int = 0, q_pos=None, backward: bool = False, out=None,
            out_dtype=None):
     """Rotary positions of rows x [n][d] or [n][heads][d] (bf16 or fp32, any
@@ -196,7 +201,7 @@ def rotary(x, rot: Rotary, *, q_start: int = 0, q_pos=None, backward: bool = Fal
             raise ValueError(f"out must have x's shape {tuple(shape)} and device, and out_dtype")
         ya = _rows_array(out, "out")
     if q_pos is not None:
-        _need(q_pos, "q_pos", (n,) if rot.axes == 1 else (n, rot.axes), _i32, device)
+        _need(q_pos, "q_pos", _positions(n, rot), _i32, device)
     _launch(device, load_library().hytopk_rotary, _plan(rot, device), n, heads, d, xa, ya,
             _address(q_pos), int(q_start), 1 if backward else 0)
     return out
@@ -255,7 +260,7 @@ def cache_write(x, codes, scale=None, *, fmt=None, start: int = 0, slots=None, r
     if shape[-1] != c.d or (shape[1] if len(shape) == 3 else 1) != c.heads:
         raise ValueError(f"x {tuple(shape)} does not fit cache rows of {c.heads} x {c.d}")
     if q_pos is not None:
-        _need(q_pos, "q_pos", (n,) if rotary is None or rotary.axes == 1 else (n, rotary.axes), _i32, device)
+        _need(q_pos, "q_pos", _positions(n, rotary), _i32, device)
     if slots is not None:
         _need(slots, "slots", (n,), _i32, device)
     if workspace is not None:
@@ -336,9 +341,8 @@ class NormSaved(NamedTuple):
     fmt: str | None
 
 
-def _norm_shape(t, name: str):
+def _norm_shape(shape, name: str):
     """n, heads and d of rows [n][d] or [n][heads][d]."""
-    shape = t.shape
     if len(shape) == 2:
         return shape[0], 1, shape[1]
     if len(shape) == 3:
@@ -347,11 +351,9 @@ def _norm_shape(t, name: str):
 
 
 def _norm(weight, bias, d, eps, device) -> Norm:
-    dtype = _f32
-    if weight is not None:
-        dtype = weight.dtype
-    elif bias is not None:
-        dtype = bias.dtype
+    if weight is None and bias is None:
+        return Norm(None, None, 1, eps)
+    dtype = bias.dtype if weight is None else weight.dtype
     if dtype != _f32 and dtype != _bf16:
         raise TypeError(f"weight and bias must be bfloat16 or float32, got {dtype}")
     if weight is not None:
@@ -363,25 +365,29 @@ def _norm(weight, bias, d, eps, device) -> Norm:
 
 def _saved(s: NormSaved, shape, device):
     """The rows or the cache that a NormSaved stands for."""
+    rows, scale, stats, fmt = s
     lead = shape[:-1]
-    _need(s.stats, "stats", (*lead, 2), _f32, device)
-    if s.fmt is None:
-        if s.scale is not None:
+    _need(stats, "stats", (*lead, 2), _f32, device)
+    if fmt is None:
+        if scale is not None:
             raise ValueError("rows that are kept as they are take no scale")
-        if s.rows.shape != shape or s.rows.device != device:
+        if rows.shape != shape or rows.device != device:
             raise ValueError(f"saved rows must have the shape {tuple(shape)} and be on {device}")
-        return _rows_array(s.rows, "saved rows"), None
-    if s.fmt not in _CHECKPOINTS:
-        raise ValueError(f"unknown checkpoint format {s.fmt!r}: fp8 or mxfp8")
-    if s.scale is None:
+        return _rows_array(rows, "saved rows"), None
+    if fmt not in _CHECKPOINTS:
+        raise ValueError(f"unknown checkpoint format {fmt!r}: fp8 or mxfp8")
+    if scale is None:
         raise ValueError("fp8 and mxfp8 checkpoints need scale")
-    d, n = shape[-1], math.prod(lead)
-    _need(s.rows, "saved codes", shape, _u8, device)
-    if s.fmt == "fp8":
-        _need(s.scale, "scale", lead, _f32, device)
+    _need(rows, "saved codes", shape, _u8, device)
+    if fmt == "fp8":
+        _need(scale, "scale", lead, _f32, device)
     else:
-        _need(s.scale, "scale", (*lead, d // 32), _u8, device)
-    return None, Cache(s.rows.data_ptr(), s.scale.data_ptr(), n, 1, d, _CHECKPOINTS[s.fmt], 0)
+        _need(scale, "scale", (*lead, shape[-1] // 32), _u8, device)
+    return None, _checkpoint(s, shape)
+
+
+def _checkpoint(s: NormSaved, shape) -> Cache:
+    return Cache(s.rows.data_ptr(), s.scale.data_ptr(), math.prod(shape[:-1]), 1, shape[-1], _CHECKPOINTS[s.fmt], 0)
 
 
 def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None, out_dtype=None, save=None):
@@ -391,9 +397,9 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None, out_dt
     (y, saved) and ``layer_norm_backward`` takes ``saved``: "x" keeps x itself (not a copy), "fp8" or "mxfp8"
     a checkpoint of it in 8 bits (d a multiple of 32), made in the same pass, and a NormSaved names the buffers to fill."""
     _gpu(x, "x")
-    n, heads, d = _norm_shape(x, "x")
-    xa = _rows_array(x, "x")
     shape, device = x.shape, x.device
+    n, heads, d = _norm_shape(shape, "x")
+    xa = _rows_array(x, "x")
     if out is None and (out_dtype is None or out_dtype == x.dtype):
         out = _empty_like(x, memory_format=_contiguous)
         ya = RowsArray(out.data_ptr(), heads * d, d, xa.dtype, 0)
@@ -404,10 +410,16 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None, out_dt
             raise ValueError(f"out must have x's shape {tuple(shape)} and device, and out_dtype")
         ya = _rows_array(out, "out")
     p = _norm(weight, bias, d, eps, device)
+    lib = load_library()
     if save is None:
-        _launch(device, load_library().hytopk_layer_norm, p, n, heads, d, xa, ya, None, None)
+        _launch(device, lib.hytopk_layer_norm, p, n, heads, d, xa, ya, None, None)
         return out
-    if not isinstance(save, NormSaved):
+    cache = None
+    if isinstance(save, NormSaved):
+        rows, cache = _saved(save, shape, device)
+        if cache is None and (rows.data != xa.data or save.rows.dtype != x.dtype or save.rows.stride() != x.stride()):
+            raise ValueError("a NormSaved without a format keeps x itself")
+    else:
         stats = x.new_empty((*shape[:-1], 2), dtype=_f32)
         if save == "x":
             save = NormSaved(x, None, stats, None)
@@ -416,21 +428,19 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None, out_dt
                 raise ValueError("checkpoints in 8 bits need d in multiples of 32")
             scale = (x.new_empty(shape[:-1], dtype=_f32) if save == "fp8"
                      else x.new_empty((*shape[:-1], d // 32), dtype=_u8))
-            save = NormSaved(x.new_empty(shape, dtype=_u8), scale, stats, save)
+            save = NormSaved(_empty_like(x, dtype=_u8, memory_format=_contiguous), scale, stats, save)
+            cache = _checkpoint(save, shape)
         else:
             raise ValueError(f"save must be 'x', 'fp8', 'mxfp8' or a NormSaved, got {save!r}")
-    rows, cache = _saved(save, shape, device)
-    if cache is None and (rows.data != xa.data or save.rows.dtype != x.dtype or save.rows.stride() != x.stride()):
-        raise ValueError("a NormSaved without a format keeps x itself")
-    if cache is None and rows.data == ya.data and rows.data:
+    if cache is None and xa.data == ya.data and xa.data:
         raise ValueError("x is kept for the backward: out must not be x")
-    _launch(device, load_library().hytopk_layer_norm, p, n, heads, d, xa, ya, save.stats.data_ptr(), cache)
+    _launch(device, lib.hytopk_layer_norm, p, n, heads, d, xa, ya, save.stats.data_ptr(), cache)
     return out, save
 
 
 def layer_norm_backward_workspace_bytes(dy) -> int:
     """Workspace bytes of layer_norm_backward for dweight or dbias."""
-    return int(load_library().hytopk_layer_norm_backward_workspace(*_norm_shape(dy, "dy")))
+    return int(load_library().hytopk_layer_norm_backward_workspace(*_norm_shape(dy.shape, "dy")))
 
 
 def layer_norm_backward(dy, saved: NormSaved, weight=None, *, want=("dx", "dweight", "dbias"), dx_dtype=None,
@@ -440,41 +450,40 @@ def layer_norm_backward(dy, saved: NormSaved, weight=None, *, want=("dx", "dweig
     over all rows in a fixed order), those of ``want``.  ``weight`` is the forward's.  ``out`` gives tensors for some
     of them; dx may be dy or the saved rows themselves."""
     _gpu(dy, "dy")
-    lib = load_library()
-    n, heads, d = _norm_shape(dy, "dy")
-    ga = _rows_array(dy, "dy")
     shape, device = dy.shape, dy.device
+    n, heads, d = _norm_shape(shape, "dy")
+    ga = _rows_array(dy, "dy")
     p = _norm(weight, None, d, 0.0, device)
     rows, cache = _saved(saved, shape, device)
     res = {} if out is None else dict(out)
-    for name in res:
-        if name not in ("dx", "dweight", "dbias"):
-            raise ValueError(f"unknown gradient name in out: {name!r}")
     for name in want:
-        if name in res:
-            continue
+        if name not in res:
+            if name == "dx":
+                res[name] = (_empty_like(dy, memory_format=_contiguous) if dx_dtype is None
+                             else dy.new_empty(shape, dtype=dx_dtype))
+            else:
+                res[name] = dy.new_empty(d, dtype=_f32)
+    xa = dweight = dbias = None
+    for name, t in res.items():
         if name == "dx":
-            res[name] = (_empty_like(dy, memory_format=_contiguous) if dx_dtype is None
-                         else dy.new_empty(shape, dtype=dx_dtype))
-        elif name in ("dweight", "dbias"):
-            res[name] = dy.new_empty(d, dtype=_f32)
+            if t.shape != shape or t.device != device or dx_dtype not in (None, t.dtype):
+                raise ValueError(f"dx must have dy's shape {tuple(shape)} and device, and dx_dtype")
+            xa = _rows_array(t, "dx")
+            continue
+        _need(t, name, (d,), _f32, device)
+        if name == "dweight":
+            dweight = t.data_ptr()
+        elif name == "dbias":
+            dbias = t.data_ptr()
         else:
-            raise ValueError(f"unknown gradient name in want: {name!r}")
-    dx, dweight, dbias = res.get("dx"), res.get("dweight"), res.get("dbias")
-    xa = None
-    if dx is not None:
-        if dx.shape != shape or dx.device != device or dx_dtype not in (None, dx.dtype):
-            raise ValueError(f"dx must have dy's shape {tuple(shape)} and device, and dx_dtype")
-        xa = _rows_array(dx, "dx")
-    for t, name in ((dweight, "dweight"), (dbias, "dbias")):
-        if t is not None:
-            _need(t, name, (d,), _f32, device)
+            raise ValueError(f"unknown gradient name {name!r}")
+    lib = load_library()
     if workspace is not None:
         _workspace(workspace, device)
-    elif dweight is not None or dbias is not None:
+    elif dweight or dbias:
         workspace = dy.new_empty(lib.hytopk_layer_norm_backward_workspace(n, heads, d), dtype=_u8)
     _launch(device, lib.hytopk_layer_norm_backward, p, n, heads, d, ga, rows, cache, saved.stats.data_ptr(), xa,
-            _address(dweight), _address(dbias), _address(workspace), 0 if workspace is None else workspace.numel())
+            dweight, dbias, _address(workspace), 0 if workspace is None else workspace.numel())
     return res
 
 
