@@ -1240,7 +1240,8 @@ size_t hytopk_layer_norm_backward_workspace(int64_t n, int32_t heads, int32_t d)
   size_t need = 0;
   guarded([&]() -> int {
     const int rc = check_norm_rows(n, heads, d);
-    if (rc == HYTOPK_OK) need = align_up((size_t)hk::norm_backward_blocks(n * heads, d) * 2 * hk::norm_columns(d) * sizeof(float));
+    const int blocks = rc == HYTOPK_OK ? hk::norm_backward_blocks(n * heads, d) : 1;
+    if (blocks > 1) need = align_up((size_t)blocks * 2 * hk::norm_columns(d) * sizeof(float));
     return rc;
   });
   return need;
@@ -1262,8 +1263,7 @@ int hytopk_layer_norm_backward(const hytopk_norm* norm, int64_t n, int32_t heads
     if ((rc = check_stats(stats))) return rc;
     if (!stats && n > 0) return fail(HYTOPK_EINVAL, "the backward needs the forward's stats");
     if (misaligned(dweight, 4) || misaligned(dbias, 4)) return fail(HYTOPK_EINVAL, "dweight and dbias must be 4-byte aligned");
-    const bool sums = dweight || dbias;
-    const int64_t need = sums ? (int64_t)hytopk_layer_norm_backward_workspace(n, heads, d) : 0;
+    const int64_t need = dweight || dbias ? (int64_t)hytopk_layer_norm_backward_workspace(n, heads, d) : 0;
     if (need && (rc = check_ws(workspace, workspace_bytes, (size_t)need))) return rc;
     if (n > 0 && dx) {
       if (!rows_apart(dx, n, heads, d)) return fail(HYTOPK_EINVAL, "rows of dx overlap each other");

@@ -342,7 +342,7 @@ struct NormBackArgs {
   int64_t dyts, dyhs, dxts, dxhs;
   const void* weight;  // [d], or null (1)
   const float2* stats;  // [rows]
-  float* part;         // [norm_backward_blocks][2][norm_columns(d)], or null: no sums
+  float* part;         // [norm_backward_blocks][2][norm_columns(d)] of more than one workgroup, or null: no sums
   int rows, heads;
 };
 

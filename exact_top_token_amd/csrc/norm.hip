@@ -18,44 +18,57 @@ constexpr int kAny = 2;
 // A backward's x from a checkpoint (kRowsBF16, kRowsFP32, kAny: rows).
 constexpr int kCodesFP8 = 3, kCodesMXFP8 = 4;
 
-// Eight consecutive elements of a row, as loaded; `e` of them counts where only whole pieces exist
-// (16-byte access) as eight.
+// `e` elements `step` apart, as stored; the others stay.
+__device__ __forceinline__ void load_each(const void* base, int64_t at, int step, int e, bool fp32, uint32_t* v) {
+  if (fp32) {
+    const uint32_t* p = static_cast<const uint32_t*>(base) + at;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < e) v[i] = p[i * step];
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(base) + at;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < e) v[i] = p[i * step];
+  }
+}
+
+// Eight elements of a row, as loaded, `step` apart, of which `e` exist (with 16-byte access: neighbours, and all).
 template <int T>
 struct Piece {
   Raw8<T> raw;
   __device__ __forceinline__ void zero() { raw.zero(); }
-  __device__ __forceinline__ void load(const void* base, int64_t at, int, bool) { raw.template load<true>(base, at); }
+  __device__ __forceinline__ void load(const void* base, int64_t at, int, int, bool) { raw.template load<true>(base, at); }
   __device__ __forceinline__ void floats(float* v) const { raw.floats(v); }
 };
 template <>
 struct Piece<kAny> {
-  float v[8];
+  uint32_t v[8];  // as stored: a conversion beside the loads would wait for each
+  bool wide;
   __device__ __forceinline__ void zero() {
+    wide = true;
 #pragma unroll
-    for (float& x : v) x = 0.0f;
+    for (uint32_t& x : v) x = 0u;
   }
-  __device__ __forceinline__ void load(const void* base, int64_t at, int e, bool fp32) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = 0.0f;
-      if (i < e) v[i] = fp32 ? load1<kRowsFP32>(base, at + i) : load1<kRowsBF16>(base, at + i);
-    }
+  __device__ __forceinline__ void load(const void* base, int64_t at, int step, int e, bool fp32) {
+    wide = fp32;
+    load_each(base, at, step, e, fp32, v);
   }
   __device__ __forceinline__ void floats(float* o) const {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = v[i];
+    for (int i = 0; i < 8; ++i) o[i] = __uint_as_float(wide ? v[i] : v[i] << 16);
   }
 };
 
 // PAST: not kept in the caches.
 template <int T, bool PAST>
-__device__ __forceinline__ void put(void* base, int64_t at, int e, bool fp32, const float* v) {
+__device__ __forceinline__ void put(void* base, int64_t at, int step, int e, bool fp32, const float* v) {
   if constexpr (T == kAny) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (i >= e) continue;
-      if (fp32) store1<kRowsFP32>(base, at + i, v[i]);
-      else store1<kRowsBF16>(base, at + i, v[i]);
+      if (fp32) store1<kRowsFP32>(base, at + i * step, v[i]);
+      else store1<kRowsBF16>(base, at + i * step, v[i]);
     }
   } else {
     store8<T, PAST>(base, at, v);
@@ -68,12 +81,12 @@ __device__ __forceinline__ void put_codes(uint8_t* to, const u32x2& c) {
   else *reinterpret_cast<u32x2*>(to) = c;
 }
 
-// Eight elements of a weight or bias from element `at`, of which `e` exist, or `other` without one.  WHOLE: pieces of
-// eight, 16-byte aligned; loaded first and read later, so that loads of several are under way together.
+// Eight elements of a weight or bias from element `at`, `step` apart, of which `e` exist, or `other` without one.  WHOLE: neighbours,
+// 16-byte aligned; loaded first and read later, so that loads of several are under way together.
 template <bool WHOLE>
 struct Parameters {
   u32x4 w[2];
-  __device__ __forceinline__ void load(const void* p, bool fp32, int at, int e) {
+  __device__ __forceinline__ void load(const void* p, bool fp32, int at, int step, int e) {
     w[0] = w[1] = u32x4{0u, 0u, 0u, 0u};
     if (!p || e == 0) return;
     if constexpr (WHOLE) {
@@ -81,9 +94,10 @@ struct Parameters {
       w[0] = *reinterpret_cast<const u32x4*>(c);
       if (fp32) w[1] = *reinterpret_cast<const u32x4*>(c + 16);
     } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < e) w[i >> 2][i & 3] = __float_as_uint(fp32 ? load1<kRowsFP32>(p, at + i) : load1<kRowsBF16>(p, at + i));
+      uint32_t v[8] = {};
+      load_each(p, at, step, e, fp32, v);
+      w[0] = u32x4{v[0], v[1], v[2], v[3]};
+      w[1] = u32x4{v[4], v[5], v[6], v[7]};
     }
   }
   __device__ __forceinline__ void floats(const void* p, bool fp32, float other, float* v) const {
@@ -94,7 +108,7 @@ struct Parameters {
       unpack_bf16(w[0], v);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i >> 2][i & 3]);
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(fp32 ? w[i >> 2][i & 3] : w[i >> 2][i & 3] << 16);
     }
   }
 };
@@ -131,6 +145,23 @@ __device__ __forceinline__ void lanes_add(float (&x)[N], int log_p) {
   }
 }
 
+// The sum over the lanes of a wave whose numbers agree modulo 1 << log_p, in each of them (rows of 16 are rotated).
+__device__ __forceinline__ void rows_add(float (&x)[8], int log_p) {
+  auto each = [&](auto step) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = step(x[i]);
+  };
+  switch (log_p) {
+    case 0: each(add_dpp<0xb1>); [[fallthrough]];
+    case 1: each(add_dpp<0x4e>); [[fallthrough]];
+    case 2: each(add_dpp<0x124>); [[fallthrough]];
+    case 3: each(add_dpp<0x128>); [[fallthrough]];
+    case 4: each(add_16); [[fallthrough]];
+    case 5: each(add_32); [[fallthrough]];
+    default: break;
+  }
+}
+
 // Joins what the waves of a row hold (P > 64 threads a row; `flip` alternates between two
 // halves, so that one barrier a step is enough: the other half is read by waves still in the last step).
 template <typename Join>
@@ -154,6 +185,20 @@ __device__ __forceinline__ float inverse_root(float v) {
   const bool low = v < 0x1p-96f;
   return __builtin_amdgcn_rsqf(low ? v * 0x1p96f : v) * (low ? 0x1p48f : 1.0f);
 }
+
+// A thread's elements of a piece of P threads: eight neighbours or, where rows are accessed one element at a time and their width is no
+// multiple of eight, every P-th, so that neighbouring threads access neighbours (sums then add up in another order).
+struct Spread {
+  int first, step, log_step;
+  __device__ __forceinline__ Spread(bool any, int d, int lane, int log_p) {
+    const bool apart = any && d % 8 != 0;
+    log_step = apart ? log_p : 0;
+    step = 1 << log_step;
+    first = apart ? lane : 8 * lane;
+  }
+  // How many exist of a row that is `left` elements long from the piece's first on.
+  __device__ __forceinline__ int count(int left) const { return min(max((left - first + step - 1) >> log_step, 0), 8); }
+};
 
 // A thread's place in rows `ts` and `hs` apart: of the row's elements from `e` on, `step` further each round where
 // rows are one axis (one head).
@@ -199,18 +244,18 @@ __global__ void __launch_bounds__(kNormThreads) layer_norm_kernel(NormArgs a, No
   const int d = g.d, P = 1 << g.log_p, RB = kNormThreads >> g.log_p;
   const int lr = threadIdx.x & (P - 1), rl = threadIdx.x >> g.log_p;
   const float inv_d = 1.0f / (float)d;
-  // elements of the thread's k-th piece: all but the last pieces are whole
-  const int last = min(max(d - 8 * (lr + (K - 1) * P), 0), 8);
-  auto count = [&](int k) { return k < K - 1 ? 8 : last; };
+  const Spread spread(IN == kAny, d, lr, g.log_p);
+  const int e0 = spread.first, es = spread.step, last = spread.count(d - (K - 1) * P * 8);
+  auto count = [&](int k) { return k < K - 1 ? 8 : last; };  // all but the last pieces are whole
   const unsigned rows = a.rows;
   unsigned row = blockIdx.x * (RB * g.rounds) + rl;
-  Walk from(row, a.heads, a.xts, a.xhs, RB, 8 * lr), to(row, a.heads, a.yts, a.yhs, RB, 8 * lr);
+  Walk from(row, a.heads, a.xts, a.xhs, RB, e0), to(row, a.heads, a.yts, a.yhs, RB, e0);
   Piece<IN> raw[K];  // the next row's elements, under way while this one is worked on
   auto fetch = [&](unsigned at_row) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       raw[k].zero();
-      if (at_row < rows && count(k) > 0) raw[k].load(a.x, from.at + 8 * k * P, count(k), g.x32);
+      if (at_row < rows && count(k) > 0) raw[k].load(a.x, from.at + 8 * k * P, es, count(k), g.x32);
     }
   };
   fetch(row);
@@ -219,8 +264,8 @@ __global__ void __launch_bounds__(kNormThreads) layer_norm_kernel(NormArgs a, No
     Parameters<IN != kAny> pw[K], pb[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      pw[k].load(a.weight, g.fp32, 8 * (lr + k * P), count(k));
-      pb[k].load(a.bias, g.fp32, 8 * (lr + k * P), count(k));
+      pw[k].load(a.weight, g.fp32, e0 + 8 * k * P, es, count(k));
+      pb[k].load(a.bias, g.fp32, e0 + 8 * k * P, es, count(k));
     }
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -238,7 +283,7 @@ __global__ void __launch_bounds__(kNormThreads) layer_norm_kernel(NormArgs a, No
     const unsigned now = row;
     row += RB;
     if (r + 1 < (int)g.rounds) {
-      from.next(row, a.heads, a.xts, a.xhs, 8 * lr);
+      from.next(row, a.heads, a.xts, a.xhs, e0);
       fetch(row);
     }
 
@@ -313,10 +358,10 @@ __global__ void __launch_bounds__(kNormThreads) layer_norm_kernel(NormArgs a, No
         if (count(k) == 0) continue;
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[k][i] = fmaf(fmaf(v[k][i], rstd, off), w[k][i], b[k][i]);
-        put<OUT, PAST>(a.y, to.at + 8 * k * P, count(k), g.y32, v[k]);
+        put<OUT, PAST>(a.y, to.at + 8 * k * P, es, count(k), g.y32, v[k]);
       }
     }
-    if (r + 1 < (int)g.rounds) to.next(row, a.heads, a.yts, a.yhs, 8 * lr);
+    if (r + 1 < (int)g.rounds) to.next(row, a.heads, a.yts, a.yhs, e0);
   }
 }
 
@@ -418,8 +463,11 @@ struct NormBackGrid {
   uint32_t x32 : 1;   // rows accessed one element at a time
   uint32_t dy32 : 1;
   uint32_t dx32 : 1;
-  uint32_t blocks;    // workgroups
+  uint32_t blocks : 10;  // workgroups, at most 512
+  // One workgroup writes the results itself: `part` is dweight and dbias lies so many floats behind it, or one of them alone.
+  int32_t behind;
 };
+constexpr int32_t kParts = INT32_MIN, kWeightAlone = INT32_MIN + 1, kBiasAlone = INT32_MIN + 2;
 static_assert(sizeof(NormBackArgs) + sizeof(NormBackGrid) <= 112, "launches");
 
 namespace {
@@ -428,8 +476,8 @@ template <int X>
 struct XPiece {
   Piece<X> raw;
   __device__ __forceinline__ void zero() { raw.zero(); }
-  __device__ __forceinline__ void load(const NormBackArgs& a, int64_t, int64_t at, int e, bool fp32) {
-    raw.load(a.x, at, e, fp32);
+  __device__ __forceinline__ void load(const NormBackArgs& a, int64_t, int64_t at, int step, int e, bool fp32) {
+    raw.load(a.x, at, step, e, fp32);
   }
   __device__ __forceinline__ void floats(float* v) const { raw.floats(v); }
 };
@@ -437,7 +485,7 @@ template <int FMT>
 struct CodePiece {
   Stored8<FMT> raw;
   __device__ __forceinline__ void zero() { raw = Stored8<FMT>{}; }
-  __device__ __forceinline__ void load(const NormBackArgs& a, int64_t row, int64_t at, int, bool) {
+  __device__ __forceinline__ void load(const NormBackArgs& a, int64_t row, int64_t at, int, int, bool) {
     raw.load(static_cast<const uint8_t*>(a.x), a.scale, row, at);
   }
   __device__ __forceinline__ void floats(float* v) const { raw.decode(v); }
@@ -455,11 +503,12 @@ template <int X, int DY, int DX, int K, bool PAST>
 __global__ void __launch_bounds__(kBackThreads) layer_norm_backward_kernel(NormBackArgs a, NormBackGrid g) {
 #pragma clang fp contract(off)  // as forward
   __shared__ float2 red[2][kBackThreads / kWave];
-  __shared__ float cols[kBackThreads / kWave][kWave * 8];
+  __shared__ __attribute__((aligned(16))) float cols[kBackThreads * K * 16];  // [groups][2][K P 8]
   const int d = g.d, P = 1 << g.log_p, RB = kBackThreads >> g.log_p;
   const int lr = threadIdx.x & (P - 1), rl = threadIdx.x >> g.log_p;
   const float inv_d = 1.0f / (float)d;
-  const int last = min(max(d - 8 * (lr + (K - 1) * P), 0), 8);
+  const Spread spread(X == kAny, d, lr, g.log_p);
+  const int e0 = spread.first, es = spread.step, last = spread.count(d - (K - 1) * P * 8);
   auto count = [&](int k) { return k < K - 1 ? 8 : last; };
   float w[K][8], dw[K][8], db[K][8];
 #pragma unroll
@@ -473,8 +522,8 @@ __global__ void __launch_bounds__(kBackThreads) layer_norm_backward_kernel(NormB
   // a checkpoint's rows are one axis
   const int xheads = coded ? 1 : a.heads;
   const int64_t xts = coded ? d : a.xts, xhs = coded ? 0 : a.xhs;
-  Walk from(row, xheads, xts, xhs, step, 8 * lr), up(row, a.heads, a.dyts, a.dyhs, step, 8 * lr);
-  Walk to(row, a.heads, a.dxts, a.dxhs, step, 8 * lr);
+  Walk from(row, xheads, xts, xhs, step, e0), up(row, a.heads, a.dyts, a.dyhs, step, e0);
+  Walk to(row, a.heads, a.dxts, a.dxhs, step, e0);
   XPiece<X> xr[K];  // the next row's elements and statistics, under way while this one is worked on
   Piece<DY> yr[K];
   float2 stats;
@@ -485,8 +534,8 @@ __global__ void __launch_bounds__(kBackThreads) layer_norm_backward_kernel(NormB
       xr[k].zero();
       yr[k].zero();
       if (have && count(k) > 0) {
-        yr[k].load(a.dy, up.at + 8 * k * P, count(k), g.dy32);
-        xr[k].load(a, at_row, from.at + 8 * k * P, count(k), g.x32);
+        yr[k].load(a.dy, up.at + 8 * k * P, es, count(k), g.dy32);
+        xr[k].load(a, at_row, from.at + 8 * k * P, es, count(k), g.x32);
       }
     }
     stats = have ? a.stats[at_row] : make_float2(0.0f, 0.0f);
@@ -495,7 +544,7 @@ __global__ void __launch_bounds__(kBackThreads) layer_norm_backward_kernel(NormB
   {
     Parameters<DY != kAny> pw[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k) pw[k].load(a.weight, g.fp32, 8 * (lr + k * P), count(k));
+    for (int k = 0; k < K; ++k) pw[k].load(a.weight, g.fp32, e0 + 8 * k * P, es, count(k));
 #pragma unroll
     for (int k = 0; k < K; ++k) pw[k].floats(a.weight, g.fp32, 1.0f, w[k]);
   }
@@ -511,8 +560,8 @@ __global__ void __launch_bounds__(kBackThreads) layer_norm_backward_kernel(NormB
     }
     const unsigned now = row;
     row += step;  // below 2^31 + 2^18
-    from.next(row, xheads, xts, xhs, 8 * lr);
-    up.next(row, a.heads, a.dyts, a.dyhs, 8 * lr);
+    from.next(row, xheads, xts, xhs, e0);
+    up.next(row, a.heads, a.dyts, a.dyhs, e0);
     fetch(row);
     float s[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -541,43 +590,44 @@ __global__ void __launch_bounds__(kBackThreads) layer_norm_backward_kernel(NormB
         if (count(k) == 0) continue;
 #pragma unroll
         for (int i = 0; i < 8; ++i) dy[k][i] = fmaf(dy[k][i], rstd, fmaf(h[k][i], c2, c1));
-        put<DX, PAST>(a.dx, to.at + 8 * k * P, count(k), g.dx32, dy[k]);
+        put<DX, PAST>(a.dx, to.at + 8 * k * P, es, count(k), g.dx32, dy[k]);
       }
     }
-    to.next(row, a.heads, a.dxts, a.dxhs, 8 * lr);
+    to.next(row, a.heads, a.dxts, a.dxhs, e0);
   }
   if (!a.part) return;
-  // The columns' sums over the workgroup's row groups: over the wave's lanes, then over the waves.
-  const int dp = norm_columns(d);
-  float* sums = a.part + (int64_t)blockIdx.x * 2 * dp;
+  // The columns' sums over the workgroup's rows: over a wave's lanes, then (P < 64) over the waves or over the row groups, whose
+  // sums meet in LDS.
+  const int dp = norm_columns(d), width = K * P * 8, groups = min(RB, kBackThreads / kWave);
+  const int group = P < kWave ? (int)threadIdx.x >> 6 : rl;
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
+  for (int side = 0; side < 2; ++side)
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      float* c = side ? db[k] : dw[k];
-      for (int off = P; off < kWave; off <<= 1)
+    for (int k = 0; k < K; ++k) {
+      float (&c)[8] = side ? db[k] : dw[k];
+      rows_add(c, g.log_p);
+      if (P < kWave && lane_id() >= P) continue;
+      float* to = cols + (group * 2 + side) * width + e0 + 8 * k * P;
+      if (X != kAny || es == 1) {
+        reinterpret_cast<f32x4*>(to)[0] = f32x4{c[0], c[1], c[2], c[3]};
+        reinterpret_cast<f32x4*>(to)[1] = f32x4{c[4], c[5], c[6], c[7]};
+      } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] += __shfl_xor(c[i], off);
-      const int e0 = 8 * (lr + k * P);
-      auto store = [&] {
-#pragma unroll
-        for (int i = 0; i < 8; i += 4)
-          if (e0 + i < dp) *reinterpret_cast<f32x4*>(sums + side * dp + e0 + i) = f32x4{c[i], c[i + 1], c[i + 2], c[i + 3]};
-      };
-      if (P == kBackThreads) {  // one row at a time: nothing to join
-        store();
-        continue;
+        for (int i = 0; i < 8; ++i) to[i * es] = c[i];
       }
-      __syncthreads();  // the last piece's sums are read
+    }
+  __syncthreads();
+  for (int q = threadIdx.x; q < dp / 2; q += kBackThreads) {  // four columns
+    const int side = q >= dp / 4, e0 = 4 * (q - side * (dp / 4));
+    f32x4 v = *reinterpret_cast<const f32x4*>(cols + side * width + e0);
+    for (int i = 1; i < groups; ++i) v += *reinterpret_cast<const f32x4*>(cols + (i * 2 + side) * width + e0);
+    if (g.behind == kParts) {
+      *reinterpret_cast<f32x4*>(a.part + ((int64_t)blockIdx.x * 2 + side) * dp + e0) = v;
+    } else if (g.behind != (side ? kWeightAlone : kBiasAlone)) {
+      float* to = a.part + (side && g.behind != kBiasAlone ? g.behind : 0) + e0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) cols[threadIdx.x >> 6][i * kWave + lane_id()] = c[i];
-      __syncthreads();
-      if (rl != 0) continue;
-      const int step = max(P / kWave, 1);  // waves of a row group
-      for (int wv = (threadIdx.x >> 6) + step; wv < kBackThreads / kWave; wv += step)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] += cols[wv][i * kWave + lane_id()];
-      store();
+      for (int i = 0; i < 4; ++i)
+        if (e0 + i < d) to[i] = v[i];
     }
   }
 }
@@ -661,55 +711,74 @@ RowShape back_shape(int d) { return row_shape(d, 9, 3, 9); }
 }  // namespace
 
 int norm_backward_blocks(int64_t rows, int d) {
-  const int64_t rb = kBackThreads >> back_shape(d).log_p;
-  return (int)std::min<int64_t>((rows + rb - 1) / rb, back_shape(d).k == 1 ? 512 : 256);
+  const RowShape shape = back_shape(d);
+  const int64_t rb = kBackThreads >> shape.log_p, sets = (rows + rb - 1) / rb;
+  // Few rows take one workgroup and one launch (through the binding, one against two: 64 x 128 8.5 and 10.8 us, 128 x 128 8.5 and
+  // 10.8, but 512 x 128 12.2 and 11.0; 4 x 8,192 11.7 and 10.9).
+  if (sets <= (d % 8 || d > 2048 ? 2 : 4)) return 1;
+  return (int)std::min<int64_t>(sets, shape.k == 1 ? 512 : 256);
 }
 
 hipError_t launch_layer_norm_backward(const NormBackArgs& args, int d, bool weight32, int x_dtype, int codes, int dy_dtype,
                                       int dx_dtype, float* dweight, float* dbias, hipStream_t s) {
   if (d <= 0 || d > kMaxNorm) return hipErrorInvalidValue;
   NormBackArgs a = args;
+  if (a.rows <= 0) a.dx = nullptr;
+  const bool sums = dweight || dbias;
+  if (!a.dx && !sums) return hipSuccess;
   const bool rows = codes == kBF16;  // else a checkpoint's
-  const int blocks = norm_backward_blocks(a.rows, d);
-  if (blocks > 0 && (a.dx || a.part)) {
-    // rows that lie evenly over tokens and heads are one axis
-    if (a.heads > 1 && a.dyts == a.heads * a.dyhs && (!rows || a.xts == a.heads * a.xhs) &&
-        (!a.dx || a.dxts == a.heads * a.dxhs)) {
-      a.heads = 1;
-      a.dyts = a.dyhs;
-      if (rows) a.xts = a.xhs;
-      a.dxts = a.dxhs;
-    }
-    const RowShape shape = back_shape(d);
-    NormBackGrid g{};
-    g.d = (uint32_t)d;
-    g.log_p = (uint32_t)shape.log_p;
-    g.fp32 = weight32;
-    g.x32 = x_dtype == kRowsFP32;
-    g.dy32 = dy_dtype == kRowsFP32;
-    g.dx32 = dx_dtype == kRowsFP32;
-    g.blocks = (uint32_t)blocks;
-    auto ok = [&](const void* p, int64_t ts, int64_t hs, int dtype) {
-      return aligned16(p, a.rows == a.heads ? 0 : ts, a.heads == 1 ? 0 : hs, dtype);
-    };
-    const bool vec = d % 8 == 0 && aligned16(a.weight, 0, 0, kRowsBF16) && ok(a.dy, a.dyts, a.dyhs, dy_dtype) && (!rows || ok(a.x, a.xts, a.xhs, x_dtype)) &&
-                     (!a.dx || ok(a.dx, a.dxts, a.dxhs, dx_dtype));
-    hipError_t e;
-    if (!vec) {
-      e = rows ? backward_k<kAny, kAny, kAny>(a, g, shape.k, s)
-               : codes == kFP8 ? backward_k<kCodesFP8, kAny, kAny>(a, g, shape.k, s)
-                               : backward_k<kCodesMXFP8, kAny, kAny>(a, g, shape.k, s);
-    } else if (codes == kFP8) {
-      e = backward_io<kCodesFP8>(a, g, shape.k, dy_dtype, dx_dtype, s);
-    } else if (codes == kMXFP8) {
-      e = backward_io<kCodesMXFP8>(a, g, shape.k, dy_dtype, dx_dtype, s);
-    } else {
-      e = x_dtype == kRowsBF16 ? backward_io<kRowsBF16>(a, g, shape.k, dy_dtype, dx_dtype, s)
-                               : backward_io<kRowsFP32>(a, g, shape.k, dy_dtype, dx_dtype, s);
-    }
-    if (e != hipSuccess) return e;
+  // rows that lie evenly over tokens and heads are one axis
+  if (a.heads > 1 && a.dyts == a.heads * a.dyhs && (!rows || a.xts == a.heads * a.xhs) &&
+      (!a.dx || a.dxts == a.heads * a.dxhs)) {
+    a.heads = 1;
+    a.dyts = a.dyhs;
+    if (rows) a.xts = a.xhs;
+    a.dxts = a.dxhs;
   }
-  if (!dweight && !dbias) return hipSuccess;
+  const RowShape shape = back_shape(d);
+  const int blocks = norm_backward_blocks(a.rows, d);
+  NormBackGrid g{};
+  g.d = (uint32_t)d;
+  g.log_p = (uint32_t)shape.log_p;
+  g.fp32 = weight32;
+  g.x32 = x_dtype == kRowsFP32;
+  g.dy32 = dy_dtype == kRowsFP32;
+  g.dx32 = dx_dtype == kRowsFP32;
+  g.blocks = (uint32_t)blocks;
+  g.behind = kParts;
+  auto ok = [&](const void* p, int64_t ts, int64_t hs, int dtype) {
+    return aligned16(p, a.rows == a.heads ? 0 : ts, a.heads == 1 ? 0 : hs, dtype);
+  };
+  const bool vec = d % 8 == 0 && aligned16(a.weight, 0, 0, kRowsBF16) && ok(a.dy, a.dyts, a.dyhs, dy_dtype) &&
+                   (!rows || ok(a.x, a.xts, a.xhs, x_dtype)) && (!a.dx || ok(a.dx, a.dxts, a.dxhs, dx_dtype));
+  auto launch = [&](const NormBackArgs& b) {
+    if (!vec) {
+      return rows ? backward_k<kAny, kAny, kAny>(b, g, shape.k, s)
+                  : codes == kFP8 ? backward_k<kCodesFP8, kAny, kAny>(b, g, shape.k, s)
+                                  : backward_k<kCodesMXFP8, kAny, kAny>(b, g, shape.k, s);
+    }
+    if (codes == kFP8) return backward_io<kCodesFP8>(b, g, shape.k, dy_dtype, dx_dtype, s);
+    if (codes == kMXFP8) return backward_io<kCodesMXFP8>(b, g, shape.k, dy_dtype, dx_dtype, s);
+    return x_dtype == kRowsBF16 ? backward_io<kRowsBF16>(b, g, shape.k, dy_dtype, dx_dtype, s)
+                                : backward_io<kRowsFP32>(b, g, shape.k, dy_dtype, dx_dtype, s);
+  };
+  if (sums && blocks == 1) {  // the one workgroup writes them itself
+    const int64_t behind = (int64_t)(reinterpret_cast<intptr_t>(dbias) - reinterpret_cast<intptr_t>(dweight)) / 4;
+    if (dweight && dbias && (behind <= kBiasAlone || behind > INT32_MAX)) {  // too far apart: by themselves, dy's rows before dx may replace them
+      NormBackArgs bias = a;
+      bias.dx = nullptr;
+      bias.part = dbias;
+      g.behind = kBiasAlone;
+      const hipError_t e = launch(bias);
+      if (e != hipSuccess) return e;
+      dbias = nullptr;
+    }
+    a.part = dweight ? dweight : dbias;
+    g.behind = !dbias ? kWeightAlone : !dweight ? kBiasAlone : (int32_t)behind;
+    return launch(a);
+  }
+  hipError_t e = launch(a);
+  if (e != hipSuccess || !sums) return e;
   // 256 contiguous bytes a row where that leaves 32 workgroups or more, else 64
   const int quads = norm_columns(d) / 2;
   if (quads >= 512)

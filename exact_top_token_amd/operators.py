@@ -439,7 +439,7 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None, out_dt
 
 
 def layer_norm_backward_workspace_bytes(dy) -> int:
-    """Workspace bytes of layer_norm_backward for dweight or dbias."""
+    """Workspace bytes of layer_norm_backward for dweight or dbias (0: none)."""
     return int(load_library().hytopk_layer_norm_backward_workspace(*_norm_shape(dy.shape, "dy")))
 
 
@@ -481,7 +481,9 @@ def layer_norm_backward(dy, saved: NormSaved, weight=None, *, want=("dx", "dweig
     if workspace is not None:
         _workspace(workspace, device)
     elif dweight or dbias:
-        workspace = dy.new_empty(lib.hytopk_layer_norm_backward_workspace(n, heads, d), dtype=_u8)
+        need = lib.hytopk_layer_norm_backward_workspace(n, heads, d)
+        if need:
+            workspace = dy.new_empty(need, dtype=_u8)
     _launch(device, lib.hytopk_layer_norm_backward, p, n, heads, d, ga, rows, cache, saved.stats.data_ptr(), xa,
             dweight, dbias, _address(workspace), 0 if workspace is None else workspace.numel())
     return res

@@ -424,7 +424,8 @@ typedef struct {
 int hytopk_layer_norm(const hytopk_norm* norm, int64_t n, int32_t heads, int32_t d, const hytopk_rows* x,
                       const hytopk_rows* y, float* stats, const hytopk_cache* save, void* stream);
 
-/* Workspace bytes of hytopk_layer_norm_backward when dweight or dbias is asked for (0 on invalid input). */
+/* Workspace bytes of hytopk_layer_norm_backward when dweight or dbias is asked for (0: none, for few rows, or on
+ * invalid input). */
 size_t hytopk_layer_norm_backward_workspace(int64_t n, int32_t heads, int32_t d);
 
 /* The gradients of hytopk_layer_norm from dy [n][heads][d], with stats as it gave them and
@@ -434,7 +435,7 @@ size_t hytopk_layer_norm_backward_workspace(int64_t n, int32_t heads, int32_t d)
  * x is the forward's input (`x`, `saved` NULL) or its checkpoint (`saved`, `x` NULL), whose decoded rows
  * then stand for x in h; mean and rstd are those of x itself.  Sums are fp32 in
  * an order that depends on the sizes alone: results are bitwise reproducible.  dx, dweight and dbias may be
- * NULL to skip them; dweight and dbias are fully written, the workspace (256-byte aligned) is required for
+ * NULL to skip them; dweight and dbias are fully written, the workspace (256-byte aligned) is for
  * either.  norm gives the weight (its bias and eps are not read).  dx may be dy or x itself; otherwise
  * nothing that is written, the workspace included, may overlap anything else. */
 int hytopk_layer_norm_backward(const hytopk_norm* norm, int64_t n, int32_t heads, int32_t d, const hytopk_rows* dy,

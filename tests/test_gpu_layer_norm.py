@@ -277,6 +277,45 @@ def test_no_rows(hk):
             assert r["dx"].shape == shape and not r["dweight"].any() and not r["dbias"].any()
 
 
+@pytest.mark.parametrize("d", [64, 128, 201, 576, 1024, 4096, 8192])
+def test_few_rows(hk, d):
+    """Around the number of rows up to which one workgroup writes the sums itself; each of the sums alone."""
+    w = _rand(d, 50, FP32, 0.2, 1.0)
+    at_once = max(1, 512 // max(1, 1 << max(0, (d + 7) // 8 - 1).bit_length()))
+    seen = set()
+    for n in sorted({1, 2, 3, 4, 5, *(k * at_once + e for k in (1, 2, 4, 8, 32) for e in (-1, 0, 1))} - {0}):
+        x, dy = _rows(n, 1, d, n, BF16)[:, 0], _rand((n, d), n + 1)
+        _, saved = hk.layer_norm(x, w, save="x")
+        seen.add(hk.layer_norm_backward_workspace_bytes(dy) == 0)
+        res = hk.layer_norm_backward(dy, saved, w)
+        check_backward(res, dy, f64(x), saved.stats, w)
+        for name in ("dweight", "dbias"):
+            assert torch.equal(hk.layer_norm_backward(dy, saved, w, want=(name,))[name], res[name]), (n, name)
+        # results in the middle of other memory: nothing beside them is written
+        room = torch.full((3, d + 3), 7.0, device="cuda")
+        out = {"dweight": room[2, 1:d + 1], "dbias": room[0, 2:d + 2]}
+        hk.layer_norm_backward(dy, saved, w, want=(), out=out)
+        assert torch.equal(out["dweight"], res["dweight"]) and torch.equal(out["dbias"], res["dbias"])
+        assert bool((room[1] == 7.0).all()) and int((room == 7.0).sum()) >= (d + 3) + 6
+    assert seen == {True, False}
+
+
+def test_sums_far_apart(hk):
+    """dweight and dbias more than 2^31 floats apart, either first, dx over dy."""
+    if torch.cuda.mem_get_info()[0] < 30 << 30:
+        pytest.skip("needs 30 GiB of GPU memory")
+    d = 96
+    base = torch.empty((1 << 31) + 4 * d, device="cuda")
+    x, w, dy = _rows(20, 2, d, 51, BF16), _rand(d, 52), _rand((20, 2, d), 53)
+    _, saved = hk.layer_norm(x, w, save="x")
+    want = hk.layer_norm_backward(dy, saved, w)
+    lo, hi = base[:d], base[-d:]
+    for a, b in ((lo, hi), (hi, lo)):
+        g = dy.clone()
+        r = hk.layer_norm_backward(g, saved, w, out={"dweight": a, "dbias": b, "dx": g})
+        assert all(torch.equal(r[name], want[name]) for name in want)
+
+
 def test_sums_of_many_rows(hk):
     """131,072 rows whose gradients cancel: the sums stay within their roundings."""
     n, d = 131072, 64

@@ -54,7 +54,11 @@ def cache(codes=CODES, scale=SCALE, L=15, heads=1, d=64, dtype=hk.FP8_E4M3):
     return hk.Cache(codes, scale, L, heads, d, dtype, 0)
 
 
-def backward(lib, n=5, heads=3, d=64, dy=dict(), x=dict(), dx=dict(), saved=None, w=W, dtype=FP32, stats=STATS, dw=DW, db=None, ws=WS,
+def kept(**kw):
+    return cache(**{"L": 300, **kw})
+
+
+def backward(lib, n=100, heads=3, d=64, dy=dict(), x=dict(), dx=dict(), saved=None, w=W, dtype=FP32, stats=STATS, dw=DW, db=None, ws=WS,
              ws_bytes=1 << 30, norm=True):
     """With dbias over dweight, which is looked for last."""
     a = None if dy is None else rows(**{"addr": DY, "heads": heads, "d": d, **dy})
@@ -70,7 +74,7 @@ def test_the_last_checks(lib):
                dict(save=cache(dtype=hk.MXFP8_E4M3)), dict(save=cache(L=1 << 20)), dict(d=8192, heads=1), dict(eps=0.0), dict(d=1)):
         refused(lib, forward(lib, **kw), EINVAL, LAST_FWD)
     for kw in (dict(), dict(n=1), dict(dx=dict(addr=DY)), dict(dx=dict(addr=X)), dict(dx=None), dict(dy=dict(ts=0, hs=0)),
-               dict(x=None, saved=cache()), dict(x=None, saved=cache(dtype=hk.MXFP8_E4M3)), dict(w=None), dict(d=8192, heads=1)):
+               dict(x=None, saved=kept()), dict(x=None, saved=kept(dtype=hk.MXFP8_E4M3)), dict(w=None), dict(d=8192, heads=1), dict(n=5)):
         refused(lib, backward(lib, **kw), EINVAL, LAST_BACK)
 
 
@@ -123,13 +127,13 @@ def test_forward_overlaps(lib, kw):
 
 @pytest.mark.parametrize("kw,status,words", [
     (dict(dy=None), EINVAL, "rows are NULL"), (dict(x=None), EINVAL, "input or its checkpoint"),
-    (dict(saved=cache()), EINVAL, "input or its checkpoint"), (dict(stats=None), EINVAL, "needs the forward's stats"),
+    (dict(saved=kept()), EINVAL, "input or its checkpoint"), (dict(stats=None), EINVAL, "needs the forward's stats"),
     (dict(stats=STATS + 4), EINVAL, "8-byte"), (dict(dw=DW + 2), EINVAL, "4-byte"), (dict(db=DB + 1), EINVAL, "4-byte"),
     (dict(ws=None), EWORKSPACE, "NULL"), (dict(ws=WS + 128), EWORKSPACE, "256-byte"), (dict(ws_bytes=255), EWORKSPACE, "too small"),
     (dict(dx=dict(hs=0)), EINVAL, "rows of dx overlap"), (dict(dx=dict(dtype=3)), EINVAL, "rows dtype"),
     (dict(dx=dict(addr=DY + 2)), EINVAL, "dy and dx overlap"), (dict(dx=dict(addr=DY, dtype=FP32)), EINVAL, "dy and dx overlap"),
     (dict(dx=dict(addr=X - 2)), EINVAL, "x and dx overlap"), (dict(x=dict(hs=0), dx=dict(addr=X)), EINVAL, "x and dx overlap"),
-    (dict(x=None, saved=cache(L=14)), EINVAL, "outside the cache"), (dict(x=None, saved=cache(dtype=hk.MXFP4_E2M1)), EUNSUPPORTED, "FP8 or MXFP8"),
+    (dict(x=None, saved=kept(L=299)), EINVAL, "outside the cache"), (dict(x=None, saved=kept(dtype=hk.MXFP4_E2M1)), EUNSUPPORTED, "FP8 or MXFP8"),
 ])
 def test_backward_refusals(lib, kw, status, words):
     refused(lib, backward(lib, **kw), status, words)
@@ -137,8 +141,8 @@ def test_backward_refusals(lib, kw, status, words):
 
 @pytest.mark.parametrize("kw", [
     dict(dx=dict(addr=W)), dict(dx=dict(addr=STATS - 2)), dict(dx=dict(addr=DW)), dict(dx=dict(addr=WS)), dict(dw=W), dict(dw=STATS),
-    dict(dw=DY), dict(dw=X + 2 * STEP - 4), dict(db=X), dict(db=DX), dict(db=WS), dict(ws=DY), dict(ws=X), dict(ws=W), dict(ws=STATS),
-    dict(ws=DX), dict(x=None, saved=cache(codes=DX)), dict(x=None, saved=cache(scale=DW)), dict(x=None, saved=cache(codes=WS)),
+    dict(dw=DY), dict(dw=X + 40 * STEP - 4), dict(db=X), dict(db=DX), dict(db=WS), dict(ws=DY), dict(ws=X), dict(ws=W), dict(ws=STATS),
+    dict(ws=DX), dict(x=None, saved=kept(codes=DX)), dict(x=None, saved=kept(scale=DW)), dict(x=None, saved=kept(codes=WS)),
 ])
 def test_backward_overlaps(lib, kw):
     kw = dict(dict(db=DB), **kw)
@@ -158,7 +162,13 @@ def test_nothing_to_do(lib):
 def test_workspace(lib):
     need = lib.hytopk_layer_norm_backward_workspace
     assert need(0, 1, 64) == 0 and need(-1, 1, 64) == 0 and need(5, 0, 64) == 0 and need(5, 1, 8193) == 0 and need(1 << 30, 2, 64) == 0
-    for n, heads, d in ((1, 1, 1), (77, 6, 201), (131072, 1, 128), (8192, 1, 5120), (2 ** 31 - 1, 1, 8192)):
+    # few rows: none, and one that is given is not looked at
+    for n, heads, d in ((0, 1, 64), (1, 1, 1), (1, 1, 8192), (1, 64, 128), (8, 1, 64), (1024, 1, 1)):
+        assert need(n, heads, d) == 0
+        for ws in (dict(ws=None), dict(ws=W), dict(ws=W + 4, ws_bytes=1)):
+            refused(lib, backward(lib, n=n, heads=heads, d=d, **ws), EINVAL, LAST_BACK)
+            refused(lib, backward(lib, n=n, heads=heads, d=d, db=W, **ws), EINVAL, LAST_BACK)
+    for n, heads, d in ((77, 6, 201), (131072, 1, 128), (8192, 1, 5120), (2 ** 31 - 1, 1, 8192)):
         size = need(n, heads, d)
         assert size % 256 == 0 and 0 < size <= 512 * 2 * (d + 3) * 4 + 256
         # one byte less is refused
@@ -275,8 +285,9 @@ def test_the_binding_s_refusals_on_the_gpu():
                dict(workspace=torch.empty(4096, device="cuda")), dict(workspace=torch.empty(4096, dtype=torch.uint8))):
         with pytest.raises((ValueError, TypeError)):
             hk.layer_norm_backward(y, saved, **kw)
+    z, kept_z = hk.layer_norm(torch.randn((400, 2, 64), device="cuda"), w, save="x")
     with pytest.raises(hk.HytopkError):
-        hk.layer_norm_backward(y, saved, workspace=torch.empty(255, dtype=torch.uint8, device="cuda"))
+        hk.layer_norm_backward(z, kept_z, workspace=torch.empty(255, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
         hk.layer_norm_backward(y[:, :1], saved)
     with pytest.raises(hk.HytopkError):  # a gradient over what is read
