@@ -894,11 +894,11 @@ hk::RotArgs rot_args(const hytopk_rotary_plan* p, const int32_t* q_pos, int64_t 
   if (!p) return r;
   r.freq = p->freq;
   r.pos = q_pos;
-  r.pos0 = (int)q_start;  // below 2^31
+  if (q_pos) r.axes = std::max(p->axes, 1);
+  else r.pos0 = (int)q_start;  // below 2^31
   r.gain = (float)p->gain;
   r.turn = backward ? -r.gain : r.gain;
-  r.dim = (uint16_t)p->dim;
-  r.axes = (uint16_t)std::max(p->axes, 1);
+  r.dim = p->dim;
   return r;
 }
 

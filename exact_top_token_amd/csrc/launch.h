@@ -264,11 +264,13 @@ constexpr int kRotHalf = 0, kRotInterleaved = 1;       // hytopk_rotary_layout
 struct RotArgs {
   const double* freq;  // [dim/2] radians a position; with several axes, behind them int [dim/2]: each pair's
   const int* pos;      // [n][axes] positions, or null (pos0 + i on every axis)
-  int pos0;
+  union {
+    int pos0;          // without positions
+    int axes;          // with them; at least 1
+  };
   float gain;          // factor on the cosines
   float turn;          // factor on the sines: gain, or -gain for the transposed rotation
-  uint16_t dim;        // at most 1,024
-  uint16_t axes;       // at least 1
+  int dim;
 };
 
 struct RotaryArgs {
