@@ -394,6 +394,8 @@ bool past_caches(int64_t rows, int d, int dtype) { return rows * d * rows_bytes(
 template <int IN, int OUT, int SAVE, bool PAST>
 hipError_t layer_norm_past(const NormArgs& a, NormGrid g, int k, hipStream_t s) {
   const int64_t rb = kNormThreads >> g.log_p, sets = (a.rows + rb - 1) / rb;
+  // About 2,048 workgroups, of at most eight rounds (131,072 x 128 by 1,024, 2,048 and 4,096 of them 12.4, 11.8 and 12.3 us, 5,003 x 7,168
+  // 28.4, 27.9 and 28.6), and no more than a launch holds.
   const int64_t rounds = std::max(std::min<int64_t>((sets + 2047) / 2048, 8), (sets + kMostBlocks - 1) / kMostBlocks);
   g.rounds = (uint32_t)rounds;
   const dim3 grid((unsigned)((sets + rounds - 1) / rounds)), block(kNormThreads);
@@ -536,13 +538,23 @@ __global__ void __launch_bounds__(kBackThreads) layer_norm_backward_kernel(NormB
   float2 stats;
   auto fetch = [&](unsigned at_row) {
     const bool have = at_row < rows;
+    // dy and x by turns, or one behind the other where both are fp32, whose pieces the compiler otherwise keeps in memory (8,192 x 8,192
+    // 155 us against 125; from an FP8 checkpoint by turns 96 against 107)
+    constexpr bool kTurns = !(X == kRowsFP32 && DY == kRowsFP32);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      xr[k].zero();
       yr[k].zero();
+      if constexpr (kTurns) xr[k].zero();
       if (have && count(k) > 0) {
         yr[k].load(a.dy, up.at + 8 * k * P, es, count(k), g.dy32);
-        xr[k].load(a, at_row, from.at + 8 * k * P, es, count(k), g.x32);
+        if constexpr (kTurns) xr[k].load(a, at_row, from.at + 8 * k * P, es, count(k), g.x32);
+      }
+    }
+    if constexpr (!kTurns) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        xr[k].zero();
+        if (have && count(k) > 0) xr[k].load(a, at_row, from.at + 8 * k * P, es, count(k), g.x32);
       }
     }
     stats = have ? a.stats[at_row] : make_float2(0.0f, 0.0f);
@@ -714,6 +726,8 @@ hipError_t backward_io(const NormBackArgs& a, const NormBackGrid& g, int k, int 
                          : backward_k<X, kRowsFP32, kRowsFP32>(a, g, k, s);
 }
 
+// Of equals the most threads: their sums of columns are fewer each, and a workgroup's waves more (8,192 x 2,048 on 256 x 1 and 128 x 2
+// threads 30.2 and 30.5 us, 16,384 x 1,024 on 128 x 1 and 64 x 2 26.3 and 26.8).
 RowShape back_shape(int d) { return row_shape(d, 9, 3, 9); }
 
 }  // namespace
@@ -724,6 +738,8 @@ int norm_backward_blocks(int64_t rows, int d) {
   // Few rows take one workgroup and one launch (through the binding, one against two: 64 x 128 8.5 and 10.8 us, 128 x 128 8.5 and
   // 10.8, but 512 x 128 12.2 and 11.0; 4 x 8,192 11.7 and 10.9).
   if (sets <= (d % 8 || d > 2048 ? 2 : 4)) return 1;
+  // As many as the chip holds at once: sixteen waves a CU with one piece a thread, else eight (131,072 x 128 on 256, 512 and 1,024
+  // workgroups 29.7, 24.9 and 29.1 us, 8,192 x 5,120 on 256 and 512 67.0 and 76.9).
   return (int)std::min<int64_t>(sets, shape.k == 1 ? 512 : 256);
 }
 

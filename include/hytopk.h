@@ -411,7 +411,7 @@ typedef struct {
  * elements:
  *   mean = sum x / d,  rstd = (sum (x - mean)^2 / d + eps)^(-1/2),
  *   y = (x - mean) rstd weight + bias
- * in fp32, rounded once to y's type.  The squares of a row's deviations must sum below 2^128; a
+ * in fp32, rounded once to y's type.  A row's values, and the squares of its deviations, must sum below 2^128; a
  * constant row gives bias, or NaN with eps = 0.  A row that is not finite gives NaN in its own
  * row alone.
  * stats (fp32 [n][heads][2], 8-byte aligned, or NULL): mean and rstd, for the backward.

@@ -25,6 +25,7 @@ def hk():
 
 
 def _room(gib):
+    torch.cuda.empty_cache()  # what earlier tests left with torch
     if torch.cuda.mem_get_info()[0] < gib << 30:
         pytest.skip(f"needs {gib} GiB of GPU memory")
 
