@@ -91,7 +91,7 @@ class Rotary:
     [dim/2] (radians a position) the frequencies, for a model with its own.
 
     ``sections`` (pairs of each axis, dim/2 in all) is for tokens with a position on
-    each of several axes, such as time, height and width; ``q_pos`` is then int32 [n][axes].  The axes'
+    each of several axes, such as time, height and width; ``q_pos`` is then int32 [n][axes] ([n] for one).  The axes'
     pairs lie one behind the other or, with ``cycle``, in turn: axis a > 0 takes pairs a, a + A, a + 2A, ... of A axes,
     as many as it has, and axis 0 the others.  ``restart`` begins the frequencies anew on each axis, as those of a
     rotation of its pairs alone."""

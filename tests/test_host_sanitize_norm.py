@@ -1,5 +1,5 @@
 """The argument validation of the layer norm and of rotary plans of several axes under AddressSanitizer and
-UndefinedBehaviorSanitizer, as test_host_sanitize_operators.py does it for the operators before them: none of the driver's calls
+UndefinedBehaviorSanitizer, as test_host_sanitize_operators.py does it for the operators before them: none of its calls
 gets as far as a HIP call."""
 import concurrent.futures as cf
 import glob
