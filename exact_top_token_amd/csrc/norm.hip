@@ -584,16 +584,19 @@ __global__ void __launch_bounds__(kBackThreads) layer_norm_backward_kernel(NormB
     fetch(row);
     float s[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int k = 0; k < K; ++k) {
+      // elements that do not exist were read as 0 and keep it: mean rstd alone may pass fp32
+      const float m = count(k) > 0 ? mean : 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        h[k][i] = (h[k][i] - mean) * rstd;
+        h[k][i] = (h[k][i] - (X == kAny && i >= count(k) ? 0.0f : m)) * rstd;
         dw[k][i] = fmaf(dy[k][i], h[k][i], dw[k][i]);
         db[k][i] += dy[k][i];
         dy[k][i] *= w[k][i];
         s[0] += dy[k][i];
         s[1] = fmaf(dy[k][i], h[k][i], s[1]);
       }
+    }
     if (!a.dx) continue;
     lanes_add(s, g.log_p);
     if (P > kWave) {
