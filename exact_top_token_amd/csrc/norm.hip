@@ -162,15 +162,15 @@ __device__ __forceinline__ void rows_add(float (&x)[8], int log_p) {
   }
 }
 
-// Joins what the waves of a row hold (P > 64 threads a row; `flip` alternates between two
-// halves, so that one barrier a step is enough: the other half is read by waves still in the last step).
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6); }
+
+// Joins what the waves of a row hold (P > 64 threads a row).  One barrier: steps take two arrays by turns, as waves still in
+// the last step read the other.  The forward takes its wave's number as a scalar, whose addresses take no registers of the loop.
 template <typename Join>
-__device__ __forceinline__ float2 join_waves(float2 (*red)[kBackThreads / kWave], int& flip, int P, float2 v, Join join) {
-  float2* part = red[flip];
-  flip ^= 1;
-  if (lane_id() == 0) part[threadIdx.x >> 6] = v;
+__device__ __forceinline__ float2 join_waves(float2* part, int wave, int P, float2 v, Join join) {
+  const int waves = P / kWave, w0 = wave & ~(waves - 1);
+  if (lane_id() == 0) part[wave] = v;
   __syncthreads();
-  const int waves = P / kWave, w0 = (threadIdx.x >> 6) & ~(waves - 1);
   v = part[w0];
   for (int w = 1; w < waves; ++w) v = join(v, part[w0 + w]);
   return v;
@@ -236,7 +236,9 @@ namespace {
 // y = (x - mean) / sqrt(var + eps) * weight + bias of each row.  A row is read once and stays in registers: a
 // first sum gives m0, the mean but for that sum's rounding; the sums of x - m0 and its square then give the rest of
 // the mean and the variance about m0, less that rest's square, so neither an offset of the row nor its sum's
-// rounding reaches the deviations.  SAVE: the row is also quantised as a cache row of its own, from the same read.
+// rounding reaches the deviations.  Where the row's first element is as near the mean as roundings leave m0, it is m0: the deviations
+// of a constant row are 0 then, whatever its size (of a row of 1e9 m0 is off by 64, whose square's rounding is far above eps; past
+// 1e25 the square itself passes fp32).  SAVE: the row is also quantised as a cache row of its own, from the same read.
 // Bound by memory: bf16 131,072 x 128 12.2 us (5.5 TB/s), 8,192 x 4,096 23.1 (5.8), 5,003 x 7,168 27.8 (5.2); with an FP8
 // checkpoint 18.2, 31.6 and 38.0 us (narrow rows by the instructions of the quotients, 4.6 TB/s), with MXFP8 15.8, 28.0 and 32.8.  The
 // next row's elements are under way while one is worked on; places along the rows are kept, not formed again
@@ -244,7 +246,8 @@ namespace {
 template <int IN, int OUT, int SAVE, int K, bool PAST>
 __global__ void __launch_bounds__(kNormThreads) layer_norm_kernel(NormArgs a, NormGrid g) {
 #pragma clang fp contract(off)  // every path (alignment, types, checkpoint) gives the same bits
-  __shared__ float2 red[2][kBackThreads / kWave];
+  __shared__ float2 red[2][kNormThreads / kWave];
+  __shared__ float heads[kNormThreads / kWave];  // rows of several waves: their first elements
   const int d = g.d, P = 1 << g.log_p, RB = kNormThreads >> g.log_p;
   const int lr = threadIdx.x & (P - 1), rl = threadIdx.x >> g.log_p;
   const float inv_d = 1.0f / (float)d;
@@ -277,7 +280,6 @@ __global__ void __launch_bounds__(kNormThreads) layer_norm_kernel(NormArgs a, No
       pb[k].floats(a.bias, g.fp32, 0.0f, b[k]);
     }
   }
-  int flip = 0;
   // `left` rows of this round's first row on, the same in the whole workgroup
   int left = (int)(rows - (row - rl));
   for (int r = 0; r < (int)g.rounds && left > 0; ++r, left -= RB) {
@@ -302,13 +304,27 @@ __global__ void __launch_bounds__(kNormThreads) layer_norm_kernel(NormArgs a, No
     }
     lanes_add(sum, g.log_p);
     if constexpr (SAVE == kFP8) top = lanes_max(top, P);
+    float first;
     if (P > kWave) {
-      const float2 s = join_waves(red, flip, P, make_float2(sum[0], top),
-                                  [](float2 x, float2 y) { return make_float2(x.x + y.x, fmaxf(x.y, y.y)); });
-      sum[0] = s.x;
-      top = s.y;
+      if constexpr (SAVE == kFP8) {
+        if (lane_id() == 0) heads[wave_id()] = v[0][0];
+        const float2 s = join_waves(red[0], wave_id(), P, make_float2(sum[0], top),
+                                    [](float2 x, float2 y) { return make_float2(x.x + y.x, fmaxf(x.y, y.y)); });
+        sum[0] = s.x;
+        top = s.y;
+        first = heads[wave_id() & -(P / kWave)];
+      } else {
+        const float2 s = join_waves(red[0], wave_id(), P, make_float2(sum[0], v[0][0]),
+                                    [](float2 x, float2 y) { return make_float2(x.x + y.x, x.y); });
+        sum[0] = s.x;
+        first = s.y;
+      }
+    } else {
+      first = __shfl(v[0][0], lane_id() & -P);
     }
-    const float m0 = sum[0] * inv_d;
+    float m0 = sum[0] * inv_d;
+    // 17 roundings at most lie between a constant row's m0 and its value
+    if (fabsf(first - m0) < fabsf(m0) * 0x1p-19f) m0 = first;
     const int64_t code0 = (int64_t)now * d + 8 * lr;
     if constexpr (SAVE == kFP8) {
       const Reciprocal by(e4m3_scale(top));
@@ -347,7 +363,7 @@ __global__ void __launch_bounds__(kNormThreads) layer_norm_kernel(NormArgs a, No
     }
     lanes_add(s, g.log_p);
     if (P > kWave) {
-      const float2 j = join_waves(red, flip, P, make_float2(s[0], s[1]),
+      const float2 j = join_waves(red[1], wave_id(), P, make_float2(s[0], s[1]),
                                   [](float2 x, float2 y) { return make_float2(x.x + y.x, x.y + y.y); });
       s[0] = j.x;
       s[1] = j.y;
@@ -600,8 +616,9 @@ __global__ void __launch_bounds__(kBackThreads) layer_norm_backward_kernel(NormB
     if (!a.dx) continue;
     lanes_add(s, g.log_p);
     if (P > kWave) {
-      const float2 j = join_waves(red, flip, P, make_float2(s[0], s[1]),
+      const float2 j = join_waves(red[flip], threadIdx.x >> 6, P, make_float2(s[0], s[1]),
                                   [](float2 x, float2 y) { return make_float2(x.x + y.x, x.y + y.y); });
+      flip ^= 1;
       s[0] = j.x;
       s[1] = j.y;
     }

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from gpu_util import say
-from test_gpu_layer_norm import check_backward
+from test_gpu_layer_norm import check_backward, check_forward
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +66,73 @@ def test_the_gradient_of_constant_rows_from_a_checkpoint(hk, d, fmt):
         got = hk.layer_norm_backward(g, hk.NormSaved(codes, scale, stats, fmt), w, dx_dtype=FP32)
         check_backward(got, g, f64(x), stats, w, coded=True)
         assert not got["dweight"].any()
+
+
+# ----------------------------------------------------------------- forward
+
+def _constants(d, seed):
+    """Rows of one value each, of sizes from 1e-3 to 2^127 / d, among rows of their own values."""
+    rng = np.random.default_rng(seed)
+    size = np.array([1e-3, 1.0, 1e3, 1e6, 1e9, 1e15, 1e25, 0.5 * 2.0 ** 127 / d])
+    c = (np.repeat(size, 12) * rng.uniform(1, 2, 96) * rng.choice([-1, 1], 96)).astype(np.float32)
+    x = torch.from_numpy(c)[:, None].expand(96, d).clone()
+    x[::4] = torch.from_numpy(rng.standard_normal((24, d)).astype(np.float32))
+    flat = torch.ones(96, dtype=torch.bool)
+    flat[::4] = d == 1
+    return x, flat
+
+
+# 41, 55, 107 and 3,993: d times the rounded 1 / d is not 1 after rounding
+@pytest.mark.parametrize("d", [1, 3, 24, 41, 55, 64, 96, 107, 128, 160, 201, 576, 1000, 1536, 2056, 3993, 5120, 7168, 8191, 8192])
+def test_constant_rows_of_any_size_give_the_bias(hk, d):
+    """Deviations are 0 exactly: y is the bias, the mean the value, rstd eps^(-1/2) (the instruction's 2^-23, a rounding of eps), and
+    NaN without eps.  The rows of normal numbers between them are the definition's."""
+    say(f"norm: constant rows, d={d}")
+    w, b = _rand(d, 5, FP32, 0.2, 1.0), _rand(d, 6)
+    for dtype in (FP32, BF16):
+        x, flat = _constants(d, d)
+        x = x.to(dtype).cuda()
+        saves = ["x"] + (["fp8", "mxfp8"] if d % 32 == 0 else [])
+        for rows in (x, _off_16_bytes(x), x.view(32, 3, d)):
+            for save in saves:
+                for eps in (1e-5, 1e-12):
+                    y, saved = hk.layer_norm(rows, w, b, eps=eps, out_dtype=FP32, save=save)
+                    y, st = y.reshape(96, d), saved.stats.reshape(96, 2)
+                    assert torch.equal(y[flat], b.expand(int(flat.sum()), d))
+                    assert torch.equal(st[flat, 0], x[flat, 0].float())
+                    assert float((st[flat, 1].double() * eps ** 0.5 - 1).abs().max()) <= 2.0 ** -22
+                    if d > 1:
+                        check_forward(y[~flat], st[~flat], x[~flat], w, b, eps)
+        y = hk.layer_norm(x, w, b, eps=0.0, out_dtype=FP32)
+        assert torch.isnan(y[flat]).all() and torch.isfinite(y[~flat]).all()
+        # both passes together
+        y, saved = hk.layer_norm(x, w, b, eps=1e-6, save="x")
+        dy = _rand((96, d), 7, FP32, d ** -0.5)
+        got = hk.layer_norm_backward(dy, saved, w)
+        check_backward(got, dy, f64(x), saved.stats, w)
+        assert torch.isfinite(got["dx"]).all() and torch.isfinite(got["dweight"]).all()
+
+
+@pytest.mark.parametrize("d", [96, 128, 1100, 5120])
+def test_rows_far_from_zero(hk, d):
+    """Rows of deviations of size 1 about 2^10 .. 2^22, their first element among the others, far from them, or next to the mean.  A shift m0
+    within 2^-18 of the mean (2^-19 of itself from a value, 17 roundings) leaves the mean of the deviations below 2^-18 |mean|, whose
+    square is taken from that of the deviations: rstd is off by 28 u of 1 + 2 (2^-18 mean)^2 / var, of var here about 1."""
+    say(f"norm: rows far from zero, d={d}")
+    base = _rand((39, d), 8)
+    base[0::3, 0] = 30.0
+    base[1::3, 0] = 0.0
+    off = 2.0 ** torch.arange(10, 23).repeat_interleave(3).double().cuda()
+    x = (base.double() + off[:, None]).float()
+    x64 = f64(x)
+    y, saved = hk.layer_norm(x, eps=1e-6, save="x")
+    mean, var = x64.mean(1, keepdims=True), x64.var(1, keepdims=True)
+    rstd = (var + 1e-6) ** -0.5
+    ratio = 1 + 2 * (2.0 ** -18 * mean) ** 2 / var
+    st = f64(saved.stats)
+    assert (np.abs(st[:, 1:] / rstd - 1) <= 32 * U * ratio).all()
+    assert (np.abs(st[:, :1] - mean) <= U * np.abs(mean) + 56 * U * (2.0 ** -18 * mean + var ** 0.5)).all()
+    # a deviation is off by 2 u of itself and of the shift, the deviations' mean by 50 u of theirs, y by rstd's error and three roundings
+    c = np.abs(x64 - mean)
+    tol = rstd * (2 * U * (c + 2.0 ** -18 * mean) + 52 * U * (c.mean(1, keepdims=True) + 2.0 ** -18 * mean)) + c * rstd * U * (32 * ratio + 3)
+    assert (np.abs(f64(y) - (x64 - mean) * rstd) <= tol).all()
