@@ -598,21 +598,27 @@ __global__ void __launch_bounds__(kBackThreads) layer_norm_backward_kernel(NormB
     from.next(row, xheads, xts, xhs, e0);
     up.next(row, a.heads, a.dyts, a.dyhs, e0);
     fetch(row);
+    // Elements that do not exist were read as 0, of x and of dy: their h has to be finite, no more.  Where mean rstd is not they
+    // are given the mean (8,000 x 4,099 in bf16 73.2 us; 74.8 with these elements left out of every row).
+    if (__any(!(fabsf(mean) * rstd <= 0x1.fffffep127f))) {
+      int here = last;
+      asm volatile("" : "+v"(here));  // compared here and not before the loop, where the results would take registers
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i >= here) h[K - 1][i] = mean;
+    }
     float s[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      // elements that do not exist were read as 0 and keep it: mean rstd alone may pass fp32
-      const float m = count(k) > 0 ? mean : 0.0f;
+    for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        h[k][i] = (h[k][i] - (X == kAny && i >= count(k) ? 0.0f : m)) * rstd;
+        h[k][i] = (h[k][i] - mean) * rstd;
         dw[k][i] = fmaf(dy[k][i], h[k][i], dw[k][i]);
         db[k][i] += dy[k][i];
         dy[k][i] *= w[k][i];
         s[0] += dy[k][i];
         s[1] = fmaf(dy[k][i], h[k][i], s[1]);
       }
-    }
     if (!a.dx) continue;
     lanes_add(s, g.log_p);
     if (P > kWave) {
