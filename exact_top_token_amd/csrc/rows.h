@@ -174,11 +174,12 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 
 // The scale of an FP8 row whose largest magnitude is m: max(m / 448, 2^-126), 1 for a row of zeros.  The quotient is rounded
 // as a division's: a product with the rounded 1 / 448 and one correction by the exact remainder (all 2^23
-// significands compared with the division's).
+// significands compared with the division's).  An infinite m has no remainder, and its scale is infinite, so that the whole row reads as
+// NaN: it comes from the product less 2^-20 of it, which is below every other quotient.
 __device__ __forceinline__ float e4m3_scale(float m) {
   constexpr float kInv = 1.0f / 448.0f;
   const float q = m * kInv;
-  return m > 0.0f ? fmaxf(fmaf(fmaf(-448.0f, q, m), kInv, q), 0x1p-126f) : 1.0f;
+  return m > 0.0f ? fmaxf(fmaxf(fmaf(fmaf(-448.0f, q, m), kInv, q), 0x1p-126f), m * (kInv * (1.0f - 0x1p-20f))) : 1.0f;
 }
 
 // The E4M3 bytes of four exact quotients x / scale.  `below` and `above` are 1 / scale less and plus 2^-21 of it, so x
