@@ -115,11 +115,11 @@ __device__ __forceinline__ void rot_table(const RotArgs& r, int64_t t0, int nt, 
       continue;
     }
     // the pair's axis; one that does not exist is taken as the last, so that no position outside the array is read
-    const int* at = r.pos + t0 * r.axes;
+    const int axes = r.pos ? r.axes : 0;
     unsigned axis = 0;
-    if (r.pos && r.axes > 1) axis = min((unsigned)reinterpret_cast<const int*>(r.freq + half)[i], (unsigned)r.axes - 1u);
+    if (axes > 1) axis = min((unsigned)reinterpret_cast<const int*>(r.freq + half)[i], (unsigned)axes - 1u);
     for (int t = first; t < nt; t += steps) {
-      const int pos = r.pos ? at[__umul24(t, r.axes) + axis] : r.pos0 + (int)t0 + t;  // below 2^31
+      const int pos = r.pos ? (r.pos + t0 * axes)[__umul24(t, axes) + axis] : r.pos0 + (int)t0 + t;  // below 2^31
       to[t * half] = rot_entry(r, f, pos);
     }
   }
