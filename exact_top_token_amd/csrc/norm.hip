@@ -166,8 +166,8 @@ __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane
 
 // Joins what the waves of a row hold (P > 64 threads a row).  One barrier: steps take two arrays by turns, as waves still in
 // the last step read the other.  The forward takes its wave's number as a scalar, whose addresses take no registers of the loop.
-template <typename Join>
-__device__ __forceinline__ float2 join_waves(float2* part, int wave, int P, float2 v, Join join) {
+template <typename V, typename Join>
+__device__ __forceinline__ V join_waves(V* part, int wave, int P, V v, Join join) {
   const int waves = P / kWave, w0 = wave & ~(waves - 1);
   if (lane_id() == 0) part[wave] = v;
   __syncthreads();
@@ -247,7 +247,7 @@ template <int IN, int OUT, int SAVE, int K, bool PAST>
 __global__ void __launch_bounds__(kNormThreads) layer_norm_kernel(NormArgs a, NormGrid g) {
 #pragma clang fp contract(off)  // every path (alignment, types, checkpoint) gives the same bits
   __shared__ float2 red[2][kNormThreads / kWave];
-  __shared__ float heads[kNormThreads / kWave];  // rows of several waves: their first elements
+  __shared__ float4 red4[kNormThreads / kWave];
   const int d = g.d, P = 1 << g.log_p, RB = kNormThreads >> g.log_p;
   const int lr = threadIdx.x & (P - 1), rl = threadIdx.x >> g.log_p;
   const float inv_d = 1.0f / (float)d;
@@ -307,12 +307,11 @@ __global__ void __launch_bounds__(kNormThreads) layer_norm_kernel(NormArgs a, No
     float first;
     if (P > kWave) {
       if constexpr (SAVE == kFP8) {
-        if (lane_id() == 0) heads[wave_id()] = v[0][0];
-        const float2 s = join_waves(red[0], wave_id(), P, make_float2(sum[0], top),
-                                    [](float2 x, float2 y) { return make_float2(x.x + y.x, fmaxf(x.y, y.y)); });
+        const float4 s = join_waves(red4, wave_id(), P, make_float4(sum[0], v[0][0], top, 0.0f),
+                                    [](float4 x, float4 y) { return make_float4(x.x + y.x, x.y, fmaxf(x.z, y.z), 0.0f); });
         sum[0] = s.x;
-        top = s.y;
-        first = heads[wave_id() & -(P / kWave)];
+        first = s.y;
+        top = s.z;
       } else {
         const float2 s = join_waves(red[0], wave_id(), P, make_float2(sum[0], v[0][0]),
                                     [](float2 x, float2 y) { return make_float2(x.x + y.x, x.y); });
