@@ -48,6 +48,8 @@
  *   * `stream` is a hipStream_t (NULL = the legacy default stream).  Every
  *     call is ordered on it.  hytopk_select synchronises that stream once (to
  *     read the failure count); replay and baseline are fully asynchronous.
+ *   * Struct fields named `reserved` are set to 0: they are not read now, and a
+ *     later version may give them a meaning (hytopk_rotary_plan's axes was one).
  *   * Ownership: the caller allocates every buffer, including the workspace.
  *     The library allocates no device memory.
  *   * Errors: arguments are validated before any launch, so a negative return
@@ -330,7 +332,8 @@ typedef struct {
   int32_t dim;         /* rotated elements of a head, even, first + dim <= d */
   int32_t first;
   int32_t layout;      /* hytopk_rotary_layout */
-  int32_t axes;        /* 0 or 1: one position a token; up to 16 */
+  int32_t axes;        /* 0 or 1: one position a token; up to 16.  Always read: it was a `reserved` that nothing
+                          read, so a caller that left it unset then has to set it now */
 } hytopk_rotary_plan;
 
 /* The frequencies and gain of a plan, computed on the host in 64 bits:
@@ -411,8 +414,9 @@ typedef struct {
  * elements:
  *   mean = sum x / d,  rstd = (sum (x - mean)^2 / d + eps)^(-1/2),
  *   y = (x - mean) rstd weight + bias
- * in fp32, rounded once to y's type.  A row's values, and the squares of its deviations, must sum below 2^128; a
- * constant row gives bias, or NaN with eps = 0.  A row that is not finite gives NaN in its own
+ * in fp32, rounded once to y's type.  A row's values, and the squares of their differences from any one of them, must
+ * sum below 2^128.  With eps below 2^-100, deviations below 2^-62 lose digits (their squares are subnormal), below 2^-75 all
+ * of them.  A constant row of any size gives bias, or NaN with eps = 0.  A row that is not finite gives NaN in its own
  * row alone.
  * stats (fp32 [n][heads][2], 8-byte aligned, or NULL): mean and rstd, for the backward.
  * save (or NULL): a checkpoint of x in 8 bits for the backward, taken from the same read: cache rows
@@ -433,7 +437,8 @@ size_t hytopk_layer_norm_backward_workspace(int64_t n, int32_t heads, int32_t d)
  *   dx = rstd (g - mean(g) - h mean(g h))   (means over the row)
  *   dweight [d] = sum over rows of dy h,   dbias [d] = sum over rows of dy   (fp32)
  * x is the forward's input (`x`, `saved` NULL) or its checkpoint (`saved`, `x` NULL), whose decoded rows
- * then stand for x in h; mean and rstd are those of x itself.  Sums are fp32 in
+ * then stand for x in h; mean and rstd are those of x itself.  mean is fp32, so h of a row far from zero is off by up to
+ * 2^-24 |mean| rstd from the norm's own, and dx and dweight with it (y is not: its mean is not rounded).  Sums are fp32 in
  * an order that depends on the sizes alone: results are bitwise reproducible.  dx, dweight and dbias may be
  * NULL to skip them; dweight and dbias are fully written, the workspace (256-byte aligned) is for
  * either.  norm gives the weight (its bias and eps are not read).  dx may be dy or x itself; otherwise

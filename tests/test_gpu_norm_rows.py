@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from gpu_util import say
+from oracle import operators as op
 from test_gpu_layer_norm import check_backward, check_forward
 
 pytestmark = pytest.mark.gpu
@@ -136,3 +137,30 @@ def test_rows_far_from_zero(hk, d):
     c = np.abs(x64 - mean)
     tol = rstd * (2 * U * (c + 2.0 ** -18 * mean) + 52 * U * (c.mean(1, keepdims=True) + 2.0 ** -18 * mean)) + c * rstd * U * (32 * ratio + 3)
     assert (np.abs(f64(y) - (x64 - mean) * rstd) <= tol).all()
+
+
+# ------------------------------------------- the gradient far from zero
+
+@pytest.mark.parametrize("d", [96, 128, 1100, 5120])
+@pytest.mark.parametrize("offset", [0.0, 2.0 ** 10, 2.0 ** 15, 2.0 ** 18])
+def test_the_gradient_of_rows_far_from_zero(hk, d, offset):
+    """Against the derivative with the mean and deviation of x in 64 bits.  The mean is kept in fp32, off by u |mean| (and 52 u of the
+    deviations' mean size), so h is off by that times rstd; rstd, off by 32 u, is in h and in dx."""
+    say(f"norm: the gradient far from zero, d={d}, {offset}")
+    x, w, dy = _rand((64, d), 9, FP32, offset=offset), _rand(d, 10, FP32, 0.2, 1.0), _rand((64, d), 11, FP32, d ** -0.5)
+    _, saved = hk.layer_norm(x, w, eps=1e-6, save="x")
+    got = hk.layer_norm_backward(dy, saved, w)
+    x64, dy64, w64 = f64(x), f64(dy), f64(w)
+    mean, rstd = x64.mean(1), (x64.var(1) + 1e-6) ** -0.5
+    dx, dw, db = op.layer_norm_backward(dy64, x64, mean, rstd, w64)
+    r, a = rstd[:, None], np.abs(dy64)
+    dev = np.abs(x64 - mean[:, None])
+    h, g = dev * r, a * np.abs(w64)
+    eh = r * (1.001 * U * np.abs(mean)[:, None] + 52 * U * dev.mean(1, keepdims=True)) + 34 * U * h
+    row = lambda t: t.mean(1, keepdims=True)  # noqa: E731
+    size = g + row(g) + h * row(g * h)
+    tol = r * (eh * row(g * h) + (h + eh) * row(g * eh) + (32 + 60) * U * size)
+    assert (np.abs(f64(got["dx"]) - dx) <= tol).all()
+    chain = 155 + 64 / 256
+    assert (np.abs(f64(got["dweight"]) - dw) <= U * chain * (a * h).sum(0) + (a * eh).sum(0)).all()
+    assert (np.abs(f64(got["dbias"]) - db) <= U * chain * a.sum(0)).all()
