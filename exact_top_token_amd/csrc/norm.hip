@@ -239,10 +239,10 @@ namespace {
 // rounding reaches the deviations.  Where the row's first element is as near the mean as roundings leave m0, it is m0: the deviations
 // of a constant row are 0 then, whatever its size (of a row of 1e9 m0 is off by 64, whose square's rounding is far above eps; past
 // 1e25 the square itself passes fp32).  SAVE: the row is also quantised as a cache row of its own, from the same read.
-// Bound by memory: bf16 131,072 x 128 12.2 us (5.5 TB/s), 8,192 x 4,096 23.1 (5.8), 5,003 x 7,168 27.8 (5.2); with an FP8
-// checkpoint 18.2, 31.6 and 38.0 us (narrow rows by the instructions of the quotients, 4.6 TB/s), with MXFP8 15.8, 28.0 and 32.8.  The
+// Bound by memory: bf16 131,072 x 128 11.5 us (5.8 TB/s), 8,192 x 4,096 23.3 (5.8), 5,003 x 7,168 27.8 (5.2); with an FP8
+// checkpoint 18.1, 32.1 and 39.3 us (narrow rows by the instructions of the quotients, 4.6 TB/s), with MXFP8 14.2, 29.2 and 32.7.  The
 // next row's elements are under way while one is worked on; places along the rows are kept, not formed again
-// (131,072 x 128 14.6 us with 64-bit products a row).
+// (131,072 x 128 14.6 us with 64-bit products a row, against 12.2 of the kernel as it was then).
 template <int IN, int OUT, int SAVE, int K, bool PAST>
 __global__ void __launch_bounds__(kNormThreads) layer_norm_kernel(NormArgs a, NormGrid g) {
 #pragma clang fp contract(off)  // every path (alignment, types, checkpoint) gives the same bits
@@ -402,15 +402,15 @@ RowShape row_shape(int d, int most_log_p, int most_k, int best_log_p) {
   return best;
 }
 
-// Results larger than the chip's L2 caches (32 MiB) go past them: the forward of 8,192 x 4,096 23.0 us against 28.8, the
-// backward of 131,072 x 128 21.9 against 25.5.  Rows off 16 bytes do not.
+// Results larger than the chip's L2 caches (32 MiB) go past them: the forward of 8,192 x 4,096 23.8 us against 28.8, the
+// backward of 131,072 x 128 21.3 against 25.2.  Rows off 16 bytes do not.
 bool past_caches(int64_t rows, int d, int dtype) { return rows * d * rows_bytes(dtype) >= int64_t(32) << 20; }
 
 template <int IN, int OUT, int SAVE, bool PAST>
 hipError_t layer_norm_past(const NormArgs& a, NormGrid g, int k, hipStream_t s) {
   const int64_t rb = kNormThreads >> g.log_p, sets = (a.rows + rb - 1) / rb;
-  // About 2,048 workgroups, of at most eight rounds (131,072 x 128 by 1,024, 2,048 and 4,096 of them 12.4, 11.8 and 12.3 us, 5,003 x 7,168
-  // 28.4, 27.9 and 28.6), and no more than a launch holds.
+  // About 2,048 workgroups, of at most eight rounds (131,072 x 128 by 1,024, 2,048 and 4,096 of them 12.2, 11.5 and 11.9 us, 5,003 x 7,168
+  // 28.9, 28.2 and 28.6), and no more than a launch holds.
   const int64_t rounds = std::max(std::min<int64_t>((sets + 2047) / 2048, 8), (sets + kMostBlocks - 1) / kMostBlocks);
   g.rounds = (uint32_t)rounds;
   const dim3 grid((unsigned)((sets + rounds - 1) / rounds)), block(kNormThreads);
@@ -453,8 +453,8 @@ hipError_t launch_layer_norm(const NormArgs& args, int d, bool weight32, int in_
     a.xts = a.xhs;
     a.yts = a.yhs;
   }
-  // of equals two pieces a thread for rows of several waves (with one and two 13.2 and 12.2 us of 8,192 x 2,048, with four and
-  // two 25.2 and 23.0 of 8,192 x 4,096)
+  // of equals two pieces a thread for rows of several waves (with one and two 20.8 and 19.1 us of 8,192 x 2,048 with an FP8 checkpoint,
+  // 20.0 and 17.6 of 16,384 x 1,024; without one 12.4 and 12.9, 12.7 and 12.6; with four and two 25.6 and 23.7 of 8,192 x 4,096)
   const RowShape shape = row_shape(d, 8, 4, d > 2048 ? 8 : d > 1024 ? 7 : 6);
   NormGrid g{};
   g.d = (uint32_t)d;
@@ -521,8 +521,8 @@ struct XPiece<kCodesMXFP8> : CodePiece<kMXFP8> {};
 // forward's, so both of a row's sums are formed at once; each row is read once and stays in registers, and a thread keeps the sums
 // of its columns over all its rows: as few workgroups as fill the chip (512 with one piece a thread, else 256, of 512
 // threads) keep what is written of them small (1,024 workgroups of 256 threads: 8,192 x 5,120 87 us against 62 then).
-// Bound by memory: bf16 131,072 x 128 22.6 us with the sums, 16.4 without (6.2 TB/s), 8,192 x 5,120 52 (4.8 TB/s); from an FP8
-// checkpoint with fp32 gradients 23.6 against 27.9 from bf16 rows.
+// Bound by memory: bf16 131,072 x 128 21.3 us with the sums, 16.1 without (6.2 TB/s), 8,192 x 5,120 52 (4.8 TB/s); from an FP8
+// checkpoint with fp32 gradients 23.5 against 27.5 from bf16 rows.
 template <int X, int DY, int DX, int K, bool PAST>
 __global__ void __launch_bounds__(kBackThreads) layer_norm_backward_kernel(NormBackArgs a, NormBackGrid g) {
 #pragma clang fp contract(off)  // as forward
@@ -553,8 +553,8 @@ __global__ void __launch_bounds__(kBackThreads) layer_norm_backward_kernel(NormB
   float2 stats;
   auto fetch = [&](unsigned at_row) {
     const bool have = at_row < rows;
-    // dy and x by turns, or one behind the other where both are fp32, whose pieces the compiler otherwise keeps in memory (8,192 x 8,192
-    // 155 us against 125; from an FP8 checkpoint by turns 96 against 107)
+    // dy and x by turns, or one behind the other where both are fp32 (8,192 x 5,120 to bf16 80.5 us against 82.6 by turns; from an
+    // FP8 checkpoint 8,192 x 8,192 by turns 97.7 against 107)
     constexpr bool kTurns = !(X == kRowsFP32 && DY == kRowsFP32);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -751,8 +751,8 @@ hipError_t backward_io(const NormBackArgs& a, const NormBackGrid& g, int k, int 
                          : backward_k<X, kRowsFP32, kRowsFP32>(a, g, k, s);
 }
 
-// Of equals the most threads: their sums of columns are fewer each, and a workgroup's waves more (8,192 x 2,048 on 256 x 1 and 128 x 2
-// threads 30.2 and 30.5 us, 16,384 x 1,024 on 128 x 1 and 64 x 2 26.3 and 26.8).
+// Of equals the most threads, whose sums of columns are fewer each (little lies between them: 8,192 x 2,048 on 256 x 1 and 128 x 2
+// threads 23.1 and 22.2 us, 16,384 x 1,024 on 128 x 1 and 64 x 2 21.9 and 21.8).
 RowShape back_shape(int d) { return row_shape(d, 9, 3, 9); }
 
 }  // namespace
@@ -760,11 +760,12 @@ RowShape back_shape(int d) { return row_shape(d, 9, 3, 9); }
 int norm_backward_blocks(int64_t rows, int d) {
   const RowShape shape = back_shape(d);
   const int64_t rb = kBackThreads >> shape.log_p, sets = (rows + rb - 1) / rb;
-  // Few rows take one workgroup and one launch (through the binding, one against two: 64 x 128 8.5 and 10.8 us, 128 x 128 8.5 and
-  // 10.8, but 512 x 128 12.2 and 11.0; 4 x 8,192 11.7 and 10.9).
+  // Few rows take one workgroup and one launch (through the binding, one against two: 128 x 128 10.0 and 12.7 us, 384 x 128 10.6 and
+  // 12.6, 512 x 128 12.9 and 12.6; 32 x 201 9.9 and 12.7, 64 x 201 10.0 and 12.7, 96 x 201 12.7 both; 8 x 2,048 10.0 and 12.8, 16 x 2,048
+  // 10.7 and 12.8; 2 x 8,192 10.0 and 12.9, 4 x 8,192 12.0 and 12.8).  The limits lie at a quarter to a half of where two become as fast.
   if (sets <= (d % 8 || d > 2048 ? 2 : 4)) return 1;
-  // As many as the chip holds at once: sixteen waves a CU with one piece a thread, else eight (131,072 x 128 on 256, 512 and 1,024
-  // workgroups 29.7, 24.9 and 29.1 us, 8,192 x 5,120 on 256 and 512 67.0 and 76.9).
+  // As many as the chip holds at once: sixteen waves a CU with one piece a thread, else eight (131,072 x 128 on 256, 512 and 1,020
+  // workgroups 22.3, 21.5 and 23.7 us, 8,192 x 5,120 on 256 and 512 52.0 and 58.3).
   return (int)std::min<int64_t>(sets, shape.k == 1 ? 512 : 256);
 }
 
